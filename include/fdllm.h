@@ -74,12 +74,14 @@ typedef enum {
 
 typedef enum {
   FDLLM_DTYPE_F32 = 0,     /* float32 weights and activations, CUDA cores */
-  FDLLM_DTYPE_BF16 = 1     /* bfloat16 weights, run on tensor cores: the GEMM weights
+  FDLLM_DTYPE_BF16 = 1,    /* bfloat16 weights, run on tensor cores: the GEMM weights
                               are held as fp16 on the device (exact for every bf16
                               value of magnitude in [2^-17, 65504]); activations, q,
                               the K/V cache and the softmax weights stored as two fp16
                               terms (hi + lo, ~22 significant bits); float32
                               accumulation and residual stream */
+  FDLLM_DTYPE_F16 = 2      /* float16: operands of fdllm_kv8_* and fdllm_sample only, not a
+                              model dtype (fdllm_create refuses it) */
 } fdllm_dtype;
 
 /* Model shape and numerics.  Requirements (FDLLM_ERR_ARG otherwise):
@@ -379,6 +381,193 @@ FDLLM_API int fdllm_attention(fdllm_ctx* ctx, const void* q_dev, void* o_dev, in
  * too many splits, beyond the maximum, not an sm_100 GPU), CUDA, TIMEOUT. */
 FDLLM_API int fdllm_gemm_noalloc(const void* w_dev, const void* x_dev, float* y_dev, int N, int M,
                                  int K, int splits, void* cuda_stream);
+
+/* ------------------------------------------------------------------------
+ * 8-bit paged K/V cache and token sampling: operators for a caller's own
+ * decode loop (the decoder above keeps its own two-term fp16 cache).
+ *
+ * Conventions of the fdllm_kv8_* calls and fdllm_sample, where they differ
+ * from the calls above:
+ *   - They need no ctx, run on the current CUDA device and only ENQUEUE work
+ *     on cuda_stream (NULL = the legacy default stream): they return without
+ *     waiting, allocate nothing, keep nothing between calls and can be
+ *     captured into a CUDA graph.  Everything they read must be written, and
+ *     everything they write must stay allocated, in stream order.
+ *   - Every pointer inside the structs is a device pointer; the structs
+ *     themselves are host memory, read only during the call.
+ *   - Calls on different streams or devices, or from several host threads,
+ *     are independent as long as their outputs and workspaces are distinct.
+ *   - Argument errors return FDLLM_ERR_ARG before anything is launched, a
+ *     failed launch FDLLM_ERR_CUDA; the message is fdllm_last_error(NULL) of
+ *     the calling thread.  What only the device can see (a page id outside
+ *     the pool, a length beyond the page table) is checked there: the access
+ *     is skipped and a FDLLM_KV8_BAD_* bit is or-ed into *status, when
+ *     status is not NULL.  No call clears *status.
+ * ------------------------------------------------------------------------ */
+#define FDLLM_KV8_PAGE 64   /* positions per page */
+#define FDLLM_KV8_BLOCK 16  /* positions that share a scale (per K/V head) */
+#define FDLLM_KV8_BAD_PAGE 1   /* a page id outside [0, n_pages) where one was needed */
+#define FDLLM_KV8_BAD_RANGE 2  /* starts, lens, pos or the rotation table out of range */
+
+/* One layer's 8-bit K/V cache: key and value = code * scale, code an int8 in
+ * [-127, 127], one float scale >= 0 for each block of 16 positions and K/V
+ * head.  Codes of page p, head g, position t (0..63), dim d lie at
+ * [p * page_stride + (g * 64 + t) * head_dim + d], the scale of its block
+ * t / 16 at [p * scale_stride + g * 4 + t / 16] (K and V alike).  Sequence
+ * i's positions [64 j, 64 j + 64) are in page page_table[i * table_stride +
+ * j], j < max_pages; entries of pages that a call does not need are not
+ * read.  Requirements: head_dim 32, 64 or 128; k, v 16-byte aligned;
+ * page_stride >= n_kv_heads * 64 * head_dim and a multiple of 16 (0 = that
+ * product); scale_stride >= n_kv_heads * 4 (0 = that); table_stride >=
+ * max_pages (0 = max_pages); max_pages <= 2^24; n_seqs and n_kv_heads in
+ * [1, 65535]. */
+typedef struct {
+  int8_t* k;
+  int8_t* v;
+  float* k_scale;
+  float* v_scale;
+  const int32_t* page_table;
+  int64_t page_stride;    /* codes (bytes) from page to page */
+  int64_t scale_stride;   /* floats from page to page */
+  int64_t table_stride;   /* entries from sequence to sequence */
+  int32_t n_pages;
+  int32_t n_seqs;
+  int32_t max_pages;
+  int32_t n_kv_heads;
+  int32_t head_dim;
+} fdllm_kv8;
+
+/* Operands of fdllm_kv8_append.  Row r of k and v holds n_kv_heads vectors
+ * of head_dim contiguous elements, head g at [r * strides[0] + g *
+ * strides[1]] (strides in elements; rows and heads start on 16-byte
+ * boundaries); q likewise with n_heads. */
+typedef struct {
+  int32_t dtype;           /* fdllm_dtype of k, v, q and of the three outputs */
+  int32_t n_tokens;        /* rows of k, v and q */
+  int32_t n_heads;         /* heads of q; unused when q is NULL */
+  int32_t max_new;         /* launch hint: largest number of rows of one sequence
+                              (0 = n_tokens); a wrong hint only costs time */
+  const void* k;
+  const void* v;
+  const void* q;           /* optional */
+  int64_t k_strides[2];
+  int64_t v_strides[2];
+  int64_t q_strides[2];
+  const int32_t* starts;   /* [n_seqs + 1]: sequence i's rows are [starts[i], starts[i + 1]) */
+  const int32_t* lens;     /* [n_seqs]: positions of sequence i that hold tokens before the call */
+  const int32_t* pos;      /* optional [n_seqs]: position of sequence i's first row (NULL: lens,
+                              an append; a decoder that rewrites its block passes the block start) */
+  const float* rope;       /* optional [rope_len][head_dim / 2][2]: (cos, sin) of every position
+                              and pair (d, d + head_dim / 2); NULL: no rotation */
+  int32_t rope_len;
+  int32_t reserved;        /* 0 */
+  void* k_out;             /* optional dense [n_tokens, n_kv_heads, head_dim]: the new rows as the
+                              cache now stands for them (code * scale) */
+  void* v_out;             /* optional, likewise */
+  void* q_out;             /* the rotated q, dense [n_tokens, n_heads, head_dim]; NULL iff q is;
+                              may be q itself when q is dense */
+  int32_t* lens_out;       /* optional [n_seqs], neither lens nor pos: max(lens, position after the last row) */
+  int32_t* status;         /* optional */
+} fdllm_kv8_append_args;
+
+/* Store new keys and values into the cache, the rotation of k (and q)
+ * applied on the way.  Row starts[i] + j goes to position pos[i] + j of
+ * sequence i:
+ *     x' = [x_lo c - x_hi s, x_hi c + x_lo s]      (k and q; v is stored as it is)
+ * For each touched block of 16 positions and head, with the old tokens of
+ * the block that stay (positions below lens[i] that the call does not
+ * write),
+ *     scale = max(old scale if any old token stays, max|x'| * fl(1/127)),
+ *     code  = clamp(rint(x' * fl(1 / scale)), -127, 127),
+ *     staying old code = rint(code * fl(old scale / scale)),
+ * every operation rounded to float32 on its own (no fused multiply-add, so
+ * codes are reproducible to the bit); a scale below 2^-100 is stored as 0
+ * with codes 0.  Infinite values do not count in max|x'| and store +-127,
+ * NaN stores 0.  Positions of a block that hold no token are left as they
+ * are, and so are rows behind starts[n_seqs] of the outputs.  Rows whose
+ * position is beyond the page table or the rotation table are skipped
+ * (BAD_RANGE), blocks on a bad page too (BAD_PAGE; their q rows are still
+ * rotated).  The pages a call writes must be distinct within its table.
+ * Errors: ARG, CUDA. */
+FDLLM_API int fdllm_kv8_append(const fdllm_kv8* cache, const fdllm_kv8_append_args* args,
+                               void* cuda_stream);
+
+/* Operands of fdllm_kv8_attention. */
+typedef struct {
+  int32_t dtype;           /* fdllm_dtype of q and out */
+  int32_t n_tokens;        /* rows of q and out */
+  int32_t n_heads;         /* query heads, a multiple of n_kv_heads; query head h reads K/V head
+                              h / (n_heads / n_kv_heads) */
+  int32_t max_q;           /* launch hint: largest number of rows of one sequence (0 = n_tokens) */
+  int32_t max_len;         /* launch hint: largest lens (0 = 64 max_pages); wrong hints only cost
+                              time */
+  float scale;             /* softmax scale, e.g. 1 / sqrt(head_dim); finite */
+  const void* q;           /* [n_tokens, n_heads, head_dim], strides as for the append */
+  int64_t q_strides[2];
+  const int32_t* starts;   /* [n_seqs + 1] */
+  const int32_t* lens;     /* [n_seqs]: keys [0, lens[i]) of sequence i */
+  void* out;               /* like q, with its own strides; not overlapping q */
+  int64_t out_strides[2];
+  void* workspace;         /* 16-byte aligned, workspace_bytes long, free to be overwritten while
+                              the call's work runs; may be NULL (keys are then not split) */
+  size_t workspace_bytes;
+  int32_t* status;         /* optional */
+} fdllm_kv8_attention_args;
+
+/* Workspace with which fdllm_kv8_attention splits long contexts over the
+ * GPU for these operands (pointers are not looked at; the current device
+ * is).  Errors: ARG, CUDA. */
+FDLLM_API int fdllm_kv8_attention_workspace(const fdllm_kv8* cache,
+                                            const fdllm_kv8_attention_args* args, size_t* bytes);
+
+/* o = softmax(scale * q K^T) V for every row and head over the sequence's
+ * cached keys [0, lens[i]), without a mask among them: the attention of one
+ * new token, of a diffusion block over its prefix, itself and the suffix, or
+ * of a ragged batch of either.  The products run on fp16 tensor-core
+ * operands (codes are exact there) with float32 accumulation and float32
+ * softmax statistics; float32 q and softmax weights are carried as two fp16
+ * terms.  Rows of a sequence without keys give 0; rows behind
+ * starts[n_seqs] are left as they are.  Keys on a bad page are left out
+ * (BAD_PAGE).  A workspace smaller than asked is an error.  Errors: ARG,
+ * CUDA. */
+FDLLM_API int fdllm_kv8_attention(const fdllm_kv8* cache, const fdllm_kv8_attention_args* args,
+                                  void* cuda_stream);
+
+/* Operands of fdllm_sample; the four filters' arrays hold one value per row
+ * and may be NULL (temperature 1, filter off). */
+typedef struct {
+  const void* logits;        /* [rows, vocab], element-aligned */
+  int64_t row_stride;        /* elements from row to row, >= vocab */
+  int32_t dtype;             /* fdllm_dtype of logits */
+  int32_t rows;
+  int32_t vocab;             /* 1 .. 2^18 */
+  int32_t mask_id;           /* a token that is never drawn (e.g. the decoder's mask id); -1: none */
+  const float* temperature;  /* > 0; otherwise the row is greedy */
+  const int32_t* top_k;      /* <= 0: off */
+  const float* top_p;        /* >= 1: off */
+  const float* min_p;        /* <= 0: off */
+  const double* u;           /* [rows] uniform numbers in [0, 1) */
+  int32_t* tok;              /* [rows] */
+  float* prob;               /* optional [rows] */
+} fdllm_sample_args;
+
+/* Draw one token per row.  With l the row's logits, m their maximum over the
+ * tokens that may be drawn, w_i = exp((l_i - m) / temperature) in float64
+ * (temperature 1 for a greedy row), and the tokens sorted by falling logit,
+ * the lower id first among equal ones:
+ *   top_k  keeps the first top_k tokens;
+ *   top_p  then keeps tokens while the weight before them is below top_p
+ *          times the weight top_k kept (always the first);
+ *   min_p  then keeps those with w_i >= min(min_p, 1).
+ * tok is the lowest id at which the kept weight summed in order of the ids
+ * passes u times all kept weight (the last kept id if none does); a greedy
+ * row takes the first sorted token.  prob is the token's share of the kept
+ * weight: with no filter and temperature 1 or a greedy row, the decoder's
+ * confidence.  A weight below 2^-45 counts as 0.  NaN and -inf logits are
+ * never drawn (a row with nothing to draw gives tok -1, prob 0); +inf ones
+ * share all the weight.  Weights are summed as integers, so results do not
+ * depend on timing.  Errors: ARG, CUDA. */
+FDLLM_API int fdllm_sample(const fdllm_sample_args* args, void* cuda_stream);
 
 /* Per-kernel-class timing.  While enabled, every launch the ctx makes is
  * bracketed by CUDA events on the ctx's stream and accumulated per class

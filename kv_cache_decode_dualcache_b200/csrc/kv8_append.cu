@@ -1,0 +1,302 @@
+// fdllm_kv8_append: rotation, 8-bit rounding and storing of new keys and
+// values into the paged cache, one launch.
+//
+// One warp takes one block of 16 positions of one head: K (rotated, rounded,
+// stored), V (rounded, stored) or q (rotated, written back in its type).  A
+// lane holds 8 dims and their 8 rotation partners (d + head_dim / 2) of
+// head_dim / 32 tokens in registers, so a block is read once, its maximum is
+// one warp reduction and its codes leave in 8-byte stores; nothing passes
+// through shared memory.
+//
+// Bound: the bytes of the rows (read), the codes and the optional outputs
+// (written); the (cos, sin) rows are shared by the heads of a token and come
+// from L1/L2.
+#include <algorithm>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "kv8.h"
+
+namespace fd {
+namespace {
+
+constexpr int BLK = FDLLM_KV8_BLOCK;
+constexpr int APP_WARPS = 8;
+constexpr float TINY_SCALE = 7.888609052210118e-31f;  // 2^-100
+
+struct AppendP {
+  fdllm_kv8 c;
+  fdllm_kv8_append_args a;
+};
+
+// 8 consecutive elements as float (16-byte aligned; plain loads, q_out may
+// be q itself).
+template <typename T> FD_DEV void load8(const T* p, float* x);
+template <> FD_DEV void load8<float>(const float* p, float* x) {
+  const float4 a = *reinterpret_cast<const float4*>(p);
+  const float4 b = *reinterpret_cast<const float4*>(p + 4);
+  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+}
+template <> FD_DEV void load8<__half>(const __half* p, float* x) {
+  const uint4 u = *reinterpret_cast<const uint4*>(p);
+  const __half2* h = reinterpret_cast<const __half2*>(&u);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(h[i]);
+    x[2 * i] = f.x;
+    x[2 * i + 1] = f.y;
+  }
+}
+template <> FD_DEV void load8<__nv_bfloat16>(const __nv_bfloat16* p, float* x) {
+  const uint4 u = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+
+template <typename T> FD_DEV void store8(T* p, const float* x) {
+  T v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = from_f<T>(x[i]);
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(v) / 16; ++i)
+    reinterpret_cast<uint4*>(p)[i] = reinterpret_cast<const uint4*>(v)[i];
+}
+
+FD_DEV float finite_abs(float x) {
+  const float a = fabsf(x);
+  return a <= 3.402823466e38f ? a : 0.0f;   // inf and NaN do not count
+}
+
+// clamp(rint(y), -127, 127), NaN -> 0 (the conversion saturates and maps NaN
+// to 0).
+FD_DEV int to_code(float y) { return max(-127, min(127, __float2int_rn(y))); }
+
+FD_DEV uint2 pack8(const int* q) {
+  uint2 r;
+  r.x = (q[0] & 255) | ((q[1] & 255) << 8) | ((q[2] & 255) << 16) | ((uint32_t)q[3] << 24);
+  r.y = (q[4] & 255) | ((q[5] & 255) << 8) | ((q[6] & 255) << 16) | ((uint32_t)q[7] << 24);
+  return r;
+}
+
+FD_DEV uint2 rescale8(uint2 w, float ratio) {
+  int q[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t u = i < 4 ? w.x : w.y;
+    const int code = (int)(int8_t)(u >> (8 * (i & 3)));
+    q[i] = __float2int_rn(__fmul_rn((float)code, ratio));
+  }
+  return pack8(q);
+}
+
+template <typename T, int HD>
+__global__ void __launch_bounds__(APP_WARPS * 32) kv8_append_kernel(const AppendP P) {
+  constexpr int LPT = HD / 16;      // lanes per token
+  constexpr int TPP = 32 / LPT;     // tokens per pass
+  constexpr int NP = BLK / TPP;     // passes over the block
+  constexpr int H2 = HD / 2;
+  const fdllm_kv8& c = P.c;
+  const fdllm_kv8_append_args& a = P.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int seq = blockIdx.z;
+  const int head = blockIdx.x * APP_WARPS + warp;   // K heads, V heads, q heads
+  const int Hkv = c.n_kv_heads;
+
+  const int r_lo = min(max(a.starts[seq], 0), a.n_tokens);
+  const int r_hi = min(max(a.starts[seq + 1], r_lo), a.n_tokens);
+  const int len_in = a.lens[seq];
+  const int w0 = a.pos ? a.pos[seq] : len_in;
+  int n = r_hi - r_lo;
+  int bad = 0;
+  int limit = c.max_pages * FDLLM_KV8_PAGE;
+  const int len = min(max(len_in, 0), limit);
+  if (len != len_in) bad |= FDLLM_KV8_BAD_RANGE;
+  if (a.rope) limit = min(limit, a.rope_len);
+  if (n > 0 && (w0 < 0 || w0 > limit - n)) {
+    bad |= FDLLM_KV8_BAD_RANGE;
+    n = w0 < 0 ? 0 : max(limit - w0, 0);
+  }
+  const int w1 = w0 + n;
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) {
+    if (bad && a.status) atomicOr(a.status, bad);
+    if (a.lens_out) a.lens_out[seq] = n > 0 ? max(len, w1) : len;
+  }
+  if (n == 0 || head >= 2 * Hkv + (a.q ? a.n_heads : 0)) return;
+
+  const bool is_q = head >= 2 * Hkv, is_v = !is_q && head >= Hkv;
+  const int g = is_q ? head - 2 * Hkv : is_v ? head - Hkv : head;
+  const T* src = reinterpret_cast<const T*>(is_q ? a.q : is_v ? a.v : a.k);
+  const int64_t* st = is_q ? a.q_strides : is_v ? a.v_strides : a.k_strides;
+  src += (int64_t)g * st[1];
+  const int64_t row_stride = st[0];
+  T* out = reinterpret_cast<T*>(is_q ? a.q_out : is_v ? a.v_out : a.k_out);
+  const int out_heads = is_q ? a.n_heads : Hkv;
+  const bool rotate = a.rope != nullptr && !is_v;
+  const int sub = lane % LPT, tk = lane / LPT;
+  const int d0 = 8 * sub;
+
+  const int b_lo = w0 / BLK, b_hi = (w1 - 1) / BLK;
+  for (int b = b_lo + blockIdx.y; b <= b_hi; b += gridDim.y) {
+    const int base = b * BLK;
+    float x[NP][16];   // dims d0 .. d0 + 7, then their partners
+    float top = 0.0f;
+#pragma unroll
+    for (int p = 0; p < NP; ++p) {
+      const int at = base + p * TPP + tk;
+      if (at >= w0 && at < w1) {
+        const T* row = src + (int64_t)(r_lo + at - w0) * row_stride + d0;
+        load8<T>(row, x[p]);
+        load8<T>(row + H2, x[p] + 8);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[p][i] = 0.0f;
+      }
+    }
+    if (rotate) {
+#pragma unroll
+      for (int p = 0; p < NP; ++p) {
+        const int at = base + p * TPP + tk;
+        if (at >= w0 && at < w1) {
+          const float4* cs = reinterpret_cast<const float4*>(a.rope + ((int64_t)at * H2 + d0) * 2);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float4 w = __ldg(cs + i);
+            const float cw[2] = {w.x, w.z}, sw[2] = {w.y, w.w};
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const float lo = x[p][2 * i + j], hi = x[p][8 + 2 * i + j];
+              x[p][2 * i + j] = __fsub_rn(__fmul_rn(lo, cw[j]), __fmul_rn(hi, sw[j]));
+              x[p][8 + 2 * i + j] = __fadd_rn(__fmul_rn(hi, cw[j]), __fmul_rn(lo, sw[j]));
+            }
+          }
+        }
+      }
+    }
+    if (is_q) {
+#pragma unroll
+      for (int p = 0; p < NP; ++p) {
+        const int at = base + p * TPP + tk;
+        if (at >= w0 && at < w1) {
+          T* o = out + ((int64_t)(r_lo + at - w0) * out_heads + g) * HD + d0;
+          store8<T>(o, x[p]);
+          store8<T>(o + H2, x[p] + 8);
+        }
+      }
+      continue;
+    }
+    const int page = c.page_table[(int64_t)seq * c.table_stride + base / FDLLM_KV8_PAGE];
+    if (page < 0 || page >= c.n_pages) {
+      if (lane == 0 && a.status) atomicOr(a.status, FDLLM_KV8_BAD_PAGE);
+      continue;
+    }
+    const int sb = base % FDLLM_KV8_PAGE / BLK;
+    float* sp = (is_v ? c.v_scale : c.k_scale) + (int64_t)page * c.scale_stride + g * 4 + sb;
+    int8_t* codes = (is_v ? c.v : c.k) + (int64_t)page * c.page_stride +
+                    ((int64_t)g * FDLLM_KV8_PAGE + sb * BLK) * HD + d0;
+    // old tokens of the block that stay: before w0, or behind the new rows
+    const bool any_kept = base < min(len, w0) || w1 < min(len, base + BLK);
+    const float old = any_kept ? *sp : 0.0f;
+#pragma unroll
+    for (int p = 0; p < NP; ++p)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) top = fmaxf(top, finite_abs(x[p][i]));
+    top = warp_max(top);
+    float scale = fmaxf(old, __fmul_rn(top, 1.0f / 127.0f));
+    if (!(scale >= TINY_SCALE)) scale = 0.0f;
+    const float inv = scale > 0.0f ? __fdiv_rn(1.0f, scale) : 0.0f;
+    const bool regrid = any_kept && scale != old;
+    const float ratio = regrid && scale > 0.0f ? __fdiv_rn(old, scale) : 0.0f;
+    __syncwarp();   // every lane has read the old scale
+    if (lane == 0) *sp = scale;
+#pragma unroll
+    for (int p = 0; p < NP; ++p) {
+      const int slot = p * TPP + tk, at = base + slot;
+      uint2* lo = reinterpret_cast<uint2*>(codes + slot * HD);
+      uint2* hi = reinterpret_cast<uint2*>(codes + slot * HD + H2);
+      if (at >= w0 && at < w1) {
+        int q[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) q[i] = to_code(__fmul_rn(x[p][i], inv));
+        *lo = pack8(q);
+        *hi = pack8(q + 8);
+        if (out) {
+          float y[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) y[i] = __fmul_rn((float)q[i], scale);
+          T* o = out + ((int64_t)(r_lo + at - w0) * out_heads + g) * HD + d0;
+          store8<T>(o, y);
+          store8<T>(o + H2, y + 8);
+        }
+      } else if (regrid && at < len) {
+        *lo = rescale8(*lo, ratio);
+        *hi = rescale8(*hi, ratio);
+      }
+    }
+  }
+}
+
+template <typename T>
+cudaError_t launch_append_t(const AppendP& P, dim3 grid, cudaStream_t st) {
+  const dim3 block(APP_WARPS * 32);
+  switch (P.c.head_dim) {
+    case 128: return launch_k(false, kv8_append_kernel<T, 128>, grid, block, 0, st, P);
+    case 64: return launch_k(false, kv8_append_kernel<T, 64>, grid, block, 0, st, P);
+    default: return launch_k(false, kv8_append_kernel<T, 32>, grid, block, 0, st, P);
+  }
+}
+
+}  // namespace
+}  // namespace fd
+
+extern "C" int fdllm_kv8_append(const fdllm_kv8* cache, const fdllm_kv8_append_args* args,
+                                void* cuda_stream) {
+  using namespace fd;
+  const char* call = "fdllm_kv8_append";
+  AppendP P{};
+  if (const char* why = kv8::check_cache(cache, &P.c)) return kv8::fail(call, FDLLM_ERR_ARG, why);
+  if (!args) return kv8::fail(call, FDLLM_ERR_ARG, "args is NULL");
+  P.a = *args;
+  const fdllm_kv8_append_args& a = P.a;
+  const int esz = kv8::elem_bytes(a.dtype);
+  if (!esz) return kv8::fail(call, FDLLM_ERR_ARG, "unknown dtype");
+  if (a.n_tokens < 0 || a.max_new < 0 || a.reserved)
+    return kv8::fail(call, FDLLM_ERR_ARG, "n_tokens and max_new must be >= 0, reserved 0");
+  if (!a.starts || !a.lens) return kv8::fail(call, FDLLM_ERR_ARG, "starts or lens is NULL");
+  if (!kv8::aligned4({a.starts, a.lens, a.pos, a.lens_out, a.status}))
+    return kv8::fail(call, FDLLM_ERR_ARG, "int32 arrays must be 4-byte aligned");
+  if (a.lens_out && (a.lens_out == a.lens || a.lens_out == a.pos))
+    return kv8::fail(call, FDLLM_ERR_ARG, "lens_out must be neither lens nor pos");
+  if (a.rope && (a.rope_len < 1 || !kv8::aligned16(a.rope)))
+    return kv8::fail(call, FDLLM_ERR_ARG, "rope needs rope_len >= 1 and 16-byte alignment");
+  if (a.n_tokens > 0) {
+    if (!a.k || !a.v) return kv8::fail(call, FDLLM_ERR_ARG, "k or v is NULL");
+    if (!kv8::rows_ok(a.k, a.k_strides, esz) || !kv8::rows_ok(a.v, a.v_strides, esz) ||
+        (a.q && !kv8::rows_ok(a.q, a.q_strides, esz)))
+      return kv8::fail(call, FDLLM_ERR_ARG, "rows and heads of k, v and q must be 16-byte aligned");
+  }
+  if ((a.q != nullptr) != (a.q_out != nullptr))
+    return kv8::fail(call, FDLLM_ERR_ARG, "q and q_out go together");
+  if (a.q && (a.n_heads < 1 || a.n_heads > 65535))
+    return kv8::fail(call, FDLLM_ERR_ARG, "n_heads must be in [1, 65535]");
+  if (!kv8::aligned16(a.k_out) || !kv8::aligned16(a.v_out) || !kv8::aligned16(a.q_out))
+    return kv8::fail(call, FDLLM_ERR_ARG, "outputs must be 16-byte aligned");
+
+  // Blocks of 16 that a run of max_new rows can touch; the kernel strides
+  // over whatever a sequence has beyond that.
+  const int rows = a.max_new > 0 ? std::min(a.max_new, a.n_tokens) : a.n_tokens;
+  const int64_t blocks = std::max<int64_t>(1, ((int64_t)rows + 2 * BLK - 2) / BLK);
+  const int heads = 2 * P.c.n_kv_heads + (a.q ? a.n_heads : 0);
+  const dim3 grid((heads + APP_WARPS - 1) / APP_WARPS, (unsigned)std::min<int64_t>(blocks, 65535),
+                  P.c.n_seqs);
+  cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
+  const cudaError_t e = a.dtype == FDLLM_DTYPE_F32    ? launch_append_t<float>(P, grid, st)
+                        : a.dtype == FDLLM_DTYPE_BF16 ? launch_append_t<__nv_bfloat16>(P, grid, st)
+                                                      : launch_append_t<__half>(P, grid, st);
+  if (e != cudaSuccess) return kv8::fail(call, FDLLM_ERR_CUDA, cudaGetErrorString(e));
+  return FDLLM_OK;
+}

@@ -31,8 +31,9 @@ EXPORTED = ("fdllm_create", "fdllm_load_weights", "fdllm_generate", "fdllm_gener
             "fdllm_generate_batch", "fdllm_generate_fixed_k",
             "fdllm_step_debug", "fdllm_read_kv", "fdllm_kv_similarity", "fdllm_selftest_wait_timeout",
             "fdllm_gemm", "fdllm_gemm_f16", "fdllm_attention",
-            "fdllm_gemm_noalloc", "fdllm_profile_enable", "fdllm_profile_read",
-            "fdllm_last_error", "fdllm_launch_count", "fdllm_inexact_weight_count",
+            "fdllm_gemm_noalloc", "fdllm_kv8_append", "fdllm_kv8_attention",
+            "fdllm_kv8_attention_workspace", "fdllm_sample",
+            "fdllm_profile_enable", "fdllm_profile_read", "fdllm_last_error", "fdllm_launch_count", "fdllm_inexact_weight_count",
             "fdllm_destroy")
 
 
@@ -77,6 +78,49 @@ class FdllmKernelStat(ctypes.Structure):
                 ("flops", ctypes.c_double)]
 
 
+class FdllmKv8(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+                ("page_stride", ctypes.c_int64), ("scale_stride", ctypes.c_int64),
+                ("table_stride", ctypes.c_int64), ("n_pages", ctypes.c_int32),
+                ("n_seqs", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
+
+
+class FdllmKv8AppendArgs(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("n_tokens", ctypes.c_int32),
+                ("n_heads", ctypes.c_int32), ("max_new", ctypes.c_int32),
+                ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("q", ctypes.c_void_p),
+                ("k_token", ctypes.c_int64), ("k_head", ctypes.c_int64),
+                ("v_token", ctypes.c_int64), ("v_head", ctypes.c_int64),
+                ("q_token", ctypes.c_int64), ("q_head", ctypes.c_int64),
+                ("starts", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("pos", ctypes.c_void_p),
+                ("rope", ctypes.c_void_p), ("rope_len", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("k_out", ctypes.c_void_p),
+                ("v_out", ctypes.c_void_p), ("q_out", ctypes.c_void_p),
+                ("lens_out", ctypes.c_void_p), ("status", ctypes.c_void_p)]
+
+
+class FdllmKv8AttentionArgs(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("n_tokens", ctypes.c_int32),
+                ("n_heads", ctypes.c_int32), ("max_q", ctypes.c_int32),
+                ("max_len", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("q", ctypes.c_void_p), ("q_token", ctypes.c_int64), ("q_head", ctypes.c_int64),
+                ("starts", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("out", ctypes.c_void_p),
+                ("out_token", ctypes.c_int64), ("out_head", ctypes.c_int64),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+                ("status", ctypes.c_void_p)]
+
+
+class FdllmSampleArgs(ctypes.Structure):
+    _fields_ = [("logits", ctypes.c_void_p), ("row_stride", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("rows", ctypes.c_int32), ("vocab", ctypes.c_int32),
+                ("mask_id", ctypes.c_int32), ("temperature", ctypes.c_void_p),
+                ("top_k", ctypes.c_void_p), ("top_p", ctypes.c_void_p),
+                ("min_p", ctypes.c_void_p), ("u", ctypes.c_void_p), ("tok", ctypes.c_void_p),
+                ("prob", ctypes.c_void_p)]
+
+
 class FdllmError(RuntimeError):
     def __init__(self, code: int, msg: str):
         super().__init__(f"fdllm error {code}: {msg}")
@@ -119,6 +163,11 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.fdllm_gemm_f16.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, i32]
     lib.fdllm_attention.argtypes = [vp, vp, vp, i32, i32, i32]
     lib.fdllm_gemm_noalloc.argtypes = [vp, vp, vp, i32, i32, i32, i32, vp]
+    lib.fdllm_kv8_append.argtypes = [P(FdllmKv8), P(FdllmKv8AppendArgs), vp]
+    lib.fdllm_kv8_attention.argtypes = [P(FdllmKv8), P(FdllmKv8AttentionArgs), vp]
+    lib.fdllm_kv8_attention_workspace.argtypes = [P(FdllmKv8), P(FdllmKv8AttentionArgs),
+                                                  P(ctypes.c_size_t)]
+    lib.fdllm_sample.argtypes = [P(FdllmSampleArgs), vp]
     lib.fdllm_profile_enable.argtypes = [vp, i32]
     lib.fdllm_profile_read.argtypes = [vp, P(FdllmKernelStat), i32, P(i32)]
     lib.fdllm_last_error.argtypes = [vp]
@@ -132,6 +181,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                  "fdllm_generate_batch", "fdllm_generate_fixed_k", "fdllm_step_debug", "fdllm_read_kv",
                  "fdllm_kv_similarity", "fdllm_selftest_wait_timeout", "fdllm_gemm",
                  "fdllm_gemm_f16", "fdllm_attention", "fdllm_gemm_noalloc",
+                 "fdllm_kv8_append", "fdllm_kv8_attention", "fdllm_kv8_attention_workspace",
+                 "fdllm_sample",
                  "fdllm_profile_enable", "fdllm_profile_read", "fdllm_destroy"):
         getattr(lib, name).restype = ctypes.c_int
     _lib = lib
@@ -377,6 +428,237 @@ def fdllm_attention(ctx, q_dev, o_dev, layer: int, L: int) -> None:
         raise ValueError(f"o_dev needs {need} contiguous rows")
     _check(load_library().fdllm_attention(ctx, q_dev.data_ptr(), o_dev.data_ptr(), layer, M, L),
            ctx)
+
+
+# ------------------------------------------------ 8-bit paged K/V cache, sampling
+KV8_PAGE, KV8_BLOCK = 64, 16              # positions per page, positions that share a scale
+KV8_BAD_PAGE, KV8_BAD_RANGE = 1, 2        # bits of a call's status word
+
+
+def _type_code(t) -> int:
+    import torch
+    code = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{t.dtype} is not a type of this call (float32, bfloat16, float16)")
+    return code
+
+
+def _same_device(dev: int, **tensors) -> None:
+    for name, t in tensors.items():
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{name} must be on the same CUDA device as the other operands")
+
+
+def _vector(name: str, t, n: int, dtype) -> None:
+    """An optional contiguous 1-D tensor of n elements."""
+    if t is not None and (t.dtype != dtype or t.dim() != 1 or t.shape[0] != n
+                          or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} elements")
+
+
+def _rows(name: str, t, heads: Optional[int], hd: int) -> None:
+    if t.dim() != 3 or t.shape[2] != hd or (heads is not None and t.shape[1] != heads) or (
+            t.stride(2) != 1 and t.shape[0] > 0):
+        raise ValueError(f"{name} must be [tokens, {heads or 'heads'}, {hd}] with contiguous vectors")
+
+
+def _strides(t):
+    """Token and head strides; those of dims of one element do not matter."""
+    return (t.stride(0) if t.shape[0] > 1 else 0, t.stride(1) if t.shape[1] > 1 else 0)
+
+
+def _enqueue(dev: int, stream, call) -> int:
+    """call(stream handle) with `dev` current; stream None = torch's current
+    stream there."""
+    import torch
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(dev)
+    if torch._C._cuda_getDevice() == dev:
+        return call(stream)
+    with torch.cuda.device(dev):
+        return call(stream)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+class Kv8Cache:
+    """One layer's 8-bit paged K/V cache over the caller's tensors.
+
+    k, v: int8 [n_pages, n_kv_heads, 64, head_dim]; k_scale, v_scale: float32
+    [n_pages, n_kv_heads, 4] (pages may be strided, e.g. slices of one pool
+    for all layers; k and v alike); page_table: int32 [n_seqs, max_pages]."""
+
+    def __init__(self, k, v, k_scale, v_scale, page_table):
+        import torch
+        if k.dim() != 4 or k.dtype != torch.int8 or k.shape[2] != KV8_PAGE:
+            raise ValueError("k must be int8 [n_pages, n_kv_heads, 64, head_dim]")
+        n_pages, heads, _, hd = k.shape
+        if v.shape != k.shape or v.dtype != k.dtype or v.stride() != k.stride():
+            raise ValueError("v must have k's type, shape and strides")
+        for name, s in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if s.dtype != torch.float32 or tuple(s.shape) != (n_pages, heads, KV8_PAGE // KV8_BLOCK) \
+                    or s.stride() != k_scale.stride():
+                raise ValueError(f"{name} must be float32 [n_pages, n_kv_heads, 4], K and V alike")
+        if k.stride()[1:] != (KV8_PAGE * hd, hd, 1) or k_scale.stride()[1:] != (4, 1):
+            raise ValueError("a page's codes and scales must be contiguous")
+        if page_table.dim() != 2 or page_table.dtype != torch.int32 or (
+                page_table.stride(1) != 1 and page_table.shape[1] > 1):
+            raise ValueError("page_table must be int32 [n_seqs, max_pages] with contiguous rows")
+        self.device = k.get_device()
+        if self.device < 0:
+            raise ValueError("the cache must be on a CUDA device")
+        _same_device(self.device, v=v, k_scale=k_scale, v_scale=v_scale, page_table=page_table)
+        self.k, self.v, self.k_scale, self.v_scale, self.page_table = k, v, k_scale, v_scale, page_table
+        self.n_seqs, self.max_pages = page_table.shape
+        self.n_kv_heads, self.head_dim = heads, hd
+        one_row = self.n_seqs == 1
+        self.struct = FdllmKv8(
+            k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+            page_table.data_ptr(), k.stride(0) if n_pages > 1 else 0,
+            k_scale.stride(0) if n_pages > 1 else 0, 0 if one_row else page_table.stride(0),
+            n_pages, self.n_seqs, self.max_pages, heads, hd)
+        self._workspace: Dict[tuple, int] = {}   # bytes by shape, not memory
+
+
+def fdllm_kv8_append(cache: Kv8Cache, k, v, starts, lens, pos=None, rope=None, q=None,
+                     max_new: int = 0, stored: bool = False, lens_out=None, status=None,
+                     stream=None):
+    """Store rows k, v [tokens, n_kv_heads, head_dim] into the cache, rotated
+    by rope [positions, head_dim / 2, 2] (cos, sin), and rotate q [tokens,
+    heads, head_dim] (see the header).  Returns (q_out, k_out, v_out): the
+    rotated q (None without q) and, with stored, the rows as the cache now
+    stands for them (else None, None)."""
+    import torch
+    hd, dev = cache.head_dim, cache.device
+    _rows("k", k, cache.n_kv_heads, hd)
+    _rows("v", v, cache.n_kv_heads, hd)
+    T = k.shape[0]
+    if v.shape[0] != T or v.dtype != k.dtype or (
+            q is not None and (q.shape[0] != T or q.dtype != k.dtype)):
+        raise ValueError("k, v and q must have the same number of rows and the same type")
+    i32 = torch.int32
+    _vector("starts", starts, cache.n_seqs + 1, i32)
+    _vector("lens", lens, cache.n_seqs, i32)
+    _vector("pos", pos, cache.n_seqs, i32)
+    _vector("lens_out", lens_out, cache.n_seqs, i32)
+    _vector("status", status, 1, i32)
+    if rope is not None and (rope.dtype != torch.float32 or rope.dim() != 3 or
+                             tuple(rope.shape[1:]) != (hd // 2, 2) or not rope.is_contiguous()):
+        raise ValueError(f"rope must be contiguous float32 [positions, {hd // 2}, 2]")
+    _same_device(dev, k=k, v=v, q=q, starts=starts, lens=lens, pos=pos, rope=rope,
+                 lens_out=lens_out, status=status)
+    q_out = k_out = v_out = None
+    if q is not None:
+        _rows("q", q, None, hd)
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if stored:
+        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        v_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    ks, vs, qs = _strides(k), _strides(v), _strides(q) if q is not None else (0, 0)
+    a = FdllmKv8AppendArgs(
+        _type_code(k), T, q.shape[1] if q is not None else 0, max_new, k.data_ptr(), v.data_ptr(),
+        _ptr(q), ks[0], ks[1], vs[0], vs[1], qs[0], qs[1], _ptr(starts), _ptr(lens), _ptr(pos),
+        _ptr(rope), rope.shape[0] if rope is not None else 0, 0, _ptr(k_out), _ptr(v_out),
+        _ptr(q_out), _ptr(lens_out), _ptr(status))
+    lib = load_library()
+    _check(_enqueue(dev, stream, lambda s: lib.fdllm_kv8_append(
+        ctypes.byref(cache.struct), ctypes.byref(a), s)), None)
+    return q_out, k_out, v_out
+
+
+def fdllm_kv8_attention(cache: Kv8Cache, q, starts, lens, scale: Optional[float] = None, out=None,
+                        max_q: int = 0, max_len: int = 0, workspace=None, status=None,
+                        stream=None):
+    """softmax(scale q K^T) V of every row of q [tokens, heads, head_dim] over
+    its sequence's cached keys [0, lens[i]); scale None = 1 / sqrt(head_dim).
+    workspace: a uint8 tensor to use instead of a fresh one (its size:
+    fdllm_kv8_attention_workspace); pass one when the work is enqueued on a
+    stream that is not torch's current one."""
+    import torch
+    hd, dev = cache.head_dim, cache.device
+    _rows("q", q, None, hd)
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    else:
+        _rows("out", out, q.shape[1], hd)
+        if out.dtype != q.dtype or out.shape[0] != q.shape[0]:
+            raise ValueError("out must have q's shape and type")
+    _vector("starts", starts, cache.n_seqs + 1, torch.int32)
+    _vector("lens", lens, cache.n_seqs, torch.int32)
+    _vector("status", status, 1, torch.int32)
+    _same_device(dev, q=q, starts=starts, lens=lens, out=out, workspace=workspace, status=status)
+    qs, os_ = _strides(q), _strides(out)
+    a = FdllmKv8AttentionArgs(
+        _type_code(q), q.shape[0], q.shape[1], max_q, max_len,
+        hd ** -0.5 if scale is None else scale, q.data_ptr(), qs[0], qs[1], starts.data_ptr(),
+        lens.data_ptr(), out.data_ptr(), os_[0], os_[1], None, 0, _ptr(status))
+    if workspace is None:
+        need = fdllm_kv8_attention_workspace(cache, q.shape[0], q.shape[1], q.dtype, max_q, max_len)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    if workspace is not None:
+        a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel()
+    lib = load_library()
+    _check(_enqueue(dev, stream, lambda s: lib.fdllm_kv8_attention(
+        ctypes.byref(cache.struct), ctypes.byref(a), s)), None)
+    return out
+
+
+def fdllm_kv8_attention_workspace(cache: Kv8Cache, n_tokens: int, n_heads: int, dtype,
+                                  max_q: int = 0, max_len: int = 0) -> int:
+    """Bytes of workspace for an attention call of this shape (remembered by
+    the cache object)."""
+    import torch
+    key = (n_tokens, n_heads, dtype, max_q, max_len)
+    need = cache._workspace.get(key)
+    if need is None:
+        a = FdllmKv8AttentionArgs(_type_code(torch.empty(0, dtype=dtype)), n_tokens, n_heads, max_q,
+                                  max_len, 1.0)
+        n = ctypes.c_size_t()
+        lib = load_library()
+        _check(_enqueue(cache.device, 0, lambda s: lib.fdllm_kv8_attention_workspace(
+            ctypes.byref(cache.struct), ctypes.byref(a), ctypes.byref(n))), None)
+        if len(cache._workspace) >= 256:
+            cache._workspace.clear()
+        need = cache._workspace[key] = n.value
+    return need
+
+
+def fdllm_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None,
+                 mask_id: int = -1, tok=None, prob=None, stream=None):
+    """One token per row of logits [rows, vocab] (see the header).  u: float64
+    [rows] in [0, 1); temperature, top_p, min_p: float32 [rows] or None;
+    top_k: int32 [rows] or None.  Returns (tok int32 [rows], prob float32
+    [rows])."""
+    import torch
+    if logits.dim() != 2 or (logits.stride(1) != 1 and logits.shape[1] > 1):
+        raise ValueError("logits must be [rows, vocab] with contiguous rows")
+    rows, vocab = logits.shape
+    dev = logits.get_device()
+    if dev < 0:
+        raise ValueError("logits must be on a CUDA device")
+    f32 = torch.float32
+    _vector("u", u, rows, torch.float64)
+    _vector("temperature", temperature, rows, f32)
+    _vector("top_k", top_k, rows, torch.int32)
+    _vector("top_p", top_p, rows, f32)
+    _vector("min_p", min_p, rows, f32)
+    _vector("tok", tok, rows, torch.int32)
+    _vector("prob", prob, rows, f32)
+    _same_device(dev, u=u, temperature=temperature, top_k=top_k, top_p=top_p, min_p=min_p, tok=tok,
+                 prob=prob)
+    if tok is None:
+        tok = torch.empty(rows, dtype=torch.int32, device=logits.device)
+    if prob is None:
+        prob = torch.empty(rows, dtype=f32, device=logits.device)
+    a = FdllmSampleArgs(logits.data_ptr(), logits.stride(0) if rows > 1 else vocab,
+                        _type_code(logits), rows, vocab, mask_id, _ptr(temperature), _ptr(top_k),
+                        _ptr(top_p), _ptr(min_p), u.data_ptr(), tok.data_ptr(), prob.data_ptr())
+    lib = load_library()
+    _check(_enqueue(dev, stream, lambda s: lib.fdllm_sample(ctypes.byref(a), s)), None)
+    return tok, prob
 
 
 def fdllm_profile_enable(ctx, enable: bool = True) -> None:
