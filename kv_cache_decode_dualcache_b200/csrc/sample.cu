@@ -6,23 +6,26 @@
 // over distributed shared memory, in one launch without a workspace.
 //
 // The kept tokens are a prefix of the row sorted by (falling logit, rising
-// id), so they are described by a cut, the last kept token, and nothing is
-// sorted.  top-k looks for its cut on counts, top-p on weight sums, both in
-// three steps: a histogram of z = (m - l) / T over 256 linear bins of [0, 32)
-// (a token beyond weighs under 2^-45 and cannot be drawn), one over 256
-// bins of the bin the cut falls into, and the exact order of the few tokens
-// of that small bin.  Bins are linear in z and not in the logit's bits
-// because that spreads a row's tokens evenly: the shared-memory atomics of a
-// warp then rarely meet.  A small bin with more tokens than the list holds
-// (thousands of equal logits) is searched by bisection over the logit's bits.
-// The draw walks the ids in order.
+// id).  Usually a small superset of them is known early: min-p bounds
+// z = (m - l) / T; the top_k-th largest of the threads' own maxima bounds the
+// top_k-th token; a histogram of the weights bounds the nucleus.  Then the
+// superset is gathered (at most CAP tokens), sorted by one CTA, and the
+// filters and the draw are prefix sums.  Larger kept sets are described by
+// a cut, the last kept token, found on counts (top-k) or weight sums (top-p)
+// by a histogram over 256 linear bins of z in [0, 32) (a token beyond weighs
+// under 2^-45 and cannot be drawn), one over 256 bins of the bin the cut
+// falls into, and the exact order of the few tokens of that small bin; if
+// even that holds more than CAP tokens (thousands of equal logits), by
+// bisection over the logit's bits.  The draw then walks the ids in order.
+// Bins are linear in z and not in the logit's bits because that spreads a
+// row's tokens evenly: the shared-memory atomics of a warp then rarely meet.
 //
 // Weights are held as integers, w = rint(exp(-z) 2^44) with the exponential
 // in float64: sums of up to 2^18 weights are exact in 64 bits, so no order
 // of additions can change a cut or a token.
 //
 // Bound: the logits' bytes for many rows; for few rows the chain of cluster
-// barriers (one for the maximum, three for each search, one for the draw).
+// barriers.
 #include <algorithm>
 
 #include "common.cuh"
@@ -40,83 +43,129 @@ constexpr int MAX_SLICE = 1 << 16;           // tokens of a CTA (histogram words
 constexpr int SLICE_BYTES = 78 << 10;        // two CTAs and their lists fit on an SM
 constexpr int BINS = 256;
 constexpr float Z_BINS = 8.0f;               // bins per unit of z: 256 / 32
-constexpr int CAP = 1024;                    // tokens of a small bin whose order is taken directly
+constexpr int CAP = 1024;                    // tokens that are gathered and sorted
 constexpr double W_ONE = 17592186044416.0;   // 2^44
-constexpr uint32_t KEY_NONE = 0;             // a token that cannot be drawn
+constexpr float F_MAX = 3.402823466e38f;
 
 typedef unsigned long long u64;
 
-// Order-preserving key of a logit; NaN and -inf give KEY_NONE.
+// Order-preserving key of a live logit (> -inf).
 FD_DEV uint32_t logit_key(float l) {
-  if (!(l > -INFINITY)) return KEY_NONE;
   const uint32_t u = __float_as_uint(l + 0.0f);   // -0 and +0 are equal logits
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 FD_DEV float key_logit(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
 }
+// A token's place in the order: larger first; equal logits, the lower id.
+FD_DEV u64 order_of(float l, int id) { return ((u64)logit_key(l) << 32) | (uint32_t)~(uint32_t)id; }
+FD_DEV float order_logit(u64 o) { return key_logit((uint32_t)(o >> 32)); }
+FD_DEV int order_id(u64 o) { return (int)~(uint32_t)o; }
 
 struct Shared {
-  uint32_t hist[2][4][BINS];   // counts, or weights in words of 15, 15 and 15 bits
+  double exp2_64[64];          // 2^(j / 64)
+  uint32_t hist[2][4][BINS];   // weights in words of 15, 15 and 15 bits; counts
   u64 red[SW];
-  u64 scan[SW];
   u64 part[2];                 // this CTA's share of a cluster sum (by parity of use)
-  u64 best;                    // largest (key, lowest id)
-  u64 before;
-  int bin;
-  int n_list;
-  uint32_t list_key[CAP];      // this CTA's tokens of the small bin
-  int list_id[CAP];
-  uint32_t all_key[CAP];       // the cluster's
-  int all_id[CAP];
-  u64 all_w[CAP];
+  u64 before, before_count;
+  float top;                   // this CTA's largest logit
+  int bin, n_list, cut_id, cut_ties, pick;
   uint32_t cut_key;
-  int cut_id;
-  int cut_ties;
+  u64 list[CAP];               // this CTA's gathered tokens (order_of)
+  u64 all[CAP];                // the cluster's
+  u64 w[CAP];                  // their weights, or running sums
 };
 
-template <typename U> FD_DEV U ld_remote(const U* p, uint32_t rank) {
-  U v;
-  const uint32_t a = cluster_map(smem_u32(p), rank);
-  if constexpr (sizeof(U) == 8)
-    asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(a) : "memory");
-  else
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+FD_DEV uint32_t ld_remote32(const void* p, uint32_t rank) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cluster_map(smem_u32(p), rank)) : "memory");
+  return v;
+}
+FD_DEV u64 ld_remote64(const void* p, uint32_t rank) {
+  u64 v;
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(cluster_map(smem_u32(p), rank)) : "memory");
   return v;
 }
 
 // The row's state that every thread of the cluster knows.
 struct Row {
-  uint32_t kmax;
-  float m;
-  double temp;
+  float m;          // largest logit
   float zs;         // bins per unit of logit
-  double min_w;     // min-p
+  double md, y;     // m; log2(e) / T
+  const double* exp2_64;
   // the cut: kept are key > cut_key, and key == cut_key with id <= cut_id
   uint32_t cut_key;
   int cut_id;
-  int ties;         // kept tokens with key == cut_key (valid once a cut was set)
-  bool has_cut, listed;   // listed: the class of cut_key is in Shared::all_*
+  int ties;         // kept tokens with key == cut_key
+  bool has_cut, listed;   // listed: the class of cut_key is in Shared::all[0 .. n_list)
 };
 
-// exp((l - m) / T) of a live token.
-FD_DEV double weight(const Row& r, uint32_t key) {
-  if (key == r.kmax) return 1.0;
+// exp((l - m) / T) = 2^(n / 64 + f) of a live token: 2^(n / 64) from the
+// table and the exponent, 2^f for |f| <= 1 / 128 by its Taylor polynomial in
+// f ln 2 (error below (ln 2 / 128)^6 / 720 = 4e-17).
+FD_DEV double weight(const Row& r, float l) {
+  if (l == r.m) return 1.0;
   if (r.m == INFINITY) return 0.0;
-  return exp(((double)key_logit(key) - (double)r.m) / r.temp);
+  const double y = ((double)l - r.md) * r.y;
+  if (!(y > -60.0)) return 0.0;
+  const double magic = 6755399441055744.0;   // 1.5 2^52: rounds 64 y to an integer
+  const double t = fma(y, 64.0, magic);
+  const int n = __double2loint(t);
+  const double f = fma(t - magic, -1.0 / 64.0, y) * 0.6931471805599453;
+  double p = fma(f, 1.0 / 120.0, 1.0 / 24.0);
+  p = fma(f, p, 1.0 / 6.0);
+  p = fma(f, p, 0.5);
+  p = fma(f, p, 1.0);
+  const double s = r.exp2_64[n & 63];
+  const double w = fma(f * p, s, s);
+  return w * __hiloint2double((1023 + (n >> 6)) << 20, 0);
 }
 FD_DEV u64 fixed(double w) { return __double2ull_rn(w * W_ONE); }
 
-// Place of a token among the bins; >= BINS: too light to be drawn.
-FD_DEV float z_of(const Row& r, uint32_t key) {
-  if (key == r.kmax) return 0.0f;
-  if (r.m == INFINITY) return (float)BINS;
-  return fminf(r.m - key_logit(key), 3.402823466e38f) * r.zs;
+// Place of a token among the bins; >= BINS: not live, or too light to be drawn.
+FD_DEV float z_of(const Row& r, float l) {
+  if (l == r.m) return 0.0f;
+  return l > -INFINITY ? fminf(r.m - l, F_MAX) * r.zs : (float)BINS;
+}
+FD_DEV bool below_cut(const Row& r, float l) { return r.has_cut && logit_key(l) <= r.cut_key; }
+
+// f(index, logit) for the slice's tokens, 16 bytes at a time.
+template <typename T, typename F>
+FD_DEV void for_slice(const T* x, int n, F f) {
+  constexpr int VEC = 16 / sizeof(T);
+  const uint4* v = reinterpret_cast<const uint4*>(x);
+  for (int i = threadIdx.x; i * VEC < n; i += ST) {
+    const uint4 u = v[i];
+    const T* e = reinterpret_cast<const T*>(&u);
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) f(i * VEC + j, to_f<T>(e[j]));
+  }
 }
 
 FD_DEV u64 warp_sum64(u64 v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+// Inclusive prefix sum over the threads; *total over all of them.
+FD_DEV u64 block_scan(u64 v, Shared& s, u64* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const u64 y = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += y;
+  }
+  __syncthreads();
+  if (lane == 31) s.red[warp] = v;
+  __syncthreads();
+  u64 t = 0;
+#pragma unroll
+  for (int i = 0; i < SW; ++i) {
+    const u64 x = s.red[i];
+    if (i < warp) v += x;
+    t += x;
+  }
+  *total = t;
   return v;
 }
 FD_DEV u64 block_sum(u64 v, Shared& s) {
@@ -129,22 +178,6 @@ FD_DEV u64 block_sum(u64 v, Shared& s) {
   for (int i = 0; i < SW; ++i) t += s.red[i];
   return t;
 }
-// Exclusive prefix sum over the threads.
-FD_DEV u64 block_scan(u64 v, Shared& s) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  u64 x = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const u64 y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
-  }
-  __syncthreads();
-  if (lane == 31) s.scan[warp] = x;
-  __syncthreads();
-  u64 before = 0;
-  for (int i = 0; i < warp; ++i) before += s.scan[i];
-  return before + x - v;
-}
 // Sum of v over the CTAs (v the same in all threads of a CTA), and over those
 // of lower rank.  Alternate `use`: a part is rewritten two uses later.
 FD_DEV u64 cluster_total(u64 v, Shared& s, int n_cta, int rank, int use, u64* lower) {
@@ -153,7 +186,7 @@ FD_DEV u64 cluster_total(u64 v, Shared& s, int n_cta, int rank, int use, u64* lo
   u64 t = 0, lo = 0;
 #pragma unroll
   for (int i = 0; i < MAX_CLUSTER; ++i) {
-    const u64 x = i < n_cta ? ld_remote(&s.part[use & 1], i) : 0;
+    const u64 x = i < n_cta ? ld_remote64(&s.part[use & 1], i) : 0;
     t += x;
     if (i < rank) lo += x;
   }
@@ -161,216 +194,323 @@ FD_DEV u64 cluster_total(u64 v, Shared& s, int n_cta, int rank, int use, u64* lo
   return t;
 }
 
-// Bins of all CTAs; the bin in which the running sum reaches `need` (set by
-// the caller from the sum of all bins) goes to s.bin, what is before it to
-// s.before.
+FD_DEV void zero_hist(Shared& s, int h) {
+  for (int i = threadIdx.x; i < 4 * BINS; i += ST) (&s.hist[h][0][0])[i] = 0;
+}
+template <bool MASS>
+FD_DEV void hist_add(Shared& s, int h, int bin, const Row& r, float l) {
+  if (MASS) {
+    const u64 w = fixed(weight(r, l));
+    if (w & 0x7fff) atomicAdd(&s.hist[h][0][bin], (uint32_t)w & 0x7fff);
+    if (w & 0x3fff8000) atomicAdd(&s.hist[h][1][bin], (uint32_t)(w >> 15) & 0x7fff);
+    if (w >> 30) atomicAdd(&s.hist[h][2][bin], (uint32_t)(w >> 30));
+  }
+  atomicAdd(&s.hist[h][3][bin], 1u);
+}
+
+// The bin in which the running sum over the bins of all CTAs (weights, or
+// counts) reaches `need` = need_of(sum of all bins) goes to s.bin, what lies
+// before it to s.before, the count up to its end to s.before_count.  *above:
+// the sum of all bins.
 template <bool MASS, typename F>
-FD_DEV u64 find_bin(Shared& s, int h, int n_cta, F need_of) {
-  u64 v = 0;
+FD_DEV u64 find_bin(Shared& s, int h, int n_cta, u64* above, F need_of) {
+  u64 v = 0, c = 0;
   if (threadIdx.x < BINS) {
 #pragma unroll
     for (int i = 0; i < MAX_CLUSTER; ++i) {
       if (i >= n_cta) continue;
+      c += ld_remote32(&s.hist[h][3][threadIdx.x], i);
       if (MASS)
-        v += (u64)ld_remote(&s.hist[h][0][threadIdx.x], i) +
-             ((u64)ld_remote(&s.hist[h][1][threadIdx.x], i) << 15) +
-             ((u64)ld_remote(&s.hist[h][2][threadIdx.x], i) << 30);
-      else
-        v += ld_remote(&s.hist[h][0][threadIdx.x], i);
+        v += (u64)ld_remote32(&s.hist[h][0][threadIdx.x], i) +
+             ((u64)ld_remote32(&s.hist[h][1][threadIdx.x], i) << 15) +
+             ((u64)ld_remote32(&s.hist[h][2][threadIdx.x], i) << 30);
     }
   }
-  const u64 total = block_sum(v, s);
+  u64 total_c, total = 0;
+  const u64 upto_c = block_scan(c, s, &total_c);
+  const u64 upto = MASS ? block_scan(v, s, &total) : upto_c;
+  if (!MASS) v = c, total = total_c;
+  *above = total;
   const u64 need = need_of(total);
-  const u64 before = block_scan(v, s);
-  if (threadIdx.x < BINS && before < need && need <= before + v) {
+  if (threadIdx.x < BINS && upto - v < need && need <= upto) {
     s.bin = threadIdx.x;
-    s.before = before;
+    s.before = upto - v;
+    s.before_count = upto_c;
   }
   __syncthreads();
   return need;
 }
 
-FD_DEV void zero_hist(Shared& s, int h) {
-  for (int i = threadIdx.x; i < 4 * BINS; i += ST) (&s.hist[h][0][0])[i] = 0;
-}
-
-template <bool MASS>
-FD_DEV void hist_add(Shared& s, int h, int bin, const Row& r, uint32_t key) {
-  if (MASS) {
-    const u64 w = fixed(weight(r, key));
-    if (w & 0x7fff) atomicAdd(&s.hist[h][0][bin], (uint32_t)w & 0x7fff);
-    if (w & 0x3fff8000) atomicAdd(&s.hist[h][1][bin], (uint32_t)(w >> 15) & 0x7fff);
-    if (w >> 30) atomicAdd(&s.hist[h][2][bin], (uint32_t)(w >> 30));
-  } else {
-    atomicAdd(&s.hist[h][0][bin], 1u);
-  }
-}
-
 // Sets the cut to the `ties`-th token (by id) of the class with key r.cut_key.
-template <typename K>
-FD_DEV void nth_tie(Shared& s, Row& r, int ties, K key_at, int n, int id0, int n_cta, int rank,
+template <typename T>
+FD_DEV void nth_tie(Shared& s, Row& r, int ties, const T* x, int n, int id0, int n_cta, int rank,
                     int& use) {
   r.ties = ties;
   if (r.listed) {
     for (int j = threadIdx.x; j < s.n_list; j += ST) {
-      if (s.all_key[j] != r.cut_key) continue;
+      if ((uint32_t)(s.all[j] >> 32) != r.cut_key) continue;
       int before = 0;
       for (int i = 0; i < s.n_list; ++i)
-        before += s.all_key[i] == r.cut_key && s.all_id[i] < s.all_id[j];
-      if (before == ties - 1) s.cut_id = s.all_id[j];
+        before += (uint32_t)(s.all[i] >> 32) == r.cut_key && s.all[i] > s.all[j];
+      if (before == ties - 1) s.cut_id = order_id(s.all[j]);
     }
     __syncthreads();
     r.cut_id = s.cut_id;
+    __syncthreads();
     return;
   }
+  const float lc = key_logit(r.cut_key);
   const int run = ((n + ST - 1) / ST) | 1;
   const int i0 = min((int)threadIdx.x * run, n), i1 = min(i0 + run, n);
-  u64 mine = 0, lower;
-  for (int i = i0; i < i1; ++i) mine += key_at(i) == r.cut_key;
-  const u64 cta = block_sum(mine, s);
+  u64 mine = 0, lower, cta;
+  for (int i = i0; i < i1; ++i) mine += to_f<T>(x[i]) == lc;
+  u64 before = block_scan(mine, s, &cta) - mine;
   cluster_total(cta, s, n_cta, rank, use++, &lower);
-  u64 before = lower + block_scan(mine, s);
+  before += lower;
   if (threadIdx.x == 0) s.cut_id = -1;
   __syncthreads();
   if (before < (u64)ties && (u64)ties <= before + mine)
     for (int i = i0; i < i1; ++i)
-      if (key_at(i) == r.cut_key && ++before == (u64)ties) s.cut_id = id0 + i;
+      if (to_f<T>(x[i]) == lc && ++before == (u64)ties) s.cut_id = id0 + i;
   __syncthreads();
   // the CTA that holds it tells the others (ids as id + 1, none = 0)
   r.cut_id = (int)cluster_total((u64)(s.cut_id + 1), s, n_cta, rank, use++, nullptr) - 1;
 }
 
-// Moves the cut to where the sum over the kept tokens, in order, reaches
-// `need` = need_of(sum of all kept).  MASS: weights, else counts (of tokens
-// that are not too light; no cut when need exceeds their number).
-template <bool MASS, typename K, typename F>
-FD_DEV void search(Shared& s, Row& r, K key_at, int n, int id0, int n_cta, int rank, int& use,
-                   F need_of) {
-  const int tid = threadIdx.x;
-  const u64 w_cut = r.has_cut && MASS ? fixed(weight(r, r.cut_key)) : 0;
-  const u64 at_cut = r.has_cut ? (u64)r.ties * w_cut : 0;
-  // strictly above the cut; its class is a sum of its own
-  for (int i = tid; i < n; i += ST) {
-    const uint32_t k = key_at(i);
-    if (k == KEY_NONE || (r.has_cut && k <= r.cut_key)) continue;
-    const float z = z_of(r, k);
-    if (z < (float)BINS) hist_add<MASS>(s, 0, (int)z, r, k);
-  }
+// First step of a search: the bin of z in which the sum over the kept tokens
+// reaches need_of(all of it).
+struct Level {
+  u64 need, above, before, upto_count;   // above: strictly above the cut
+  int bin;                               // valid if 0 < need <= above
+};
+template <bool MASS, typename T, typename F>
+FD_DEV Level level1(Shared& s, const Row& r, const T* x, int n, int n_cta, F need_of) {
+  const u64 at_cut = r.has_cut ? (u64)r.ties * (MASS ? fixed(weight(r, key_logit(r.cut_key))) : 1) : 0;
+  for_slice(x, n, [&](int, float l) {
+    const float z = z_of(r, l);
+    if (z < (float)BINS && !below_cut(r, l)) hist_add<MASS>(s, 0, (int)z, r, l);
+  });
   cluster_sync();
-  u64 above = 0;
-  const u64 need = find_bin<MASS>(s, 0, n_cta, [&](u64 t) { above = t; return need_of(t + at_cut); });
-  if (need == 0) {   // only the first token
-    r.cut_key = r.kmax;
-    r.cut_id = (int)~(uint32_t)s.best;
-    r.ties = 1;
-    r.has_cut = true;
-    r.listed = false;
-  } else if (need > above) {
-    if (r.has_cut) {
-      const u64 t = w_cut ? (need - above + w_cut - 1) / w_cut : r.ties;
-      if (t < (u64)r.ties) nth_tie(s, r, (int)t, key_at, n, id0, n_cta, rank, use);
+  Level v;
+  v.need = find_bin<MASS>(s, 0, n_cta, &v.above, [&](u64 t) { return need_of(t + at_cut); });
+  v.bin = s.bin;
+  v.before = s.before;
+  v.upto_count = s.before_count;
+  return v;
+}
+
+// Moves the cut to the token at which the sum reaches v.need.
+template <bool MASS, typename T>
+FD_DEV void refine(Shared& s, Row& r, const Level& v, const T* x, int n, int id0, int n_cta,
+                   int rank, int& use) {
+  const int tid = threadIdx.x;
+  auto unit = [&](float l) { return MASS ? fixed(weight(r, l)) : (u64)1; };
+  if (v.need == 0 || v.need > v.above) {
+    const bool first = v.need == 0;   // only the first token
+    int ties = 1;
+    if (!first && r.has_cut) {
+      const u64 w = unit(key_logit(r.cut_key));
+      ties = w ? (int)min((v.need - v.above + w - 1) / w, (u64)r.ties) : r.ties;
     }
-  } else {
-    const int b1 = s.bin;
-    const u64 before1 = s.before;
-    const float lo1 = (float)b1;
-    __syncthreads();
-    for (int i = tid; i < n; i += ST) {
-      const uint32_t k = key_at(i);
-      if (k == KEY_NONE || (r.has_cut && k <= r.cut_key)) continue;
-      const float z = z_of(r, k) - lo1;
-      if (z >= 0.0f && z < 1.0f) hist_add<MASS>(s, 1, (int)(z * BINS), r, k);
-    }
+    // the first histogram is free again once every CTA has read it
     cluster_sync();
-    zero_hist(s, 0);   // every CTA has read it
-    find_bin<MASS>(s, 1, n_cta, [&](u64) { return need - before1; });
-    const int b2 = s.bin;
-    const u64 before2 = before1 + s.before;
-    if (tid == 0) s.n_list = 0;
+    zero_hist(s, 0);
     __syncthreads();
-    auto in_bin = [&](uint32_t k) {
-      if (k == KEY_NONE || (r.has_cut && k <= r.cut_key)) return false;
-      const float z = z_of(r, k) - lo1;
-      return z >= 0.0f && z < 1.0f && (int)(z * BINS) == b2;
-    };
-    for (int i = tid; i < n; i += ST) {
-      const uint32_t k = key_at(i);
-      if (in_bin(k)) {
-        const int at = atomicAdd(&s.n_list, 1);
-        if (at < CAP) {
-          s.list_key[at] = k;
-          s.list_id[at] = id0 + i;
-        }
-      }
-    }
-    cluster_sync();
-    zero_hist(s, 1);
-    int n_all = 0;
-    for (int c = 0; c < n_cta; ++c) {
-      const int nc = ld_remote(&s.n_list, c);
-      if (n_all + nc <= CAP)
-        for (int j = tid; j < nc; j += ST) {
-          const uint32_t k = ld_remote(&s.list_key[j], c);
-          s.all_key[n_all + j] = k;
-          s.all_id[n_all + j] = ld_remote(&s.list_id[j], c);
-          s.all_w[n_all + j] = MASS ? fixed(weight(r, k)) : 1;
-        }
-      n_all += nc;
-    }
-    if (n_all <= CAP) {
-      __syncthreads();
-      for (int j = tid; j < n_all; j += ST) {
-        const uint32_t kj = s.all_key[j];
-        const int idj = s.all_id[j];
-        u64 before = before2;
-        int ties = 1;
-        for (int i = 0; i < n_all; ++i) {
-          const bool tie = s.all_key[i] == kj && s.all_id[i] < idj;
-          ties += tie;
-          if (tie || s.all_key[i] > kj) before += s.all_w[i];
-        }
-        if (before < need && need <= before + s.all_w[j]) {
-          s.cut_key = kj;
-          s.cut_id = idj;
-          s.cut_ties = ties;
-        }
-      }
-      __syncthreads();
-      r.cut_key = s.cut_key;
-      r.cut_id = s.cut_id;
-      r.ties = s.cut_ties;
-      r.has_cut = r.listed = true;
-      cluster_sync();   // every CTA has read the lists' lengths
-      if (tid == 0) s.n_list = n_all;
-      __syncthreads();
-    } else {
-      // too many: bisect over the keys for the largest one that reaches need
-      uint32_t lo = r.has_cut ? r.cut_key + 1 : 1, hi = r.kmax;
-      auto upto = [&](uint32_t k0) {   // sum over the bin's tokens with key >= k0
-        u64 v = 0;
-        for (int i = tid; i < n; i += ST) {
-          const uint32_t k = key_at(i);
-          if (k >= k0 && in_bin(k)) v += MASS ? fixed(weight(r, k)) : 1;
-        }
-        return before2 + cluster_total(block_sum(v, s), s, n_cta, rank, use++, nullptr);
-      };
-      while (lo < hi) {
-        const uint32_t mid = lo + (hi - lo) / 2 + 1;
-        if (upto(mid) >= need) lo = mid; else hi = mid - 1;
-      }
-      const u64 over = lo == r.kmax ? before2 : upto(lo + 1);
-      const u64 w = MASS ? fixed(weight(r, lo)) : 1;
-      r.cut_key = lo;
+    if (first) {
+      r.cut_key = logit_key(r.m);
       r.has_cut = true;
       r.listed = false;
-      nth_tie(s, r, (int)((need - over + w - 1) / w), key_at, n, id0, n_cta, rank, use);
+      nth_tie(s, r, 1, x, n, id0, n_cta, rank, use);
+    } else if (r.has_cut && ties < r.ties) {
+      nth_tie(s, r, ties, x, n, id0, n_cta, rank, use);
     }
     return;
   }
-  // the first histogram is free again once every CTA has read it
+  const float lo = (float)v.bin;
+  for_slice(x, n, [&](int, float l) {
+    const float z = z_of(r, l) - lo;
+    if (z >= 0.0f && z < 1.0f && !below_cut(r, l)) hist_add<MASS>(s, 1, (int)(z * BINS), r, l);
+  });
   cluster_sync();
-  zero_hist(s, 0);
+  zero_hist(s, 0);   // every CTA has read it
+  u64 total;
+  find_bin<MASS>(s, 1, n_cta, &total, [&](u64) { return v.need - v.before; });
+  const int b2 = s.bin;
+  const u64 before = v.before + s.before;
+  if (tid == 0) s.n_list = 0;
   __syncthreads();
+  auto in_bin = [&](float l) {
+    const float z = z_of(r, l) - lo;
+    return z >= 0.0f && z < 1.0f && (int)(z * BINS) == b2 && !below_cut(r, l);
+  };
+  for_slice(x, n, [&](int i, float l) {
+    if (in_bin(l)) {
+      const int at = atomicAdd(&s.n_list, 1);
+      if (at < CAP) s.list[at] = order_of(l, id0 + i);
+    }
+  });
+  cluster_sync();
+  zero_hist(s, 1);
+  int n_all = 0;
+  for (int c = 0; c < n_cta; ++c) {
+    const int nc = ld_remote32(&s.n_list, c);
+    if (n_all + nc <= CAP)
+      for (int j = tid; j < nc; j += ST) {
+        const u64 o = ld_remote64(&s.list[j], c);
+        s.all[n_all + j] = o;
+        s.w[n_all + j] = unit(order_logit(o));
+      }
+    n_all += nc;
+  }
+  cluster_sync();   // every CTA has read the lists and their lengths
+  if (n_all <= CAP) {
+    for (int j = tid; j < n_all; j += ST) {
+      const u64 o = s.all[j];
+      u64 sum = before;
+      int ties = 1;
+      for (int i = 0; i < n_all; ++i) {
+        const bool over = s.all[i] > o;
+        if (over) sum += s.w[i];
+        ties += over && (s.all[i] >> 32) == (o >> 32);
+      }
+      if (sum < v.need && v.need <= sum + s.w[j]) {
+        s.cut_key = (uint32_t)(o >> 32);
+        s.cut_id = order_id(o);
+        s.cut_ties = ties;
+      }
+    }
+    if (tid == 0) s.n_list = n_all;
+    __syncthreads();
+    r.cut_key = s.cut_key;
+    r.cut_id = s.cut_id;
+    r.ties = s.cut_ties;
+    r.has_cut = r.listed = true;
+    __syncthreads();
+    return;
+  }
+  // too many: bisect over the keys for the largest one that reaches need
+  uint32_t k0 = r.has_cut ? r.cut_key + 1 : 1, k1 = logit_key(r.m);
+  const uint32_t kmax = k1;
+  auto upto = [&](uint32_t k) {   // sum up to and over the bin's tokens with key >= k
+    u64 t = 0;
+    for_slice(x, n, [&](int, float l) {
+      if (in_bin(l) && logit_key(l) >= k) t += unit(l);
+    });
+    return before + cluster_total(block_sum(t, s), s, n_cta, rank, use++, nullptr);
+  };
+  while (k0 < k1) {
+    const uint32_t mid = k0 + (k1 - k0) / 2 + 1;
+    if (upto(mid) >= v.need) k0 = mid; else k1 = mid - 1;
+  }
+  const u64 over = k0 == kmax ? before : upto(k0 + 1);
+  const u64 w = unit(key_logit(k0));
+  r.cut_key = k0;
+  r.has_cut = true;
+  r.listed = false;
+  nth_tie(s, r, (int)((v.need - over + w - 1) / w), x, n, id0, n_cta, rank, use);
+}
+
+// Sorts a[0 .. n) (n a power of two, at most 2 ST), largest first.
+FD_DEV void sort_desc(u64* a, int n) {
+  for (int size = 2; size <= n; size *= 2)
+    for (int d = size / 2; d > 0; d /= 2) {
+      // pairs of a distance up to 32 stay in the 64 elements of a warp
+      if (d >= 32) __syncthreads(); else __syncwarp();
+      const int p = threadIdx.x;
+      if (p < n / 2) {
+        const int i = 2 * d * (p / d) + p % d;
+        const u64 u = a[i], v = a[i + d];
+        const bool down = (i & size) == 0;
+        if ((u < v) == down) {
+          a[i] = v;
+          a[i + d] = u;
+        }
+      }
+      if (d >= 32) __syncthreads();
+    }
+  __syncthreads();
+}
+
+struct Filters {
+  int top_k;
+  double top_p, min_p;
+  bool greedy;
+};
+
+// The filters and the draw on s.all[0 .. n), by one CTA: all tokens down to
+// some place of the order behind the last kept one, and, unless top-p's goal
+// `need` is given (not 0), behind the last one that top-k keeps.
+FD_DEV void draw_sorted(Shared& s, const Row& r, const Filters& f, int n, u64 need, double u,
+                        int32_t* tok, float* prob) {
+  const int tid = threadIdx.x;
+  int size = 64;
+  while (size < n) size *= 2;
+  for (int i = n + tid; i < size; i += ST) s.all[i] = 0;
+  __syncthreads();
+  sort_desc(s.all, size);
+  if (f.top_k > 0) n = min(n, f.top_k);
+  // thread t takes tokens 2t and 2t + 1 of the order
+  u64 w[2], total;
+  double wd[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int i = 2 * tid + j;
+    wd[j] = i < n ? weight(r, order_logit(s.all[i])) : 0.0;
+    w[j] = fixed(wd[j]);
+  }
+  u64 upto = block_scan(w[0] + w[1], s, &total);
+  if (!(f.top_p >= 1.0)) {
+    // kept while the weight before is below top_p total
+    if (need == 0) need = (u64)ceil(fmax(f.top_p * (double)total, 0.0));
+    const u64 b1 = upto - w[1], b0 = b1 - w[0];
+    if (2 * tid > 0 && b0 >= need) w[0] = 0;
+    if (b1 >= need) w[1] = 0;
+  }
+  if (f.min_p > 0.0) {
+    if (wd[0] < f.min_p) w[0] = 0;
+    if (wd[1] < f.min_p) w[1] = 0;
+  }
+  const u64 all = block_sum(w[0] + w[1], s);
+  if (f.greedy) {
+    if (tid == 0) {
+      *tok = order_id(s.all[0]);
+      if (prob) *prob = (float)(W_ONE / (double)all);
+    }
+    return;
+  }
+  // the kept ones by rising id (those without weight last); the low word finds the weight again
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int i = 2 * tid + j;
+    if (i < size) {
+      s.list[i] = w[j] ? ((u64)(uint32_t)~(uint32_t)order_id(s.all[i]) << 32) | (uint32_t)i : 0;
+      s.w[i] = w[j];
+    }
+  }
+  const int kept = __syncthreads_count(w[0] > 0) + __syncthreads_count(w[1] > 0);
+  if (kept < size) {   // kept tokens are a prefix of the order: sort no more than them
+    int small = 64;
+    while (small < kept) small *= 2;
+    size = small;
+  }
+  sort_desc(s.list, size);
+  u64 v[2] = {0, 0};
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+    if (2 * tid + j < size && s.list[2 * tid + j]) v[j] = s.w[(uint32_t)s.list[2 * tid + j]];
+  upto = block_scan(v[0] + v[1], s, &total);
+  const u64 target = min((u64)(fmax(u, 0.0) * (double)all), all - 1);
+  const u64 b0 = upto - v[1] - v[0], b1 = upto - v[1];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const u64 lo = j ? b1 : b0;
+    if (lo <= target && target < lo + v[j]) {
+      const u64 e = s.list[2 * tid + j];
+      *tok = (int)~(uint32_t)(e >> 32);
+      if (prob)
+        *prob = (float)(weight(r, order_logit(s.all[(uint32_t)e])) / ((double)all / W_ONE));
+    }
+  }
 }
 
 template <typename T>
@@ -378,99 +518,185 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const fdllm_sample_args a
   extern __shared__ __align__(16) uint8_t smem[];
   Shared& s = *reinterpret_cast<Shared*>(smem);
   T* x = reinterpret_cast<T*>(smem + sizeof(Shared));
+  static_assert(sizeof(Shared) % 16 == 0, "the slice is read 16 bytes at a time");
   const int tid = threadIdx.x, row = blockIdx.x / n_cta, rank = blockIdx.x % n_cta;
   const int id0 = rank * slice, n = max(0, min(slice, a.vocab - id0));
   const T* src = reinterpret_cast<const T*>(a.logits) + (int64_t)row * a.row_stride + id0;
-  const int mask = a.mask_id - id0;
-  auto key_at = [&](int i) { return i == mask ? KEY_NONE : logit_key(to_f<T>(x[i])); };
   int use = 0;
 
-  // ---- the slice, and the row's largest logit
+  // ---- the slice (the masked token and the last vector's rest as -inf), and
+  // every thread's largest logit
   constexpr int VEC = 16 / sizeof(T);
-  u64 best = 0;
-  auto see = [&](int i, T v) {
-    x[i] = v;
-    const uint32_t k = i == mask ? KEY_NONE : logit_key(to_f<T>(v));
-    const u64 c = ((u64)k << 32) | (uint32_t)~(uint32_t)(id0 + i);   // equal keys: the lowest id
-    if (k != KEY_NONE && c > best) best = c;
-  };
-  if ((reinterpret_cast<uintptr_t>(src) & 15) == 0) {
-    const int nv = n / VEC;
+  const T none = from_f<T>(-INFINITY);
+  float top = -INFINITY;
+  {
+    const bool wide = (reinterpret_cast<uintptr_t>(src) & 15) == 0;
+    const int mask = a.mask_id - id0, nv = (n + VEC - 1) / VEC;
+    uint4* xv = reinterpret_cast<uint4*>(x);
 #pragma unroll 4
     for (int i = tid; i < nv; i += ST) {
-      const uint4 v = __ldcs(reinterpret_cast<const uint4*>(src) + i);
-      const T* e = reinterpret_cast<const T*>(&v);
+      uint4 u;
+      T* e = reinterpret_cast<T*>(&u);
+      if (wide && (i + 1) * VEC <= n) {
+        u = __ldcs(reinterpret_cast<const uint4*>(src) + i);
+      } else {
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) see(i * VEC + j, e[j]);
+        for (int j = 0; j < VEC; ++j) e[j] = i * VEC + j < n ? src[i * VEC + j] : none;
+      }
+      if (mask >= i * VEC && mask < (i + 1) * VEC) {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j)
+          if (i * VEC + j == mask) e[j] = none;
+      }
+      xv[i] = u;
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) top = fmaxf(top, to_f<T>(e[j]));   // NaN never wins
     }
-    for (int i = nv * VEC + tid; i < n; i += ST) see(i, src[i]);
-  } else {
-    for (int i = tid; i < n; i += ST) see(i, src[i]);
   }
   zero_hist(s, 0);
   zero_hist(s, 1);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
-  if ((tid & 31) == 0) s.red[tid >> 5] = best;
+  if (tid < 64) s.exp2_64[tid] = exp2((double)tid / 64.0);
+  if (tid == 0) s.n_list = 0;
+  {
+    const float w = warp_max(top);
+    if ((tid & 31) == 0) s.red[tid >> 5] = __float_as_uint(w);
+  }
   __syncthreads();
+  if (tid == 0) {
+    float t = -INFINITY;
 #pragma unroll
-  for (int i = 0; i < SW; ++i) best = max(best, s.red[i]);
-  if (tid == 0) s.part[1] = best;
+    for (int i = 0; i < SW; ++i) t = fmaxf(t, __uint_as_float((uint32_t)s.red[i]));
+    s.top = t;
+  }
   cluster_sync();
-  for (int i = 0; i < n_cta; ++i) best = max(best, ld_remote(&s.part[1], i));
-  if (tid == 0) s.best = best;
-  __syncthreads();
-
   Row r{};
-  r.kmax = (uint32_t)(best >> 32);
-  bool done = false;
-  if (r.kmax == KEY_NONE) {
+  r.m = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < MAX_CLUSTER; ++i)
+    if (i < n_cta) r.m = fmaxf(r.m, __uint_as_float(ld_remote32(&s.top, i)));
+
+  if (r.m == -INFINITY) {
     if (rank == 0 && tid == 0) {
       a.tok[row] = -1;
       if (a.prob) a.prob[row] = 0.0f;
     }
-    done = true;
-  }
-  if (!done) {
-    r.m = key_logit(r.kmax);
-    r.temp = a.temperature ? (double)a.temperature[row] : 1.0;
-    const bool greedy = !(r.temp > 0.0);
-    if (greedy) r.temp = 1.0;
-    r.zs = (float)fmin((double)Z_BINS / r.temp, 1e30);
-    const int top_k = a.top_k ? a.top_k[row] : 0;
-    const double top_p = a.top_p ? (double)a.top_p[row] : 1.0;
-    const double min_p = a.min_p ? fmin((double)a.min_p[row], 1.0) : 0.0;
-    if (top_k > 0)
-      search<false>(s, r, key_at, n, id0, n_cta, rank, use, [&](u64) { return (u64)top_k; });
-    if (!(top_p >= 1.0))
-      search<true>(s, r, key_at, n, id0, n_cta, rank, use,
-                   [&](u64 t) { return (u64)ceil(fmax(top_p * (double)t, 0.0)); });
+  } else {
+    Filters f;
+    double temp = a.temperature ? (double)a.temperature[row] : 1.0;
+    f.greedy = !(temp > 0.0);
+    if (f.greedy) temp = 1.0;
+    f.top_k = a.top_k ? max(a.top_k[row], 0) : 0;
+    f.top_p = a.top_p ? (double)a.top_p[row] : 1.0;
+    f.min_p = a.min_p ? fmin((double)a.min_p[row], 1.0) : 0.0;
+    const bool has_p = !(f.top_p >= 1.0);
+    const double u = a.u[row];
+    r.md = r.m;
+    r.y = 1.4426950408889634 / temp;
+    r.zs = (float)fmin((double)Z_BINS / temp, 1e30);
+    r.exp2_64 = s.exp2_64;
+    auto need_p = [&](u64 t) { return (u64)ceil(fmax(f.top_p * (double)t, 0.0)); };
 
-    // ---- the draw: every thread takes a run of ids (odd: no bank conflicts)
-    const int run = ((n + ST - 1) / ST) | 1;
-    const int i0 = min(tid * run, n), i1 = min(i0 + run, n);
-    auto kept_w = [&](int i) {
-      const uint32_t k = key_at(i);
-      if (k == KEY_NONE || (r.has_cut && (k < r.cut_key || (k == r.cut_key && id0 + i > r.cut_id))))
-        return (u64)0;
-      if (!(z_of(r, k) < (float)BINS)) return (u64)0;
-      const double w = weight(r, k);
-      return min_p > 0.0 && w < min_p ? (u64)0 : fixed(w);
-    };
-    u64 sum = 0, lower;
-    for (int i = i0; i < i1; ++i) sum += kept_w(i);
-    const u64 mine = block_sum(sum, s);
-    const u64 all = cluster_total(mine, s, n_cta, rank, use++, &lower);
-    if (greedy) {
-      if (rank == 0 && tid == 0) {
-        a.tok[row] = (int)~(uint32_t)s.best;
-        if (a.prob) a.prob[row] = (float)(W_ONE / (double)all);
+    // ---- a bound on the kept tokens' z
+    float z_end = (float)BINS;
+    bool gather = a.vocab <= CAP;
+    Level lp{};
+    if (f.min_p > 0.0 && !(has_p && f.top_k > 0)) {   // top-p's goal counts what top-k keeps
+      z_end = fminf(z_end, (float)(-log(f.min_p)) * (Z_BINS * 1.00001f) + 0.001f);
+      gather = true;
+    }
+    if (a.vocab <= CAP) {
+      if (has_p) z_end = (float)BINS;
+    } else if (f.top_k > 0 && f.top_k <= ST * n_cta / 2) {
+      const float z = z_of(r, top);
+      if (z < (float)BINS) atomicAdd(&s.hist[0][3][(int)z], 1u);
+      cluster_sync();
+      u64 above;
+      const u64 need = find_bin<false>(s, 0, n_cta, &above, [&](u64) { return (u64)f.top_k; });
+      if (need <= above) {
+        z_end = fminf(z_end, (float)(s.bin + 1));
+        gather = true;
       }
-    } else {
-      // first id whose running sum passes u all: integers, so passes its floor
-      const u64 target = min((u64)(fmax(a.u[row], 0.0) * (double)all), all - 1);
-      if (lower <= target && target < lower + mine) {
-        u64 before = lower + block_scan(sum, s);
+      cluster_sync();   // every CTA has read the histogram
+      zero_hist(s, 0);
+    } else if (f.top_k == 0 && has_p) {
+      lp = level1<true>(s, r, x, n, n_cta, need_p);
+      if (lp.need > 0 && lp.need <= lp.above) {
+        gather |= lp.upto_count <= CAP;
+        z_end = fminf(z_end, (float)(lp.bin + 1));
+      } else {
+        gather = false;
+      }
+    }
+    // ---- the tokens within the bound, if they are few
+    bool drawn = false;
+    if (gather) {
+      __syncthreads();
+      for_slice(x, n, [&](int i, float l) {
+        if (z_of(r, l) < z_end) {
+          const int at = atomicAdd(&s.n_list, 1);
+          if (at < CAP) s.list[at] = order_of(l, id0 + i);
+        }
+      });
+      cluster_sync();
+      int n_all = 0;
+      for (int c = 0; c < n_cta; ++c) {
+        const int nc = ld_remote32(&s.n_list, c);
+        if (rank == 0 && n_all + nc <= CAP)
+          for (int j = tid; j < nc; j += ST) s.all[n_all + j] = ld_remote64(&s.list[j], c);
+        n_all += nc;
+      }
+      drawn = n_all <= CAP;
+      if (drawn) {
+        if (rank == 0) draw_sorted(s, r, f, n_all, lp.need, u, a.tok + row, a.prob ? a.prob + row : nullptr);
+      } else {
+        cluster_sync();   // every CTA has read the lists' lengths
+      }
+    }
+    if (!drawn) {
+      if (f.top_k > 0) {
+        __syncthreads();
+        const Level v = level1<false>(s, r, x, n, n_cta, [&](u64) { return (u64)f.top_k; });
+        refine<false>(s, r, v, x, n, id0, n_cta, rank, use);
+        if (has_p) lp = level1<true>(s, r, x, n, n_cta, need_p);
+      }
+      if (has_p) refine<true>(s, r, lp, x, n, id0, n_cta, rank, use);
+
+      // ---- the draw: every thread takes a run of ids (odd: no bank conflicts)
+      const int run = ((n + ST - 1) / ST) | 1;
+      const int i0 = min(tid * run, n), i1 = min(i0 + run, n);
+      auto kept_w = [&](int i) {
+        const float l = to_f<T>(x[i]);
+        if (!(z_of(r, l) < z_end)) return (u64)0;
+        if (r.has_cut) {
+          const uint32_t k = logit_key(l);
+          if (k < r.cut_key || (k == r.cut_key && id0 + i > r.cut_id)) return (u64)0;
+        }
+        const double w = weight(r, l);
+        return f.min_p > 0.0 && w < f.min_p ? (u64)0 : fixed(w);
+      };
+      u64 sum = 0, lower, mine;
+      int first = 0x7fffffff;
+      for (int i = i0; i < i1; ++i) {
+        sum += kept_w(i);
+        if (f.greedy && first == 0x7fffffff && to_f<T>(x[i]) == r.m) first = id0 + i;
+      }
+      u64 before = block_scan(sum, s, &mine) - sum;
+      const u64 all = cluster_total(mine, s, n_cta, rank, use++, &lower);
+      if (f.greedy) {
+        if (tid == 0) s.pick = 0x7fffffff;
+        __syncthreads();
+        atomicMin(&s.pick, first);
+        cluster_sync();
+        if (rank == 0 && tid == 0) {
+          int t = 0x7fffffff;
+          for (int c = 0; c < n_cta; ++c) t = min(t, (int)ld_remote32(&s.pick, c));
+          a.tok[row] = t;
+          if (a.prob) a.prob[row] = (float)(W_ONE / (double)all);
+        }
+      } else {
+        // first id whose running sum passes u all: integers, so passes its floor
+        const u64 target = min((u64)(fmax(u, 0.0) * (double)all), all - 1);
+        before += lower;
         if (before <= target && target < before + sum) {
           int i = i0;
           for (;; ++i) {
@@ -478,7 +704,7 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const fdllm_sample_args a
             if (before > target) break;
           }
           a.tok[row] = id0 + i;
-          if (a.prob) a.prob[row] = (float)(weight(r, key_at(i)) / ((double)all / W_ONE));
+          if (a.prob) a.prob[row] = (float)(weight(r, to_f<T>(x[i])) / ((double)all / W_ONE));
         }
       }
     }
