@@ -44,6 +44,7 @@ constexpr int SLICE_BYTES = 78 << 10;        // two CTAs and their lists fit on 
 constexpr int BINS = 256;
 constexpr float Z_BINS = 8.0f;               // bins per unit of z: 256 / 32
 constexpr int CAP = 1024;                    // tokens that are gathered and sorted
+constexpr int DIRECT = 192;                  // tokens whose order is taken by counting
 constexpr double W_ONE = 17592186044416.0;   // 2^44
 constexpr float F_MAX = 3.402823466e38f;
 
@@ -62,19 +63,40 @@ FD_DEV u64 order_of(float l, int id) { return ((u64)logit_key(l) << 32) | (uint3
 FD_DEV float order_logit(u64 o) { return key_logit((uint32_t)(o >> 32)); }
 FD_DEV int order_id(u64 o) { return (int)~(uint32_t)o; }
 
-struct Shared {
+struct __align__(16) Shared {
   double exp2_64[64];          // 2^(j / 64)
   uint32_t hist[2][4][BINS];   // weights in words of 15, 15 and 15 bits; counts
   u64 red[SW];
   u64 part[2];                 // this CTA's share of a cluster sum (by parity of use)
   u64 before, before_count;
   float top;                   // this CTA's largest logit
-  int bin, n_list, cut_id, cut_ties, pick;
+  int bin, n_list, n_sub, cut_id, cut_ties, pick;
+  int run0, run1;              // the run of ids that holds the drawn token
   uint32_t cut_key;
   u64 list[CAP];               // this CTA's gathered tokens (order_of)
   u64 all[CAP];                // the cluster's
-  u64 w[CAP];                  // their weights, or running sums
+  u64 w[CAP];                  // their weights
+  u64 sub[CAP];                // this CTA's tokens of the smaller bin
 };
+
+// 2^(j / 64)
+__device__ const double EXP2_64[64] = {
+    1.0, 1.0108892860517005, 1.0218971486541166, 1.0330248790212284,
+    1.0442737824274138, 1.0556451783605572, 1.0671404006768237, 1.0787607977571199,
+    1.0905077326652577, 1.102382583307841, 1.1143867425958924, 1.1265216186082418,
+    1.1387886347566916, 1.1511892299529827, 1.1637248587775775, 1.1763969916502812,
+    1.189207115002721, 1.202156731452703, 1.215247359980469, 1.22848053610687,
+    1.241857812073484, 1.255380757024691, 1.2690509571917332, 1.2828700160787783,
+    1.2968395546510096, 1.3109612115247644, 1.3252366431597413, 1.339667524053303,
+    1.3542555469368927, 1.3690024229745905, 1.383909881963832, 1.3989796725383112,
+    1.4142135623730951, 1.42961333839197, 1.4451808069770467, 1.460917794180647,
+    1.4768261459394993, 1.4929077282912648, 1.5091644275934228, 1.5255981507445384,
+    1.5422108254079407, 1.559004400237837, 1.5759808451078865, 1.593142151342267,
+    1.6104903319492543, 1.6280274218573478, 1.645755478153965, 1.6636765803267364,
+    1.681792830507429, 1.7001063537185235, 1.718619298122478, 1.7373338352737062,
+    1.7562521603732995, 1.7753764925265212, 1.7947090750031072, 1.8142521755003989,
+    1.8340080864093424, 1.8539791250833855, 1.8741676341103, 1.8945759815869656,
+    1.9152065613971474, 1.9360617934922943, 1.9571441241754002, 1.978456026387951};
 
 FD_DEV uint32_t ld_remote32(const void* p, uint32_t rank) {
   uint32_t v;
@@ -91,7 +113,7 @@ FD_DEV u64 ld_remote64(const void* p, uint32_t rank) {
 struct Row {
   float m;          // largest logit
   float zs;         // bins per unit of logit
-  double md, y;     // m; log2(e) / T
+  double md, y;     // m; 64 log2(e) / T
   const double* exp2_64;
   // the cut: kept are key > cut_key, and key == cut_key with id <= cut_id
   uint32_t cut_key;
@@ -100,27 +122,30 @@ struct Row {
   bool has_cut, listed;   // listed: the class of cut_key is in Shared::all[0 .. n_list)
 };
 
-// exp((l - m) / T) = 2^(n / 64 + f) of a live token: 2^(n / 64) from the
-// table and the exponent, 2^f for |f| <= 1 / 128 by its Taylor polynomial in
-// f ln 2 (error below (ln 2 / 128)^6 / 720 = 4e-17).
+// exp((l - m) / T) of a live token = 2^((n + f) / 64): 2^(n / 64) from the
+// table and the exponent, 2^(f / 64), |f| <= 1/2, by its Taylor polynomial
+// (error below (ln 2 / 128)^5 / 120 = 4e-14).  No branch but the common
+// case's, so that the chains of several tokens overlap.
 FD_DEV double weight(const Row& r, float l) {
-  if (l == r.m) return 1.0;
-  if (r.m == INFINITY) return 0.0;
-  const double y = ((double)l - r.md) * r.y;
-  if (!(y > -60.0)) return 0.0;
-  const double magic = 6755399441055744.0;   // 1.5 2^52: rounds 64 y to an integer
-  const double t = fma(y, 64.0, magic);
+  const double y = ((double)l - r.md) * r.y;   // 64 log2 of the weight
+  const double magic = 6755399441055744.0;     // 1.5 2^52: its sum with y is an integer
+  const double t = y + magic;
   const int n = __double2loint(t);
-  const double f = fma(t - magic, -1.0 / 64.0, y) * 0.6931471805599453;
-  double p = fma(f, 1.0 / 120.0, 1.0 / 24.0);
-  p = fma(f, p, 1.0 / 6.0);
-  p = fma(f, p, 0.5);
-  p = fma(f, p, 1.0);
+  const double f = y - (t - magic);
+  constexpr double c = 0.010830424696249145;   // ln 2 / 64
+  double p = fma(f, c * c * c * c / 24.0, c * c * c / 6.0);
+  p = fma(f, p, c * c / 2.0);
+  p = fma(f, p, c);
   const double s = r.exp2_64[n & 63];
-  const double w = fma(f * p, s, s);
-  return w * __hiloint2double((1023 + (n >> 6)) << 20, 0);
+  double w = fma(f * p, s, s);
+  w = __hiloint2double(__double2hiint(w) + ((n >> 6) << 20), __double2loint(w));
+  if (!(y > -4096.0)) w = 0.0;                 // below 2^-64; NaN where +inf meets a finite logit
+  return l == r.m ? 1.0 : w;
 }
-FD_DEV u64 fixed(double w) { return __double2ull_rn(w * W_ONE); }
+// rint(w 2^44): the sum with 2^52 is an integer in the low bits.
+FD_DEV u64 fixed(double w) {
+  return (u64)__double_as_longlong(fma(w, W_ONE, 4503599627370496.0)) & 0xfffffffffffffull;
+}
 
 // Place of a token among the bins; >= BINS: not live, or too light to be drawn.
 FD_DEV float z_of(const Row& r, float l) {
@@ -129,17 +154,27 @@ FD_DEV float z_of(const Row& r, float l) {
 }
 FD_DEV bool below_cut(const Row& r, float l) { return r.has_cut && logit_key(l) <= r.cut_key; }
 
-// f(index, logit) for the slice's tokens, 16 bytes at a time.
+// f(index, logits) for the slice's tokens, 16 bytes at a time.
 template <typename T, typename F>
-FD_DEV void for_slice(const T* x, int n, F f) {
+FD_DEV void for_vectors(const T* x, int n, F f) {
   constexpr int VEC = 16 / sizeof(T);
   const uint4* v = reinterpret_cast<const uint4*>(x);
   for (int i = threadIdx.x; i * VEC < n; i += ST) {
     const uint4 u = v[i];
     const T* e = reinterpret_cast<const T*>(&u);
+    float l[VEC];
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) f(i * VEC + j, to_f<T>(e[j]));
+    for (int j = 0; j < VEC; ++j) l[j] = to_f<T>(e[j]);
+    f(i * VEC, l);
   }
+}
+// f(index, logit), one token after the other.
+template <typename T, typename F>
+FD_DEV void for_slice(const T* x, int n, F f) {
+  for_vectors(x, n, [&](int i, const float* l) {
+#pragma unroll
+    for (int j = 0; j < 16 / (int)sizeof(T); ++j) f(i + j, l[j]);
+  });
 }
 
 FD_DEV u64 warp_sum64(u64 v) {
@@ -198,9 +233,8 @@ FD_DEV void zero_hist(Shared& s, int h) {
   for (int i = threadIdx.x; i < 4 * BINS; i += ST) (&s.hist[h][0][0])[i] = 0;
 }
 template <bool MASS>
-FD_DEV void hist_add(Shared& s, int h, int bin, const Row& r, float l) {
+FD_DEV void hist_add(Shared& s, int h, int bin, u64 w) {
   if (MASS) {
-    const u64 w = fixed(weight(r, l));
     if (w & 0x7fff) atomicAdd(&s.hist[h][0][bin], (uint32_t)w & 0x7fff);
     if (w & 0x3fff8000) atomicAdd(&s.hist[h][1][bin], (uint32_t)(w >> 15) & 0x7fff);
     if (w >> 30) atomicAdd(&s.hist[h][2][bin], (uint32_t)(w >> 30));
@@ -286,9 +320,18 @@ struct Level {
 template <bool MASS, typename T, typename F>
 FD_DEV Level level1(Shared& s, const Row& r, const T* x, int n, int n_cta, F need_of) {
   const u64 at_cut = r.has_cut ? (u64)r.ties * (MASS ? fixed(weight(r, key_logit(r.cut_key))) : 1) : 0;
-  for_slice(x, n, [&](int, float l) {
-    const float z = z_of(r, l);
-    if (z < (float)BINS && !below_cut(r, l)) hist_add<MASS>(s, 0, (int)z, r, l);
+  for_vectors(x, n, [&](int, const float* l) {
+    constexpr int VEC = 16 / sizeof(T);
+    u64 w[VEC];
+    if (MASS) {
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) w[j] = fixed(weight(r, l[j]));   // chains side by side
+    }
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+      const float z = z_of(r, l[j]);
+      if (z < (float)BINS && !below_cut(r, l[j])) hist_add<MASS>(s, 0, (int)z, MASS ? w[j] : 0);
+    }
   });
   cluster_sync();
   Level v;
@@ -326,10 +369,33 @@ FD_DEV void refine(Shared& s, Row& r, const Level& v, const T* x, int n, int id0
     }
     return;
   }
+  // this CTA's tokens of the bin as a list; a list that overflows is replaced
+  // by passes over the slice
   const float lo = (float)v.bin;
-  for_slice(x, n, [&](int, float l) {
+  auto in_bin1 = [&](float l) {
     const float z = z_of(r, l) - lo;
-    if (z >= 0.0f && z < 1.0f && !below_cut(r, l)) hist_add<MASS>(s, 1, (int)(z * BINS), r, l);
+    return z >= 0.0f && z < 1.0f && !below_cut(r, l);
+  };
+  auto bin2 = [&](float l) { return (int)((z_of(r, l) - lo) * BINS); };
+  if (tid == 0) s.n_list = s.n_sub = 0;
+  __syncthreads();
+  for_slice(x, n, [&](int i, float l) {
+    if (in_bin1(l)) {
+      const int at = atomicAdd(&s.n_list, 1);
+      if (at < CAP) s.list[at] = order_of(l, id0 + i);
+    }
+  });
+  __syncthreads();
+  const int n1 = s.n_list;
+  auto for_bin = [&](auto f) {
+    if (n1 <= CAP)
+      for (int j = tid; j < n1; j += ST) f(s.list[j]);
+    else
+      for_slice(x, n, [&](int i, float l) { if (in_bin1(l)) f(order_of(l, id0 + i)); });
+  };
+  for_bin([&](u64 o) {
+    const float l = order_logit(o);
+    hist_add<MASS>(s, 1, bin2(l), MASS ? unit(l) : 0);
   });
   cluster_sync();
   zero_hist(s, 0);   // every CTA has read it
@@ -337,26 +403,22 @@ FD_DEV void refine(Shared& s, Row& r, const Level& v, const T* x, int n, int id0
   find_bin<MASS>(s, 1, n_cta, &total, [&](u64) { return v.need - v.before; });
   const int b2 = s.bin;
   const u64 before = v.before + s.before;
-  if (tid == 0) s.n_list = 0;
-  __syncthreads();
-  auto in_bin = [&](float l) {
-    const float z = z_of(r, l) - lo;
-    return z >= 0.0f && z < 1.0f && (int)(z * BINS) == b2 && !below_cut(r, l);
-  };
-  for_slice(x, n, [&](int i, float l) {
-    if (in_bin(l)) {
-      const int at = atomicAdd(&s.n_list, 1);
-      if (at < CAP) s.list[at] = order_of(l, id0 + i);
+  auto in_bin = [&](float l) { return in_bin1(l) && bin2(l) == b2; };
+  for_bin([&](u64 o) {
+    if (bin2(order_logit(o)) == b2) {
+      const int at = atomicAdd(&s.n_sub, 1);
+      if (at < CAP) s.sub[at] = o;
     }
   });
   cluster_sync();
   zero_hist(s, 1);
   int n_all = 0;
-  for (int c = 0; c < n_cta; ++c) {
-    const int nc = ld_remote32(&s.n_list, c);
+#pragma unroll
+  for (int c = 0; c < MAX_CLUSTER; ++c) {
+    const int nc = c < n_cta ? (int)ld_remote32(&s.n_sub, c) : 0;
     if (n_all + nc <= CAP)
       for (int j = tid; j < nc; j += ST) {
-        const u64 o = ld_remote64(&s.list[j], c);
+        const u64 o = ld_remote64(&s.sub[j], c);
         s.all[n_all + j] = o;
         s.w[n_all + j] = unit(order_logit(o));
       }
@@ -443,6 +505,47 @@ struct Filters {
 FD_DEV void draw_sorted(Shared& s, const Row& r, const Filters& f, int n, u64 need, double u,
                         int32_t* tok, float* prob) {
   const int tid = threadIdx.x;
+  if (n <= DIRECT) {
+    // token tid: its rank and the weight before it in the order, then in the ids
+    const bool have = tid < n;
+    const u64 o = have ? s.all[tid] : 0;
+    const float l = have ? order_logit(o) : r.m;
+    const double wd = weight(r, l);
+    u64 w = have ? fixed(wd) : 0;
+    if (have) s.w[tid] = w;
+    __syncthreads();
+    int rank = 0;
+    u64 before = 0;
+    if (have)
+      for (int i = 0; i < n; ++i)
+        if (s.all[i] > o) {
+          ++rank;
+          before += s.w[i];
+        }
+    if (f.top_k > 0 && rank >= f.top_k) w = 0;
+    if (!(f.top_p >= 1.0)) {
+      const u64 total = need ? 0 : block_sum(w, s);
+      if (need == 0) need = (u64)ceil(fmax(f.top_p * (double)total, 0.0));
+      if (rank > 0 && before >= need) w = 0;
+    }
+    if (f.min_p > 0.0 && wd < f.min_p) w = 0;
+    const u64 all = block_sum(w, s);   // every thread has read s.w
+    if (have) s.w[tid] = w;
+    __syncthreads();
+    bool mine = f.greedy && have && rank == 0;
+    if (!f.greedy && w) {
+      const u64 target = min((u64)(fmax(u, 0.0) * (double)all), all - 1);
+      u64 lower = 0;
+      for (int i = 0; i < n; ++i)
+        if ((uint32_t)s.all[i] > (uint32_t)o) lower += s.w[i];   // low words: ~id
+      mine = lower <= target && target < lower + w;
+    }
+    if (mine) {
+      *tok = order_id(o);
+      if (prob) *prob = (float)(wd / ((double)all / W_ONE));
+    }
+    return;
+  }
   int size = 64;
   while (size < n) size *= 2;
   for (int i = n + tid; i < size; i += ST) s.all[i] = 0;
@@ -555,7 +658,7 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const fdllm_sample_args a
   }
   zero_hist(s, 0);
   zero_hist(s, 1);
-  if (tid < 64) s.exp2_64[tid] = exp2((double)tid / 64.0);
+  if (tid < 64) s.exp2_64[tid] = EXP2_64[tid];
   if (tid == 0) s.n_list = 0;
   {
     const float w = warp_max(top);
@@ -591,7 +694,7 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const fdllm_sample_args a
     const bool has_p = !(f.top_p >= 1.0);
     const double u = a.u[row];
     r.md = r.m;
-    r.y = 1.4426950408889634 / temp;
+    r.y = 64.0 * 1.4426950408889634 / temp;
     r.zs = (float)fmin((double)Z_BINS / temp, 1e30);
     r.exp2_64 = s.exp2_64;
     auto need_p = [&](u64 t) { return (u64)ceil(fmax(f.top_p * (double)t, 0.0)); };
@@ -599,6 +702,7 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const fdllm_sample_args a
     // ---- a bound on the kept tokens' z
     float z_end = (float)BINS;
     bool gather = a.vocab <= CAP;
+    bool used = false;   // hist[0] holds the threads' maxima
     Level lp{};
     if (f.min_p > 0.0 && !(has_p && f.top_k > 0)) {   // top-p's goal counts what top-k keeps
       z_end = fminf(z_end, (float)(-log(f.min_p)) * (Z_BINS * 1.00001f) + 0.001f);
@@ -616,8 +720,7 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const fdllm_sample_args a
         z_end = fminf(z_end, (float)(s.bin + 1));
         gather = true;
       }
-      cluster_sync();   // every CTA has read the histogram
-      zero_hist(s, 0);
+      used = true;
     } else if (f.top_k == 0 && has_p) {
       lp = level1<true>(s, r, x, n, n_cta, need_p);
       if (lp.need > 0 && lp.need <= lp.above) {
@@ -639,20 +742,25 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const fdllm_sample_args a
       });
       cluster_sync();
       int n_all = 0;
-      for (int c = 0; c < n_cta; ++c) {
-        const int nc = ld_remote32(&s.n_list, c);
+#pragma unroll
+      for (int c = 0; c < MAX_CLUSTER; ++c) {
+        const int nc = c < n_cta ? (int)ld_remote32(&s.n_list, c) : 0;
         if (rank == 0 && n_all + nc <= CAP)
           for (int j = tid; j < nc; j += ST) s.all[n_all + j] = ld_remote64(&s.list[j], c);
         n_all += nc;
       }
       drawn = n_all <= CAP;
+      cluster_sync();   // every CTA has read the lists and their lengths
       if (drawn) {
         if (rank == 0) draw_sorted(s, r, f, n_all, lp.need, u, a.tok + row, a.prob ? a.prob + row : nullptr);
-      } else {
-        cluster_sync();   // every CTA has read the lists' lengths
+        return;
       }
     }
     if (!drawn) {
+      if (used) {
+        if (!gather) cluster_sync();   // every CTA has read the histogram
+        zero_hist(s, 0);
+      }
       if (f.top_k > 0) {
         __syncthreads();
         const Level v = level1<false>(s, r, x, n, n_cta, [&](u64) { return (u64)f.top_k; });
@@ -666,20 +774,22 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const fdllm_sample_args a
       const int i0 = min(tid * run, n), i1 = min(i0 + run, n);
       auto kept_w = [&](int i) {
         const float l = to_f<T>(x[i]);
-        if (!(z_of(r, l) < z_end)) return (u64)0;
-        if (r.has_cut) {
+        const double wd = weight(r, l);
+        u64 w = fixed(wd);
+        if (!(z_of(r, l) < z_end) || (f.min_p > 0.0 && wd < f.min_p)) w = 0;
+        if (r.has_cut && l > -INFINITY) {
           const uint32_t k = logit_key(l);
-          if (k < r.cut_key || (k == r.cut_key && id0 + i > r.cut_id)) return (u64)0;
+          if (k < r.cut_key || (k == r.cut_key && id0 + i > r.cut_id)) w = 0;
         }
-        const double w = weight(r, l);
-        return f.min_p > 0.0 && w < f.min_p ? (u64)0 : fixed(w);
+        return w;
       };
       u64 sum = 0, lower, mine;
       int first = 0x7fffffff;
-      for (int i = i0; i < i1; ++i) {
-        sum += kept_w(i);
-        if (f.greedy && first == 0x7fffffff && to_f<T>(x[i]) == r.m) first = id0 + i;
-      }
+#pragma unroll 4
+      for (int i = i0; i < i1; ++i) sum += kept_w(i);
+      if (f.greedy)
+        for (int i = i1 - 1; i >= i0; --i)
+          if (to_f<T>(x[i]) == r.m) first = id0 + i;
       u64 before = block_scan(sum, s, &mine) - sum;
       const u64 all = cluster_total(mine, s, n_cta, rank, use++, &lower);
       if (f.greedy) {
@@ -697,14 +807,32 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const fdllm_sample_args a
         // first id whose running sum passes u all: integers, so passes its floor
         const u64 target = min((u64)(fmax(u, 0.0) * (double)all), all - 1);
         before += lower;
-        if (before <= target && target < before + sum) {
-          int i = i0;
-          for (;; ++i) {
-            before += kept_w(i);
-            if (before > target) break;
+        if (tid == 0) s.run1 = -1;
+        __syncthreads();
+        if (before <= target && target < before + sum) {   // this thread's run: a warp walks it
+          s.run0 = i0;
+          s.run1 = i1;
+          s.before = before;
+        }
+        __syncthreads();
+        if (s.run1 >= 0 && tid < 32) {
+          u64 base = s.before;
+          for (int i = s.run0; i < s.run1; i += 32) {
+            const u64 w = i + tid < s.run1 ? kept_w(i + tid) : 0;
+            u64 upto = w;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+              const u64 y = __shfl_up_sync(0xffffffffu, upto, o);
+              if (tid >= o) upto += y;
+            }
+            upto += base;
+            if (upto - w <= target && target < upto) {
+              a.tok[row] = id0 + i + tid;
+              if (a.prob)
+                a.prob[row] = (float)(weight(r, to_f<T>(x[i + tid])) / ((double)all / W_ONE));
+            }
+            base = __shfl_sync(0xffffffffu, upto, 31);
           }
-          a.tok[row] = id0 + i;
-          if (a.prob) a.prob[row] = (float)(weight(r, to_f<T>(x[i])) / ((double)all / W_ONE));
         }
       }
     }

@@ -81,6 +81,35 @@ def test_rows_of_equal_logits():
         _check(y, u, temperature=[0.0] * 6, mask_id=0)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+def test_large_kept_sets(dtype):
+    """Kept sets beyond what is gathered and sorted: flat rows, wide nuclei,
+    large top_k, alone and together; heavy ties in 16-bit logits."""
+    g = torch.Generator().manual_seed(21)
+    x = (torch.randn(6, 60001, generator=g) * torch.tensor([0.01, 0.3, 1.0, 2.0, 4.0, 1.0])[:, None]).to(TYPES[dtype])
+    u = torch.rand(6, generator=g, dtype=torch.float64).tolist()
+    t = [1.0, 0.7, 1.3, 1.0, 1.0, 50.0]
+    _check(x, u, temperature=t, top_p=[0.9, 0.5, 0.95, 0.99, 0.999, 0.3], mask_id=60000)
+    _check(x, u, temperature=t, top_k=[2000, 4096, 5000, 1025, 30000, 59999])
+    _check(x, u, temperature=t, top_k=[2000, 4096, 5000, 1500, 30000, 59999],
+           top_p=[0.9, 0.5, 0.95, 0.99, 0.999, 0.3])
+    _check(x, u, temperature=t, top_k=[700, 512, 300, 1000, 1024, 250], top_p=[0.5] * 6, min_p=[0.1] * 6)
+    _check(x, u, temperature=t, min_p=[0.5, 0.01, 1e-3, 1e-4, 1e-6, 0.99])
+    _check(x, u, temperature=t, top_p=[0.9, 0.5, 0.95, 0.99, 0.999, 0.3], min_p=[0.5, 0.01, 1e-3, 1e-4, 1e-6, 0.99])
+    _check(x, u, temperature=[0.0] * 6, top_p=[0.7] * 6)
+
+
+def test_many_rows_and_the_largest_vocabulary():
+    g = torch.Generator().manual_seed(22)
+    x = _logits(g, 700, 2051, 1.5)
+    u = torch.rand(700, generator=g, dtype=torch.float64).tolist()
+    _check(x, u, top_p=[0.8] * 700, top_k=[100] * 700, mask_id=17)
+    for dtype in TYPES.values():
+        y = _logits(g, 2, 1 << 18, 1.5).to(dtype)
+        _check(y, [0.3, 0.9], top_p=[0.9, 0.2])
+        _check(y, [0.3, 0.9])
+
+
 def test_filter_settings_at_their_ends():
     g = torch.Generator().manual_seed(2)
     x = _logits(g, 8, 700)
