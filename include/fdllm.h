@@ -553,7 +553,8 @@ typedef struct {
 
 /* Draw one token per row.  With l the row's logits, m their maximum over the
  * tokens that may be drawn, w_i = exp((l_i - m) / temperature) in float64
- * (temperature 1 for a greedy row), and the tokens sorted by falling logit,
+ * (temperature 1 for a greedy row, else taken within [1e-29, 1e30]), and the
+ * tokens sorted by falling logit,
  * the lower id first among equal ones:
  *   top_k  keeps the first top_k tokens;
  *   top_p  then keeps tokens while the weight before them is below top_p

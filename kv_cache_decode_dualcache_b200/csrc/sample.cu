@@ -46,7 +46,6 @@ constexpr float Z_BINS = 8.0f;               // bins per unit of z: 256 / 32
 constexpr int CAP = 1024;                    // tokens that are gathered and sorted
 constexpr int DIRECT = 192;                  // tokens whose order is taken by counting
 constexpr double W_ONE = 17592186044416.0;   // 2^44
-constexpr float F_MAX = 3.402823466e38f;
 
 typedef unsigned long long u64;
 
@@ -65,14 +64,15 @@ FD_DEV int order_id(u64 o) { return (int)~(uint32_t)o; }
 
 struct __align__(16) Shared {
   double exp2_64[64];          // 2^(j / 64)
-  uint32_t hist[2][4][BINS];   // weights in words of 15, 15 and 15 bits; counts
+  uint32_t hist[2][3][BINS];   // weights in words of 15, 15 and 15 bits, or counts
   u64 red[SW];
   u64 part[2];                 // this CTA's share of a cluster sum (by parity of use)
-  u64 before, before_count;
+  u64 before, upto;
   float top;                   // this CTA's largest logit
-  int bin, n_list, n_sub, cut_id, cut_ties, pick;
+  int bin, n_hot, n_list, n_sub, cut_id, cut_ties, pick;
   int run0, run1;              // the run of ids that holds the drawn token
   uint32_t cut_key;
+  uint16_t hot[ST];            // threads that hold a token within the bound
   u64 list[CAP];               // this CTA's gathered tokens (order_of)
   u64 all[CAP];                // the cluster's
   u64 w[CAP];                  // their weights
@@ -122,10 +122,10 @@ struct Row {
   bool has_cut, listed;   // listed: the class of cut_key is in Shared::all[0 .. n_list)
 };
 
-// exp((l - m) / T) of a live token = 2^((n + f) / 64): 2^(n / 64) from the
-// table and the exponent, 2^(f / 64), |f| <= 1/2, by its Taylor polynomial
-// (error below (ln 2 / 128)^5 / 120 = 4e-14).  No branch but the common
-// case's, so that the chains of several tokens overlap.
+// exp((l - m) / T) = 2^((n + f) / 64) of a token with z < BINS (anything for
+// others): 2^(n / 64) from the table and the exponent, 2^(f / 64), |f| <= 1/2,
+// by its Taylor polynomial (error below (ln 2 / 128)^5 / 120 = 4e-14).
+// Without a branch, so that the chains of several tokens overlap.
 FD_DEV double weight(const Row& r, float l) {
   const double y = ((double)l - r.md) * r.y;   // 64 log2 of the weight
   const double magic = 6755399441055744.0;     // 1.5 2^52: its sum with y is an integer
@@ -137,21 +137,18 @@ FD_DEV double weight(const Row& r, float l) {
   p = fma(f, p, c * c / 2.0);
   p = fma(f, p, c);
   const double s = r.exp2_64[n & 63];
-  double w = fma(f * p, s, s);
-  w = __hiloint2double(__double2hiint(w) + ((n >> 6) << 20), __double2loint(w));
-  if (!(y > -4096.0)) w = 0.0;                 // below 2^-64; NaN where +inf meets a finite logit
-  return l == r.m ? 1.0 : w;
+  const double w = fma(f * p, s, s);
+  return __hiloint2double(__double2hiint(w) + ((n >> 6) << 20), __double2loint(w));
 }
 // rint(w 2^44): the sum with 2^52 is an integer in the low bits.
 FD_DEV u64 fixed(double w) {
   return (u64)__double_as_longlong(fma(w, W_ONE, 4503599627370496.0)) & 0xfffffffffffffull;
 }
 
-// Place of a token among the bins; >= BINS: not live, or too light to be drawn.
-FD_DEV float z_of(const Row& r, float l) {
-  if (l == r.m) return 0.0f;
-  return l > -INFINITY ? fminf(r.m - l, F_MAX) * r.zs : (float)BINS;
-}
+// Place of a token among the bins; not below BINS: not live (-inf, NaN), or
+// too light to be drawn.  Rounded on its own (no fused z - bin), so that every
+// pass puts a token into the same bin.
+FD_DEV float z_of(const Row& r, float l) { return __fmul_rn(r.m - l, r.zs); }
 FD_DEV bool below_cut(const Row& r, float l) { return r.has_cut && logit_key(l) <= r.cut_key; }
 
 // f(index, logits) for the slice's tokens, 16 bytes at a time.
@@ -168,13 +165,32 @@ FD_DEV void for_vectors(const T* x, int n, F f) {
     f(i * VEC, l);
   }
 }
-// f(index, logit), one token after the other.
-template <typename T, typename F>
-FD_DEV void for_slice(const T* x, int n, F f) {
-  for_vectors(x, n, [&](int i, const float* l) {
+// f(index, logit) for the slice's tokens with pred(logit), for rare ones: a
+// thread first marks its hits among 32 tokens, then visits them, so that a
+// warp runs f as often as its busiest lane has hits.
+template <typename T, typename P, typename F>
+FD_DEV void for_hits(const T* x, int n, P pred, F f) {
+  constexpr int VEC = 16 / sizeof(T), G = 32 / VEC;
+  const uint4* v = reinterpret_cast<const uint4*>(x);
+  for (int i0 = threadIdx.x; i0 * VEC < n; i0 += G * ST) {
+    uint32_t hits = 0;
 #pragma unroll
-    for (int j = 0; j < 16 / (int)sizeof(T); ++j) f(i + j, l[j]);
-  });
+    for (int g = 0; g < G; ++g) {
+      const int i = i0 + g * ST;
+      if (i * VEC < n) {
+        const uint4 u = v[i];
+        const T* e = reinterpret_cast<const T*>(&u);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) hits |= pred(to_f<T>(e[j])) ? 1u << (g * VEC + j) : 0u;
+      }
+    }
+    while (hits) {
+      const int b = __ffs(hits) - 1;
+      hits &= hits - 1;
+      const int i = (i0 + (b / VEC) * ST) * VEC + b % VEC;
+      f(i, to_f<T>(x[i]));
+    }
+  }
 }
 
 FD_DEV u64 warp_sum64(u64 v) {
@@ -230,46 +246,45 @@ FD_DEV u64 cluster_total(u64 v, Shared& s, int n_cta, int rank, int use, u64* lo
 }
 
 FD_DEV void zero_hist(Shared& s, int h) {
-  for (int i = threadIdx.x; i < 4 * BINS; i += ST) (&s.hist[h][0][0])[i] = 0;
+  for (int i = threadIdx.x; i < 3 * BINS; i += ST) (&s.hist[h][0][0])[i] = 0;
 }
 template <bool MASS>
 FD_DEV void hist_add(Shared& s, int h, int bin, u64 w) {
   if (MASS) {
-    if (w & 0x7fff) atomicAdd(&s.hist[h][0][bin], (uint32_t)w & 0x7fff);
-    if (w & 0x3fff8000) atomicAdd(&s.hist[h][1][bin], (uint32_t)(w >> 15) & 0x7fff);
-    if (w >> 30) atomicAdd(&s.hist[h][2][bin], (uint32_t)(w >> 30));
+    const uint32_t lo = (uint32_t)w, hi = (uint32_t)(w >> 30);
+    atomicAdd(&s.hist[h][0][bin], lo & 0x7fff);
+    atomicAdd(&s.hist[h][1][bin], (lo >> 15) & 0x7fff);
+    if (hi) atomicAdd(&s.hist[h][2][bin], hi);
+  } else {
+    atomicAdd(&s.hist[h][0][bin], 1u);
   }
-  atomicAdd(&s.hist[h][3][bin], 1u);
 }
 
 // The bin in which the running sum over the bins of all CTAs (weights, or
 // counts) reaches `need` = need_of(sum of all bins) goes to s.bin, what lies
-// before it to s.before, the count up to its end to s.before_count.  *above:
-// the sum of all bins.
+// before it to s.before, and up to its end to s.upto.  *above: the sum of
+// all bins.
 template <bool MASS, typename F>
 FD_DEV u64 find_bin(Shared& s, int h, int n_cta, u64* above, F need_of) {
-  u64 v = 0, c = 0;
-  if (threadIdx.x < BINS) {
+  // two threads a bin, each for half of the CTAs
+  const int bin = threadIdx.x >> 1, half = threadIdx.x & 1;
+  u64 v = 0;
 #pragma unroll
-    for (int i = 0; i < MAX_CLUSTER; ++i) {
-      if (i >= n_cta) continue;
-      c += ld_remote32(&s.hist[h][3][threadIdx.x], i);
-      if (MASS)
-        v += (u64)ld_remote32(&s.hist[h][0][threadIdx.x], i) +
-             ((u64)ld_remote32(&s.hist[h][1][threadIdx.x], i) << 15) +
-             ((u64)ld_remote32(&s.hist[h][2][threadIdx.x], i) << 30);
-    }
+  for (int j = 0; j < MAX_CLUSTER / 2; ++j) {
+    const int i = 2 * j + half;
+    if (i >= n_cta) continue;
+    v += ld_remote32(&s.hist[h][0][bin], i);
+    if (MASS)
+      v += ((u64)ld_remote32(&s.hist[h][1][bin], i) << 15) +
+           ((u64)ld_remote32(&s.hist[h][2][bin], i) << 30);
   }
-  u64 total_c, total = 0;
-  const u64 upto_c = block_scan(c, s, &total_c);
-  const u64 upto = MASS ? block_scan(v, s, &total) : upto_c;
-  if (!MASS) v = c, total = total_c;
-  *above = total;
-  const u64 need = need_of(total);
-  if (threadIdx.x < BINS && upto - v < need && need <= upto) {
-    s.bin = threadIdx.x;
-    s.before = upto - v;
-    s.before_count = upto_c;
+  const u64 upto = block_scan(v, s, above);
+  const u64 need = need_of(*above);
+  const u64 bin_sum = v + __shfl_xor_sync(0xffffffffu, v, 1);
+  if (half == 1 && upto - bin_sum < need && need <= upto) {
+    s.bin = bin;
+    s.before = upto - bin_sum;
+    s.upto = upto;
   }
   __syncthreads();
   return need;
@@ -314,8 +329,8 @@ FD_DEV void nth_tie(Shared& s, Row& r, int ties, const T* x, int n, int id0, int
 // First step of a search: the bin of z in which the sum over the kept tokens
 // reaches need_of(all of it).
 struct Level {
-  u64 need, above, before, upto_count;   // above: strictly above the cut
-  int bin;                               // valid if 0 < need <= above
+  u64 need, above, before, upto;   // above: strictly above the cut
+  int bin;                         // valid if 0 < need <= above
 };
 template <bool MASS, typename T, typename F>
 FD_DEV Level level1(Shared& s, const Row& r, const T* x, int n, int n_cta, F need_of) {
@@ -338,7 +353,7 @@ FD_DEV Level level1(Shared& s, const Row& r, const T* x, int n, int n_cta, F nee
   v.need = find_bin<MASS>(s, 0, n_cta, &v.above, [&](u64 t) { return need_of(t + at_cut); });
   v.bin = s.bin;
   v.before = s.before;
-  v.upto_count = s.before_count;
+  v.upto = s.upto;
   return v;
 }
 
@@ -379,11 +394,9 @@ FD_DEV void refine(Shared& s, Row& r, const Level& v, const T* x, int n, int id0
   auto bin2 = [&](float l) { return (int)((z_of(r, l) - lo) * BINS); };
   if (tid == 0) s.n_list = s.n_sub = 0;
   __syncthreads();
-  for_slice(x, n, [&](int i, float l) {
-    if (in_bin1(l)) {
-      const int at = atomicAdd(&s.n_list, 1);
-      if (at < CAP) s.list[at] = order_of(l, id0 + i);
-    }
+  for_hits(x, n, in_bin1, [&](int i, float l) {
+    const int at = atomicAdd(&s.n_list, 1);
+    if (at < CAP) s.list[at] = order_of(l, id0 + i);
   });
   __syncthreads();
   const int n1 = s.n_list;
@@ -391,7 +404,7 @@ FD_DEV void refine(Shared& s, Row& r, const Level& v, const T* x, int n, int id0
     if (n1 <= CAP)
       for (int j = tid; j < n1; j += ST) f(s.list[j]);
     else
-      for_slice(x, n, [&](int i, float l) { if (in_bin1(l)) f(order_of(l, id0 + i)); });
+      for_hits(x, n, in_bin1, [&](int i, float l) { f(order_of(l, id0 + i)); });
   };
   for_bin([&](u64 o) {
     const float l = order_logit(o);
@@ -455,9 +468,8 @@ FD_DEV void refine(Shared& s, Row& r, const Level& v, const T* x, int n, int id0
   const uint32_t kmax = k1;
   auto upto = [&](uint32_t k) {   // sum up to and over the bin's tokens with key >= k
     u64 t = 0;
-    for_slice(x, n, [&](int, float l) {
-      if (in_bin(l) && logit_key(l) >= k) t += unit(l);
-    });
+    for_hits(x, n, [&](float l) { return in_bin(l) && logit_key(l) >= k; },
+             [&](int, float l) { t += unit(l); });
     return before + cluster_total(block_sum(t, s), s, n_cta, rank, use++, nullptr);
   };
   while (k0 < k1) {
@@ -659,7 +671,7 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const fdllm_sample_args a
   zero_hist(s, 0);
   zero_hist(s, 1);
   if (tid < 64) s.exp2_64[tid] = EXP2_64[tid];
-  if (tid == 0) s.n_list = 0;
+  if (tid == 0) s.n_list = s.n_hot = 0;
   {
     const float w = warp_max(top);
     if ((tid & 31) == 0) s.red[tid >> 5] = __float_as_uint(w);
@@ -678,6 +690,13 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const fdllm_sample_args a
   for (int i = 0; i < MAX_CLUSTER; ++i)
     if (i < n_cta) r.m = fmaxf(r.m, __uint_as_float(ld_remote32(&s.top, i)));
 
+  if (r.m == INFINITY) {   // they share all the weight: equal logits, the rest is out
+    for (int i = tid; i < n; i += ST)
+      x[i] = from_f<T>(to_f<T>(x[i]) == INFINITY ? 0.0f : -INFINITY);
+    r.m = 0.0f;
+    top = top == INFINITY ? 0.0f : -INFINITY;
+    __syncthreads();
+  }
   if (r.m == -INFINITY) {
     if (rank == 0 && tid == 0) {
       a.tok[row] = -1;
@@ -688,6 +707,7 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const fdllm_sample_args a
     double temp = a.temperature ? (double)a.temperature[row] : 1.0;
     f.greedy = !(temp > 0.0);
     if (f.greedy) temp = 1.0;
+    temp = fmin(fmax(temp, 1e-29), 1e30);
     f.top_k = a.top_k ? max(a.top_k[row], 0) : 0;
     f.top_p = a.top_p ? (double)a.top_p[row] : 1.0;
     f.min_p = a.min_p ? fmin((double)a.min_p[row], 1.0) : 0.0;
@@ -695,7 +715,7 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const fdllm_sample_args a
     const double u = a.u[row];
     r.md = r.m;
     r.y = 64.0 * 1.4426950408889634 / temp;
-    r.zs = (float)fmin((double)Z_BINS / temp, 1e30);
+    r.zs = (float)((double)Z_BINS / temp);
     r.exp2_64 = s.exp2_64;
     auto need_p = [&](u64 t) { return (u64)ceil(fmax(f.top_p * (double)t, 0.0)); };
 
@@ -712,7 +732,7 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const fdllm_sample_args a
       if (has_p) z_end = (float)BINS;
     } else if (f.top_k > 0 && f.top_k <= ST * n_cta / 2) {
       const float z = z_of(r, top);
-      if (z < (float)BINS) atomicAdd(&s.hist[0][3][(int)z], 1u);
+      if (z < (float)BINS) atomicAdd(&s.hist[0][0][(int)z], 1u);
       cluster_sync();
       u64 above;
       const u64 need = find_bin<false>(s, 0, n_cta, &above, [&](u64) { return (u64)f.top_k; });
@@ -724,7 +744,8 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const fdllm_sample_args a
     } else if (f.top_k == 0 && has_p) {
       lp = level1<true>(s, r, x, n, n_cta, need_p);
       if (lp.need > 0 && lp.need <= lp.above) {
-        gather |= lp.upto_count <= CAP;
+        // none of the tokens up to the bin's end is lighter than its end
+        gather |= (double)lp.upto / W_ONE * exp((lp.bin + 1) / (double)Z_BINS) <= CAP;
         z_end = fminf(z_end, (float)(lp.bin + 1));
       } else {
         gather = false;
@@ -733,13 +754,26 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const fdllm_sample_args a
     // ---- the tokens within the bound, if they are few
     bool drawn = false;
     if (gather) {
+      // only threads whose largest logit is within it have any: their tokens
+      // are spread over all threads again
       __syncthreads();
-      for_slice(x, n, [&](int i, float l) {
-        if (z_of(r, l) < z_end) {
-          const int at = atomicAdd(&s.n_list, 1);
-          if (at < CAP) s.list[at] = order_of(l, id0 + i);
+      if (z_of(r, top) < z_end) s.hot[atomicAdd(&s.n_hot, 1)] = (uint16_t)tid;
+      __syncthreads();
+      const int per = ((n + VEC - 1) / VEC + ST - 1) / ST, items = s.n_hot * per;
+      for (int j = tid; j < items; j += ST) {
+        const int i = s.hot[j / per] + (j % per) * ST;
+        if (i * VEC >= n) continue;
+        const uint4 v = reinterpret_cast<const uint4*>(x)[i];
+        const T* e = reinterpret_cast<const T*>(&v);
+#pragma unroll
+        for (int q = 0; q < VEC; ++q) {
+          const float l = to_f<T>(e[q]);
+          if (z_of(r, l) < z_end) {
+            const int at = atomicAdd(&s.n_list, 1);
+            if (at < CAP) s.list[at] = order_of(l, id0 + i * VEC + q);
+          }
         }
-      });
+      }
       cluster_sync();
       int n_all = 0;
 #pragma unroll
@@ -772,21 +806,38 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const fdllm_sample_args a
       // ---- the draw: every thread takes a run of ids (odd: no bank conflicts)
       const int run = ((n + ST - 1) / ST) | 1;
       const int i0 = min(tid * run, n), i1 = min(i0 + run, n);
-      auto kept_w = [&](int i) {
+      auto kept = [&](int i) {
         const float l = to_f<T>(x[i]);
-        const double wd = weight(r, l);
-        u64 w = fixed(wd);
-        if (!(z_of(r, l) < z_end) || (f.min_p > 0.0 && wd < f.min_p)) w = 0;
-        if (r.has_cut && l > -INFINITY) {
+        bool in = z_of(r, l) < z_end;
+        if (r.has_cut) {
           const uint32_t k = logit_key(l);
-          if (k < r.cut_key || (k == r.cut_key && id0 + i > r.cut_id)) w = 0;
+          in = in && (k > r.cut_key || (k == r.cut_key && id0 + i <= r.cut_id));
         }
-        return w;
+        return in;
+      };
+      auto kept_w = [&](int i) {
+        const double wd = weight(r, to_f<T>(x[i]));
+        return kept(i) && !(f.min_p > 0.0 && wd < f.min_p) ? fixed(wd) : (u64)0;
       };
       u64 sum = 0, lower, mine;
       int first = 0x7fffffff;
+      if (r.has_cut || z_end < (float)BINS) {   // few are kept: mark them, then weigh them
+        for (int j0 = i0; j0 < i1; j0 += 32) {
+          uint32_t hits = 0;
+#pragma unroll 8
+          for (int j = 0; j < 32; ++j)
+            if (j0 + j < i1 && kept(j0 + j)) hits |= 1u << j;
+          while (hits) {
+            const int j = __ffs(hits) - 1;
+            hits &= hits - 1;
+            const double wd = weight(r, to_f<T>(x[j0 + j]));
+            if (!(f.min_p > 0.0 && wd < f.min_p)) sum += fixed(wd);
+          }
+        }
+      } else {
 #pragma unroll 4
-      for (int i = i0; i < i1; ++i) sum += kept_w(i);
+        for (int i = i0; i < i1; ++i) sum += kept_w(i);
+      }
       if (f.greedy)
         for (int i = i1 - 1; i >= i0; --i)
           if (to_f<T>(x[i]) == r.m) first = id0 + i;
