@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <initializer_list>
 #include <string>
 
@@ -35,6 +36,31 @@ inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 
 // Rows of `heads` vectors of hd elements that start on 16-byte boundaries.
 inline bool rows_ok(const void* p, const int64_t* strides, int esz) {
   return aligned16(p) && (strides[0] * esz) % 16 == 0 && (strides[1] * esz) % 16 == 0;
+}
+
+// Device facts that do not change, asked once per device.
+inline cudaError_t sm_count(int* n) {
+  static std::atomic<int> known[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 64 && (*n = known[dev].load(std::memory_order_relaxed)) > 0) return cudaSuccess;
+  e = cudaDeviceGetAttribute(n, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess && dev < 64) known[dev].store(*n, std::memory_order_relaxed);
+  return e;
+}
+// Raises a kernel's dynamic shared-memory limit, once per device (`ready`:
+// one bit a device).
+template <typename K>
+cudaError_t allow_smem(K kern, int bytes, std::atomic<uint64_t>& ready) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (ready.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) ready.fetch_or(bit, std::memory_order_relaxed);
+  return e;
 }
 
 // Checks *c and copies it to *out with its strides filled in.

@@ -2,12 +2,17 @@
 // 8-bit paged K/V cache.
 //
 // A query row is a (token, head-in-group) pair, so that the query heads of a
-// K/V head share every cached byte.  CTA = (tile of 16 RT rows, K/V head,
-// sequence, key split); its 8 warps take the split's keys in tiles of 32,
-// every warp with a ring of cp.async stages, softmax statistics and an
-// output accumulator of its own, so the loop has no barrier beyond the
-// warp's; the warps' results meet in shared memory at the end, the splits'
-// in a second kernel.
+// K/V head share every cached byte.  A run is a tile of 16 RT rows, a K/V head
+// and a sequence with all its pages; the pages of all runs, laid end to end,
+// are shared out evenly over the CTAs (two an SM), whatever the lengths are.
+// They are known on the device only, so every CTA sums them up for itself.
+// A CTA's 4 warps take its part of a run in tiles of 32 keys, every warp with
+// a ring of cp.async stages, softmax statistics and an output accumulator of
+// its own, so the loop has no barrier beyond the warp's; the warps' results
+// meet in shared memory.  A run that a CTA does not hold whole leaves a
+// partial result in the workspace (at most two a CTA: the end of one run and
+// the start of another), and a second kernel joins those, one block for the
+// first share boundary inside a run.
 //
 // Codes are exact in fp16 and become matrix operands on the way from shared
 // memory to registers (sign bit flipped, byte put under the exponent of
@@ -37,7 +42,7 @@
 namespace fd {
 namespace {
 
-constexpr int AT_WARPS = 8;
+constexpr int AT_WARPS = 4;    // two CTAs an SM: one's start and end hide behind the other's loop
 constexpr int TILE = 32;      // keys of a warp's tile
 constexpr int STAGES = 3;
 constexpr int PAGE = FDLLM_KV8_PAGE;
@@ -49,17 +54,63 @@ constexpr float VS_MIN = 7.888609052210118e-31f;  // 2^-100: an all-zero block s
 struct AttnP {
   fdllm_kv8 c;
   fdllm_kv8_attention_args a;
-  int n_split;       // most splits of a sequence
-  int keys;          // keys of a split, a multiple of 64
-  float* part_o;     // [split][n_tokens][n_heads][head_dim]
-  float2* part_ml;   // [split][n_tokens][n_heads] (reference max, weight sum)
+  int n_cta;         // shares (the grid)
+  float* part_o;     // [share][2][rows of a tile][head_dim]; NULL: runs are not split
+  float2* part_ml;   // [share][2][rows of a tile] (reference max, weight sum)
 };
 
-// Split length of a sequence of L keys: P.keys unless that makes more splits
-// than there is room for.
-FD_DEV int split_keys(const AttnP& P, int L) {
-  const int least = ((L + P.n_split - 1) / P.n_split + PAGE - 1) / PAGE * PAGE;
-  return max(P.keys, least);
+// A sequence's rows and runs.
+struct Seq {
+  int r_lo, rows, len, pages, tiles;   // rows: (token, head) pairs of a K/V head
+  int64_t work;                        // pages of all its runs
+};
+FD_DEV Seq seq_of(const AttnP& P, int i, int tile_rows) {
+  const fdllm_kv8_attention_args& a = P.a;
+  Seq s;
+  s.r_lo = min(max(a.starts[i], 0), a.n_tokens);
+  const int r_hi = min(max(a.starts[i + 1], s.r_lo), a.n_tokens);
+  s.rows = (r_hi - s.r_lo) * (a.n_heads / P.c.n_kv_heads);
+  s.len = min(max(a.lens[i], 0), P.c.max_pages * PAGE);
+  s.pages = max(1, (s.len + PAGE - 1) / PAGE);   // a run without keys still writes its zeros
+  s.tiles = (s.rows + tile_rows - 1) / tile_rows;
+  s.work = (int64_t)s.tiles * P.c.n_kv_heads * s.pages;
+  return s;
+}
+// Sum of all sequences' work, by a warp.
+FD_DEV int64_t total_work(const AttnP& P, int tile_rows) {
+  const int lane = threadIdx.x & 31;
+  int64_t t = 0;
+  for (int i = lane; i < P.c.n_seqs; i += 32) t += seq_of(P, i, tile_rows).work;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+  return t;
+}
+// The sequence that holds position x < total of the pages laid end to end,
+// by a warp; *off: the place within it.
+FD_DEV int find_seq(const AttnP& P, int tile_rows, int64_t x, int64_t* off) {
+  const int lane = threadIdx.x & 31;
+  int64_t base = 0;
+  for (int i0 = 0;; i0 += 32) {
+    const int64_t w = i0 + lane < P.c.n_seqs ? seq_of(P, i0 + lane, tile_rows).work : 0;
+    int64_t upto = w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += y;
+    }
+    const uint32_t hit = __ballot_sync(0xffffffffu, base + upto > x);
+    if (hit || i0 + 32 >= P.c.n_seqs) {
+      const int l = hit ? __ffs(hit) - 1 : 0;
+      *off = x - base - __shfl_sync(0xffffffffu, upto - w, l);
+      return i0 + l;
+    }
+    base += __shfl_sync(0xffffffffu, upto, 31);
+  }
+}
+// Shares in use: at least MIN_PAGES pages each.
+constexpr int MIN_PAGES = 2;
+FD_DEV int64_t shares(const AttnP& P, int64_t total) {
+  return max((int64_t)1, min((int64_t)P.n_cta, (total + MIN_PAGES - 1) / MIN_PAGES));
 }
 
 FD_DEV void cp16(uint32_t dst, const void* src) {
@@ -104,6 +155,27 @@ template <int B> FD_DEV void lds(uint32_t addr, uint32_t* w) {
     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(addr) : "memory");
 }
 
+// 4 consecutive elements of a row (aligned to their size).
+template <typename T> FD_DEV void load4(const T* p, float* x) {
+  if constexpr (sizeof(T) == 4) {
+    const float4 v = *reinterpret_cast<const float4*>(p);
+    x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+  } else {
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    const T* e = reinterpret_cast<const T*>(&u);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = to_f<T>(e[i]);
+  }
+}
+template <typename T> FD_DEV void store4(T* p, float a, float b, float c, float d) {
+  if constexpr (sizeof(T) == 4) {
+    *reinterpret_cast<float4*>(p) = make_float4(a, b, c, d);
+  } else {
+    const T e[4] = {from_f<T>(a), from_f<T>(b), from_f<T>(c), from_f<T>(d)};
+    *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(e);
+  }
+}
+
 template <int HD, int RT, bool TWO>
 struct Lay {
   static constexpr int R = 16 * RT;
@@ -120,7 +192,7 @@ struct Lay {
   static constexpr int CB = HD / 4 < 16 ? HD / 4 : 16;     // bytes of a key's row per lane and load
   static constexpr int NH = HD / (4 * CB);
   static constexpr int NW = CB / 4;
-  static_assert(STAGE % 16 == 0 && SMEM <= 232448, "shared memory layout");
+  static_assert(STAGE % 16 == 0 && SMEM <= 115712, "shared memory layout");
 };
 
 // Offset of 16-byte chunk c of row `row` in a staged tile: chunks are
@@ -140,7 +212,7 @@ template <int HD> FD_DEV int v_off(int row, int c) {
 }
 
 template <typename T, int HD, int RT, bool TWO>
-__global__ void __launch_bounds__(AT_WARPS * 32, 1) kv8_attn_kernel(const AttnP P) {
+__global__ void __launch_bounds__(AT_WARPS * 32, 2) kv8_attn_kernel(const AttnP P) {
   using L_ = Lay<HD, RT, TWO>;
   constexpr int R = L_::R, NH = L_::NH, NW = L_::NW, CB = L_::CB, NTERM = TWO ? 2 : 1;
   extern __shared__ __align__(16) uint8_t smem[];
@@ -149,20 +221,19 @@ __global__ void __launch_bounds__(AT_WARPS * 32, 1) kv8_attn_kernel(const AttnP 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int gid = lane >> 2, t = lane & 3;
   const int rep = a.n_heads / c.n_kv_heads;
-  const int g = blockIdx.y % c.n_kv_heads, seq = blockIdx.z;
+  pdl_trigger();   // the join may be set up; it waits for this grid's end
+  if (blockIdx.x == 0 && a.status)
+    for (int i = tid; i < c.n_seqs; i += AT_WARPS * 32)
+      if (a.lens[i] < 0 || a.lens[i] > c.max_pages * PAGE) atomicOr(a.status, FDLLM_KV8_BAD_RANGE);
 
-  const int r_lo = min(max(a.starts[seq], 0), a.n_tokens);
-  const int r_hi = min(max(a.starts[seq + 1], r_lo), a.n_tokens);
-  const int rows = (r_hi - r_lo) * rep;
-  const int len_in = a.lens[seq];
-  const int L = min(max(len_in, 0), c.max_pages * PAGE);
-  const bool first_cta = blockIdx.x == 0 && blockIdx.y == 0;
-  if (first_cta && tid == 0 && L != len_in && a.status) atomicOr(a.status, FDLLM_KV8_BAD_RANGE);
-  const int keys = split_keys(P, L);
-  const int n_split = max(1, (L + keys - 1) / keys);
-  const int z = blockIdx.x;
-  if (z >= n_split) return;
-  const int k_lo = z * keys, k_hi = min(L, k_lo + keys);
+  // ---- this CTA's share [x, x_end) of all runs' pages
+  const int64_t total = total_work(P, R), n_cta = shares(P, total);
+  if (blockIdx.x >= n_cta) return;
+  int64_t x = total * blockIdx.x / n_cta, off = 0;
+  const int64_t x_end = total * (blockIdx.x + 1) / n_cta;
+  if (x >= x_end) return;
+  int seq = find_seq(P, R, x, &off);
+  Seq sq = seq_of(P, seq, R);
 
   const uint32_t sbase = smem_u32(smem);
   const uint32_t ring = sbase + warp * STAGES * L_::STAGE;
@@ -171,42 +242,29 @@ __global__ void __launch_bounds__(AT_WARPS * 32, 1) kv8_attn_kernel(const AttnP 
   float* xl = xm + AT_WARPS * R;
   float* xo = reinterpret_cast<float*>(smem);                // [warp][R][XROW]
 
-  const int n_tiles = (k_hi - k_lo + TILE - 1) / TILE;
-  const int my = n_tiles > warp ? (n_tiles - warp + AT_WARPS - 1) / AT_WARPS : 0;
-  const int32_t* table = c.page_table + (int64_t)seq * c.table_stride;
-
-  for (int row0 = (blockIdx.y / c.n_kv_heads) * R; row0 < rows;
-       row0 += (gridDim.y / c.n_kv_heads) * R) {
-    // ---- q: a warp per row, lanes with 4 dims each; fragment order in shared memory
-    for (int r = warp; r < R; r += AT_WARPS) {
-      const int rr = row0 + r;
-      float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-      if (rr < rows && lane < HD / 4) {
-        const T* src = reinterpret_cast<const T*>(a.q) + (int64_t)(r_lo + rr / rep) * a.q_strides[0] +
-                       (int64_t)(g * rep + rr % rep) * a.q_strides[1] + lane * 4;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = to_f<T>(src[i]);
-      }
-      const float top = warp_max(fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3]))));
-      // 2^up brings the row's largest |q| into [2^8, 2^9)
-      const int e = (int)((__float_as_uint(top) >> 23) & 255);
-      const int up = e == 0 || e == 255 ? 0 : min(135 - e, 120);
-      const float mul = __uint_as_float((uint32_t)(up + 127) << 23);
-      if (lane < HD / 4) {
-        const int d = lane * 4, ct = d / CB, s = (ct / 4) * NW + (d % CB) / 4;
-        const int mt = r >> 4, half = (r >> 3) & 1;
-        uint8_t* dst = smem + L_::Q_OFF +
-                       (((mt * 2 + half) * (HD / 32) + s / 2) * 32 + (r & 7) * 4 + ct % 4) * 16 +
-                       (s & 1) * 8;
-        __half hi[4], lo[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) split_f16(x[i] * mul, hi[i], lo[i]);
-        *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<const uint2*>(hi);
-        if (TWO) *reinterpret_cast<uint2*>(dst + L_::Q_TERM) = *reinterpret_cast<const uint2*>(lo);
-      }
-      if (lane == 0) fac[r] = a.scale * LOG2E * __uint_as_float((uint32_t)(127 - up) << 23);
+  while (x < x_end) {
+    while (off >= sq.work) {
+      off -= sq.work;
+      sq = seq_of(P, ++seq, R);
     }
-    __syncthreads();
+    const int run = (int)(off / sq.pages), p_lo = (int)(off % sq.pages);
+    int p_hi = (int)min((int64_t)sq.pages, p_lo + (x_end - x));
+    if (!P.part_o) {   // whole runs: those that start in the share
+      if (p_lo > 0) {
+        x += sq.pages - p_lo;
+        off += sq.pages - p_lo;
+        continue;
+      }
+      p_hi = sq.pages;
+    }
+    x += p_hi - p_lo;
+    off += p_hi - p_lo;
+    const bool whole = p_lo == 0 && p_hi == sq.pages;
+    const int g = run / sq.tiles, row0 = run % sq.tiles * R, rows = sq.rows, r_lo = sq.r_lo;
+    const int k_lo = p_lo * PAGE, k_hi = min(sq.len, p_hi * PAGE);
+    const int n_tiles = (k_hi - k_lo + TILE - 1) / TILE;
+    const int my = n_tiles > warp ? (n_tiles - warp + AT_WARPS - 1) / AT_WARPS : 0;
+    const int32_t* table = c.page_table + (int64_t)seq * c.table_stride;
 
     float o[RT][HD / 8][4];
     float M[RT][2], l[RT][2];
@@ -256,6 +314,43 @@ __global__ void __launch_bounds__(AT_WARPS * 32, 1) kv8_attn_kernel(const AttnP 
 
 #pragma unroll
     for (int i = 0; i < STAGES - 1; ++i) issue(i);
+
+    // ---- q: a warp per row, lanes with 4 dims each; fragment order in shared memory
+    float qx[R / AT_WARPS][4];
+#pragma unroll
+    for (int j = 0; j < R / AT_WARPS; ++j) {
+      const int rr = row0 + warp + j * AT_WARPS;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) qx[j][i] = 0.0f;
+      if (rr < rows && lane < HD / 4)
+        load4(reinterpret_cast<const T*>(a.q) + (int64_t)(r_lo + rr / rep) * a.q_strides[0] +
+                  (int64_t)(g * rep + rr % rep) * a.q_strides[1] + lane * 4, qx[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < R / AT_WARPS; ++j) {
+      const int r = warp + j * AT_WARPS;
+      const float* x = qx[j];
+      const float top = warp_max(fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3]))));
+      // 2^up brings the row's largest |q| into [2^8, 2^9)
+      const int e = (int)((__float_as_uint(top) >> 23) & 255);
+      const int up = e == 0 || e == 255 ? 0 : min(135 - e, 120);
+      const float mul = __uint_as_float((uint32_t)(up + 127) << 23);
+      if (lane < HD / 4) {
+        const int d = lane * 4, ct = d / CB, s = (ct / 4) * NW + (d % CB) / 4;
+        const int mt = r >> 4, half = (r >> 3) & 1;
+        uint8_t* dst = smem + L_::Q_OFF +
+                       (((mt * 2 + half) * (HD / 32) + s / 2) * 32 + (r & 7) * 4 + ct % 4) * 16 +
+                       (s & 1) * 8;
+        __half hi[4], lo[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) split_f16(x[i] * mul, hi[i], lo[i]);
+        *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<const uint2*>(hi);
+        if (TWO) *reinterpret_cast<uint2*>(dst + L_::Q_TERM) = *reinterpret_cast<const uint2*>(lo);
+      }
+      if (lane == 0) fac[r] = a.scale * LOG2E * __uint_as_float((uint32_t)(127 - up) << 23);
+    }
+    __syncthreads();
+
     for (int it = 0; it < my; ++it) {
       issue(it + STAGES - 1);
       cp_wait<STAGES - 1>();
@@ -480,121 +575,113 @@ __global__ void __launch_bounds__(AT_WARPS * 32, 1) kv8_attn_kernel(const AttnP 
         acc.z = fmaf(v.z, f, acc.z);
         acc.w = fmaf(v.w, f, acc.w);
       }
-      const int tok = r_lo + rr / rep, head = g * rep + rr % rep;
-      if (n_split > 1) {
-        const int64_t at = ((int64_t)z * a.n_tokens + tok) * a.n_heads + head;
+      if (!whole) {
+        const int64_t at = ((int64_t)blockIdx.x * 2 + (p_lo == 0)) * R + r;
         *reinterpret_cast<float4*>(P.part_o + at * HD + d) = acc;
         if (d == 0) P.part_ml[at] = make_float2(mx, sum);
       } else {
+        const int tok = r_lo + rr / rep, head = g * rep + rr % rep;
         const float inv = mx == -INFINITY ? 0.0f : 1.0f / sum;
         T* dst = reinterpret_cast<T*>(a.out) + (int64_t)tok * a.out_strides[0] +
                  (int64_t)head * a.out_strides[1] + d;
-        dst[0] = from_f<T>(acc.x * inv);
-        dst[1] = from_f<T>(acc.y * inv);
-        dst[2] = from_f<T>(acc.z * inv);
-        dst[3] = from_f<T>(acc.w * inv);
+        store4(dst, acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
       }
     }
-    __syncthreads();   // exchange area and fac are rewritten by the next row tile
+    __syncthreads();   // exchange area and fac are rewritten by the next run
   }
 }
 
-// Join the splits of a row: one warp per (token, head), lanes over the dims.
-template <typename T, int HD>
+// Joins the partial results of the run around share boundary blockIdx.x + 1,
+// if that is the first boundary inside it: the end of the share before (its
+// slot 1, the run's start), and slot 0 of the shares that follow.  A warp per
+// row, lanes over the dims.
+template <typename T, int HD, int R>
 __global__ void __launch_bounds__(AT_WARPS * 32) kv8_join_kernel(const AttnP P) {
   const fdllm_kv8_attention_args& a = P.a;
-  const int lane = threadIdx.x & 31, seq = blockIdx.y;
-  const int r_lo = min(max(a.starts[seq], 0), a.n_tokens);
-  const int r_hi = min(max(a.starts[seq + 1], r_lo), a.n_tokens);
-  const int L = min(max(a.lens[seq], 0), P.c.max_pages * PAGE);
-  const int keys = split_keys(P, L), n_split = (L + keys - 1) / keys;
-  if (n_split <= 1) return;
-  const int64_t rows = (int64_t)(r_hi - r_lo) * a.n_heads;
-  for (int64_t r = blockIdx.x * AT_WARPS + (threadIdx.x >> 5); r < rows;
-       r += (int64_t)gridDim.x * AT_WARPS) {
-    const int tok = r_lo + (int)(r / a.n_heads), head = (int)(r % a.n_heads);
-    const int64_t row = (int64_t)tok * a.n_heads + head, step = (int64_t)a.n_tokens * a.n_heads;
-    float mx = -INFINITY;
-    for (int z = lane; z < n_split; z += 32) mx = fmaxf(mx, P.part_ml[z * step + row].x);
-    mx = warp_max(mx);
-    float sum = 0.0f, acc[HD / 32];
+  const int lane = threadIdx.x & 31;
+  const int64_t total = total_work(P, R), n_cta = shares(P, total), c = blockIdx.x + 1;
+  bool mine = c < n_cta;
+  int64_t off = 0;
+  const int64_t x = mine ? total * c / n_cta : 0;
+  const int seq = mine ? find_seq(P, R, x, &off) : 0;
+  const Seq sq = seq_of(P, seq, R);
+  const int p = (int)(off % sq.pages), run = (int)(off / sq.pages);
+  mine = mine && p != 0 && total * (c - 1) / n_cta <= x - p;
+  const int64_t run_end = x - p + sq.pages;
+  int n = 1;   // pieces
+  if (mine)
+    while (c + n - 1 < n_cta && total * (c + n - 1) / n_cta < run_end) ++n;
+  const int rep = a.n_heads / P.c.n_kv_heads, g = mine ? run / sq.tiles : 0;
+  const int r = blockIdx.y * AT_WARPS + (threadIdx.x >> 5), rr = mine ? run % sq.tiles * R + r : 0;
+  pdl_wait();   // by every block: this grid must not end before the one that feeds it
+  if (!mine || rr >= sq.rows) return;
+  auto piece = [&](int i) { return ((c - 1 + i) * 2 + (i == 0)) * R + r; };
+  float mx = -INFINITY;
+  for (int i = lane; i < n; i += 32) mx = fmaxf(mx, P.part_ml[piece(i)].x);
+  mx = warp_max(mx);
+  float sum = 0.0f, acc[HD / 32];
 #pragma unroll
-    for (int i = 0; i < HD / 32; ++i) acc[i] = 0.0f;
-    for (int z = 0; z < n_split; ++z) {
-      const float2 ml = P.part_ml[z * step + row];
-      const float f = ml.x == -INFINITY ? 0.0f : ex2(ml.x - mx);
-      sum = fmaf(ml.y, f, sum);
-      const float* po = P.part_o + (z * step + row) * HD;
+  for (int i = 0; i < HD / 32; ++i) acc[i] = 0.0f;
+#pragma unroll 8
+  for (int i = 0; i < n; ++i) {
+    const float2 ml = P.part_ml[piece(i)];
+    const float f = ml.x == -INFINITY ? 0.0f : ex2(ml.x - mx);
+    sum = fmaf(ml.y, f, sum);
+    const float* po = P.part_o + piece(i) * HD;
 #pragma unroll
-      for (int i = 0; i < HD / 32; ++i) acc[i] = fmaf(po[i * 32 + lane], f, acc[i]);
-    }
-    const float inv = mx == -INFINITY ? 0.0f : 1.0f / sum;
-    T* dst = reinterpret_cast<T*>(a.out) + (int64_t)tok * a.out_strides[0] +
-             (int64_t)head * a.out_strides[1];
-#pragma unroll
-    for (int i = 0; i < HD / 32; ++i) dst[i * 32 + lane] = from_f<T>(acc[i] * inv);
+    for (int j = 0; j < HD / 32; ++j) acc[j] = fmaf(po[j * 32 + lane], f, acc[j]);
   }
+  const float inv = mx == -INFINITY ? 0.0f : 1.0f / sum;
+  T* dst = reinterpret_cast<T*>(a.out) + (int64_t)(sq.r_lo + rr / rep) * a.out_strides[0] +
+           (int64_t)(g * rep + rr % rep) * a.out_strides[1];
+#pragma unroll
+  for (int j = 0; j < HD / 32; ++j) dst[j * 32 + lane] = from_f<T>(acc[j] * inv);
 }
 
 struct Plan {
-  int rt, row_tiles, n_split, keys;
+  int rt, n_cta;
   size_t bytes;
 };
 
-// Rows of a CTA and the key split.  Splits are chosen for the fewest key
-// tiles on the busiest SM, a split costing as much as 256 more keys (its
-// start, its exchange and its part of the join).
+// Rows of a tile and the number of shares: two CTAs an SM, fewer when the
+// hints say that there are not MIN_PAGES pages for each.
 Plan plan(const fdllm_kv8& c, const fdllm_kv8_attention_args& a, int num_sms) {
   Plan p{};
   const int64_t most_q = a.max_q > 0 ? std::min(a.max_q, a.n_tokens) : a.n_tokens;
   const int64_t rows = std::max<int64_t>(1, most_q * (a.n_heads / c.n_kv_heads));
   p.rt = a.dtype != FDLLM_DTYPE_F32 && rows > 16 ? 2 : 1;
-  p.row_tiles = (int)std::min<int64_t>((rows + 16 * p.rt - 1) / (16 * p.rt), 65535 / c.n_kv_heads);
   const int64_t table = (int64_t)c.max_pages * PAGE;
   const int64_t len = std::max<int64_t>(1, a.max_len > 0 ? std::min<int64_t>(a.max_len, table) : table);
-  const int64_t units = (int64_t)c.n_seqs * c.n_kv_heads * p.row_tiles;
-  int64_t best = 0, best_cost = -1;
-  for (int64_t s = 1; s <= 256; ++s) {
-    const int64_t keys = ((len + s - 1) / s + PAGE - 1) / PAGE * PAGE;
-    if (s > 1 && keys < 256) break;
-    const int64_t cost = (units * s + num_sms - 1) / num_sms * (keys + 256);
-    if (best_cost < 0 || cost < best_cost) best = s, best_cost = cost;
-  }
-  p.keys = (int)(((len + best - 1) / best + PAGE - 1) / PAGE * PAGE);
-  p.n_split = (int)((len + p.keys - 1) / p.keys);
-  p.bytes = p.n_split > 1
-                ? (size_t)p.n_split * a.n_tokens * a.n_heads * (c.head_dim + 2) * sizeof(float) : 0;
+  const double pages = (double)c.n_seqs * c.n_kv_heads * ((rows + 16 * p.rt - 1) / (16 * p.rt)) *
+                       ((len + PAGE - 1) / PAGE);
+  p.n_cta = (int)std::min<double>(2.0 * num_sms, std::ceil(pages / MIN_PAGES));
+  p.bytes = p.n_cta > 1 ? (size_t)p.n_cta * 2 * 16 * p.rt * (c.head_dim + 2) * sizeof(float) : 0;
   return p;
-}
-
-template <typename K>
-cudaError_t big_smem(K kern, int bytes) {
-  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
 template <typename T, int HD, int RT, bool TWO>
 cudaError_t launch_attn_rt(const AttnP& P, dim3 grid, cudaStream_t st) {
   auto kern = kv8_attn_kernel<T, HD, RT, TWO>;
   constexpr int smem = Lay<HD, RT, TWO>::SMEM;
-  cudaError_t e = big_smem(kern, smem);
+  static std::atomic<uint64_t> ready{0};   // devices whose limit is set
+  cudaError_t e = kv8::allow_smem(kern, smem, ready);
   if (e == cudaSuccess) e = launch_k(false, kern, grid, dim3(AT_WARPS * 32), smem, st, P);
   return e;
 }
 
 template <typename T, int HD>
 cudaError_t launch_attn_hd(const AttnP& P, const Plan& p, cudaStream_t st) {
-  const dim3 grid(p.n_split, P.c.n_kv_heads * p.row_tiles, P.c.n_seqs);
+  const dim3 grid(p.n_cta);
   cudaError_t e;
   if constexpr (std::is_same_v<T, float>)
     e = launch_attn_rt<T, HD, 1, true>(P, grid, st);
   else
     e = p.rt == 1 ? launch_attn_rt<T, HD, 1, false>(P, grid, st)
                   : launch_attn_rt<T, HD, 2, false>(P, grid, st);
-  if (e != cudaSuccess || p.n_split == 1) return e;
-  const int64_t most_q = P.a.max_q > 0 ? std::min(P.a.max_q, P.a.n_tokens) : P.a.n_tokens;
-  const dim3 jgrid((unsigned)std::min<int64_t>((most_q * P.a.n_heads + AT_WARPS - 1) / AT_WARPS, 1 << 20),
-                   P.c.n_seqs);
-  return launch_k(false, kv8_join_kernel<T, HD>, jgrid, dim3(AT_WARPS * 32), 0, st, P);
+  if (e != cudaSuccess || !P.part_o) return e;
+  const dim3 jgrid(p.n_cta - 1, 16 * p.rt / AT_WARPS), block(AT_WARPS * 32);
+  return p.rt == 1 ? launch_k(true, kv8_join_kernel<T, HD, 16>, jgrid, block, 0, st, P)
+                   : launch_k(true, kv8_join_kernel<T, HD, 32>, jgrid, block, 0, st, P);
 }
 
 template <typename T>
@@ -618,13 +705,6 @@ const char* check_args(const fdllm_kv8_attention_args* args, const fdllm_kv8& c)
   return nullptr;
 }
 
-cudaError_t sm_count(int* n) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(n, cudaDevAttrMultiProcessorCount, dev);
-  return e;
-}
-
 }  // namespace
 }  // namespace fd
 
@@ -641,7 +721,7 @@ extern "C" int fdllm_kv8_attention_workspace(const fdllm_kv8* cache,
   if (const char* why = kv8::check_cache(&shape, &c)) return kv8::fail(call, FDLLM_ERR_ARG, why);
   if (const char* why = check_args(args, c)) return kv8::fail(call, FDLLM_ERR_ARG, why);
   int sms = 0;
-  const cudaError_t e = sm_count(&sms);
+  const cudaError_t e = kv8::sm_count(&sms);
   if (e != cudaSuccess) return kv8::fail(call, FDLLM_ERR_CUDA, cudaGetErrorString(e));
   *bytes = plan(c, *args, sms).bytes;
   return FDLLM_OK;
@@ -665,23 +745,17 @@ extern "C" int fdllm_kv8_attention(const fdllm_kv8* cache, const fdllm_kv8_atten
   if (!kv8::rows_ok(a.q, a.q_strides, esz) || !kv8::rows_ok(a.out, a.out_strides, esz))
     return kv8::fail(call, FDLLM_ERR_ARG, "rows and heads of q and out must be 16-byte aligned");
   int sms = 0;
-  cudaError_t e = sm_count(&sms);
+  cudaError_t e = kv8::sm_count(&sms);
   if (e != cudaSuccess) return kv8::fail(call, FDLLM_ERR_CUDA, cudaGetErrorString(e));
-  Plan p = plan(P.c, a, sms);
-  if (!a.workspace && p.n_split > 1) {
-    p.n_split = 1;
-    p.keys = P.c.max_pages * PAGE;
-  }
-  if (p.n_split > 1) {
+  const Plan p = plan(P.c, a, sms);
+  P.n_cta = p.n_cta;
+  if (p.bytes > 0 && a.workspace) {
     if (a.workspace_bytes < p.bytes || !kv8::aligned16(a.workspace))
       return kv8::fail(call, FDLLM_ERR_ARG, "workspace needs " + std::to_string(p.bytes) +
                                                 " bytes, 16-byte aligned");
     P.part_o = static_cast<float*>(a.workspace);
-    P.part_ml = reinterpret_cast<float2*>(
-        P.part_o + (size_t)p.n_split * a.n_tokens * a.n_heads * P.c.head_dim);
+    P.part_ml = reinterpret_cast<float2*>(P.part_o + (size_t)p.n_cta * 2 * 16 * p.rt * P.c.head_dim);
   }
-  P.n_split = p.n_split;
-  P.keys = p.keys;
   cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
   e = a.dtype == FDLLM_DTYPE_F32    ? launch_attn_t<float>(P, p, st)
       : a.dtype == FDLLM_DTYPE_BF16 ? launch_attn_t<__nv_bfloat16>(P, p, st)

@@ -902,7 +902,8 @@ cudaError_t launch_sample(const fdllm_sample_args& a, cudaStream_t st) {
   const int slice = slice_of(c);
   const int smem = (int)sizeof(Shared) + slice * (int)sizeof(T);
   auto kern = sample_kernel<T>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<uint64_t> ready{0};   // devices whose limit is set
+  const cudaError_t e = kv8::allow_smem(kern, 227 << 10, ready);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((int64_t)a.rows * c));

@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 from typing import Dict, Mapping, Optional
 
@@ -163,11 +164,11 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.fdllm_gemm_f16.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, i32]
     lib.fdllm_attention.argtypes = [vp, vp, vp, i32, i32, i32]
     lib.fdllm_gemm_noalloc.argtypes = [vp, vp, vp, i32, i32, i32, i32, vp]
-    lib.fdllm_kv8_append.argtypes = [P(FdllmKv8), P(FdllmKv8AppendArgs), vp]
-    lib.fdllm_kv8_attention.argtypes = [P(FdllmKv8), P(FdllmKv8AttentionArgs), vp]
+    lib.fdllm_kv8_append.argtypes = [vp, vp, vp]        # structs by reference or packed bytes
+    lib.fdllm_kv8_attention.argtypes = [vp, vp, vp]
     lib.fdllm_kv8_attention_workspace.argtypes = [P(FdllmKv8), P(FdllmKv8AttentionArgs),
                                                   P(ctypes.c_size_t)]
-    lib.fdllm_sample.argtypes = [P(FdllmSampleArgs), vp]
+    lib.fdllm_sample.argtypes = [vp, vp]
     lib.fdllm_profile_enable.argtypes = [vp, i32]
     lib.fdllm_profile_read.argtypes = [vp, P(FdllmKernelStat), i32, P(i32)]
     lib.fdllm_last_error.argtypes = [vp]
@@ -435,52 +436,61 @@ KV8_PAGE, KV8_BLOCK = 64, 16              # positions per page, positions that s
 KV8_BAD_PAGE, KV8_BAD_RANGE = 1, 2        # bits of a call's status word
 
 
-def _type_code(t) -> int:
-    import torch
-    code = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}.get(t.dtype)
+# The calls below are short, so their binding is kept short: argument structs
+# are packed in one go, checks read each tensor's attributes once.
+_KV8_APPEND = struct.Struct("@4i3P6q4P2i5P")       # FdllmKv8AppendArgs
+_KV8_ATTENTION = struct.Struct("@5ifP2q3P2qPNP")   # FdllmKv8AttentionArgs
+_SAMPLE = struct.Struct("@Pq4i7P")                 # FdllmSampleArgs
+_types = None                                      # torch dtype -> fdllm_dtype
+
+
+def _type_code(dtype) -> int:
+    global _types
+    if _types is None:
+        import torch
+        _types = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+    code = _types.get(dtype)
     if code is None:
-        raise ValueError(f"{t.dtype} is not a type of this call (float32, bfloat16, float16)")
+        raise ValueError(f"{dtype} is not a type of this call (float32, bfloat16, float16)")
     return code
 
 
-def _same_device(dev: int, **tensors) -> None:
-    for name, t in tensors.items():
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"{name} must be on the same CUDA device as the other operands")
-
-
-def _vector(name: str, t, n: int, dtype) -> None:
-    """An optional contiguous 1-D tensor of n elements."""
-    if t is not None and (t.dtype != dtype or t.dim() != 1 or t.shape[0] != n
-                          or not t.is_contiguous()):
+def _vector(name: str, t, n: int, dtype, dev: int) -> int:
+    """Address of a contiguous 1-D tensor of n elements on device dev."""
+    if t.dtype is not dtype or t.numel() != n or t.dim() != 1 or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} elements")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on the same CUDA device as the other operands")
+    return t.data_ptr()
 
 
-def _rows(name: str, t, heads: Optional[int], hd: int) -> None:
-    if t.dim() != 3 or t.shape[2] != hd or (heads is not None and t.shape[1] != heads) or (
-            t.stride(2) != 1 and t.shape[0] > 0):
+def _rows(name: str, t, tokens: int, heads: Optional[int], hd: int, dtype, dev: int):
+    """(heads, token stride, head stride, address) of [tokens, heads, hd] rows;
+    the strides of dims of one element do not matter."""
+    shape, st = t.shape, t.stride()
+    if len(shape) != 3 or shape[2] != hd or (heads is not None and shape[1] != heads) or (
+            st[2] != 1 and shape[0] > 0):
         raise ValueError(f"{name} must be [tokens, {heads or 'heads'}, {hd}] with contiguous vectors")
+    if shape[0] != tokens or t.dtype is not dtype:
+        raise ValueError("all rows of a call must have the same number of tokens and the same type")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on the same CUDA device as the other operands")
+    return shape[1], st[0] if tokens > 1 else 0, st[1] if shape[1] > 1 else 0, t.data_ptr()
 
 
-def _strides(t):
-    """Token and head strides; those of dims of one element do not matter."""
-    return (t.stride(0) if t.shape[0] > 1 else 0, t.stride(1) if t.shape[1] > 1 else 0)
-
-
-def _enqueue(dev: int, stream, call) -> int:
-    """call(stream handle) with `dev` current; stream None = torch's current
-    stream there."""
+def _enqueue(fn, dev: int, stream, *args) -> None:
+    """fn(*args, stream handle) with `dev` current; stream None = torch's
+    current stream there."""
     import torch
     if stream is None:
         stream = torch._C._cuda_getCurrentRawStream(dev)
     if torch._C._cuda_getDevice() == dev:
-        return call(stream)
-    with torch.cuda.device(dev):
-        return call(stream)
-
-
-def _ptr(t):
-    return None if t is None else t.data_ptr()
+        rc = fn(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, stream)
+    if rc != FDLLM_OK:
+        _check(rc, None)
 
 
 class Kv8Cache:
@@ -509,7 +519,8 @@ class Kv8Cache:
         self.device = k.get_device()
         if self.device < 0:
             raise ValueError("the cache must be on a CUDA device")
-        _same_device(self.device, v=v, k_scale=k_scale, v_scale=v_scale, page_table=page_table)
+        if any(t.get_device() != self.device for t in (v, k_scale, v_scale, page_table)):
+            raise ValueError("the cache's tensors must be on one CUDA device")
         self.k, self.v, self.k_scale, self.v_scale, self.page_table = k, v, k_scale, v_scale, page_table
         self.n_seqs, self.max_pages = page_table.shape
         self.n_kv_heads, self.head_dim = heads, hd
@@ -519,6 +530,7 @@ class Kv8Cache:
             page_table.data_ptr(), k.stride(0) if n_pages > 1 else 0,
             k_scale.stride(0) if n_pages > 1 else 0, 0 if one_row else page_table.stride(0),
             n_pages, self.n_seqs, self.max_pages, heads, hd)
+        self._ref = ctypes.byref(self.struct)
         self._workspace: Dict[tuple, int] = {}   # bytes by shape, not memory
 
 
@@ -531,40 +543,35 @@ def fdllm_kv8_append(cache: Kv8Cache, k, v, starts, lens, pos=None, rope=None, q
     rotated q (None without q) and, with stored, the rows as the cache now
     stands for them (else None, None)."""
     import torch
-    hd, dev = cache.head_dim, cache.device
-    _rows("k", k, cache.n_kv_heads, hd)
-    _rows("v", v, cache.n_kv_heads, hd)
-    T = k.shape[0]
-    if v.shape[0] != T or v.dtype != k.dtype or (
-            q is not None and (q.shape[0] != T or q.dtype != k.dtype)):
-        raise ValueError("k, v and q must have the same number of rows and the same type")
-    i32 = torch.int32
-    _vector("starts", starts, cache.n_seqs + 1, i32)
-    _vector("lens", lens, cache.n_seqs, i32)
-    _vector("pos", pos, cache.n_seqs, i32)
-    _vector("lens_out", lens_out, cache.n_seqs, i32)
-    _vector("status", status, 1, i32)
-    if rope is not None and (rope.dtype != torch.float32 or rope.dim() != 3 or
-                             tuple(rope.shape[1:]) != (hd // 2, 2) or not rope.is_contiguous()):
-        raise ValueError(f"rope must be contiguous float32 [positions, {hd // 2}, 2]")
-    _same_device(dev, k=k, v=v, q=q, starts=starts, lens=lens, pos=pos, rope=rope,
-                 lens_out=lens_out, status=status)
+    hd, dev, n, i32, dtype, T = (cache.head_dim, cache.device, cache.n_seqs, torch.int32, k.dtype,
+                                 k.shape[0])
+    _, k_token, k_head, k_ptr = _rows("k", k, T, cache.n_kv_heads, hd, dtype, dev)
+    _, v_token, v_head, v_ptr = _rows("v", v, T, cache.n_kv_heads, hd, dtype, dev)
+    heads = q_token = q_head = q_ptr = q_out_ptr = k_out_ptr = v_out_ptr = rope_ptr = rope_len = 0
     q_out = k_out = v_out = None
     if q is not None:
-        _rows("q", q, None, hd)
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        heads, q_token, q_head, q_ptr = _rows("q", q, T, None, hd, dtype, dev)
+        q_out = q.new_empty(q.shape)
+        q_out_ptr = q_out.data_ptr()
     if stored:
-        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-        v_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-    ks, vs, qs = _strides(k), _strides(v), _strides(q) if q is not None else (0, 0)
-    a = FdllmKv8AppendArgs(
-        _type_code(k), T, q.shape[1] if q is not None else 0, max_new, k.data_ptr(), v.data_ptr(),
-        _ptr(q), ks[0], ks[1], vs[0], vs[1], qs[0], qs[1], _ptr(starts), _ptr(lens), _ptr(pos),
-        _ptr(rope), rope.shape[0] if rope is not None else 0, 0, _ptr(k_out), _ptr(v_out),
-        _ptr(q_out), _ptr(lens_out), _ptr(status))
-    lib = load_library()
-    _check(_enqueue(dev, stream, lambda s: lib.fdllm_kv8_append(
-        ctypes.byref(cache.struct), ctypes.byref(a), s)), None)
+        both = k.new_empty((2,) + tuple(k.shape))
+        k_out, v_out = both.unbind()
+        k_out_ptr = both.data_ptr()
+        v_out_ptr = k_out_ptr + k.numel() * k.element_size()
+    if rope is not None:
+        rope_len = rope.shape[0]
+        if rope.dtype is not torch.float32 or tuple(rope.shape[1:]) != (hd // 2, 2) or \
+                not rope.is_contiguous() or rope.get_device() != dev:
+            raise ValueError(f"rope must be contiguous float32 [positions, {hd // 2}, 2] on the "
+                             "cache's device")
+        rope_ptr = rope.data_ptr()
+    a = _KV8_APPEND.pack(
+        _type_code(dtype), T, heads, max_new, k_ptr, v_ptr, q_ptr, k_token, k_head, v_token, v_head,
+        q_token, q_head, _vector("starts", starts, n + 1, i32, dev), _vector("lens", lens, n, i32, dev),
+        0 if pos is None else _vector("pos", pos, n, i32, dev), rope_ptr, rope_len, 0, k_out_ptr,
+        v_out_ptr, q_out_ptr, 0 if lens_out is None else _vector("lens_out", lens_out, n, i32, dev),
+        0 if status is None else _vector("status", status, 1, i32, dev))
+    _enqueue(load_library().fdllm_kv8_append, dev, stream, cache._ref, a)
     return q_out, k_out, v_out
 
 
@@ -577,32 +584,30 @@ def fdllm_kv8_attention(cache: Kv8Cache, q, starts, lens, scale: Optional[float]
     fdllm_kv8_attention_workspace); pass one when the work is enqueued on a
     stream that is not torch's current one."""
     import torch
-    hd, dev = cache.head_dim, cache.device
-    _rows("q", q, None, hd)
+    hd, dev, n, i32, dtype, T = (cache.head_dim, cache.device, cache.n_seqs, torch.int32, q.dtype,
+                                 q.shape[0])
+    heads, q_token, q_head, q_ptr = _rows("q", q, T, None, hd, dtype, dev)
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        out = q.new_empty(q.shape)
+        out_token, out_head, out_ptr = heads * hd, hd, out.data_ptr()
     else:
-        _rows("out", out, q.shape[1], hd)
-        if out.dtype != q.dtype or out.shape[0] != q.shape[0]:
-            raise ValueError("out must have q's shape and type")
-    _vector("starts", starts, cache.n_seqs + 1, torch.int32)
-    _vector("lens", lens, cache.n_seqs, torch.int32)
-    _vector("status", status, 1, torch.int32)
-    _same_device(dev, q=q, starts=starts, lens=lens, out=out, workspace=workspace, status=status)
-    qs, os_ = _strides(q), _strides(out)
-    a = FdllmKv8AttentionArgs(
-        _type_code(q), q.shape[0], q.shape[1], max_q, max_len,
-        hd ** -0.5 if scale is None else scale, q.data_ptr(), qs[0], qs[1], starts.data_ptr(),
-        lens.data_ptr(), out.data_ptr(), os_[0], os_[1], None, 0, _ptr(status))
+        _, out_token, out_head, out_ptr = _rows("out", out, T, heads, hd, dtype, dev)
+    ws_ptr = ws_bytes = 0
     if workspace is None:
-        need = fdllm_kv8_attention_workspace(cache, q.shape[0], q.shape[1], q.dtype, max_q, max_len)
-        if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    if workspace is not None:
-        a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel()
-    lib = load_library()
-    _check(_enqueue(dev, stream, lambda s: lib.fdllm_kv8_attention(
-        ctypes.byref(cache.struct), ctypes.byref(a), s)), None)
+        ws_bytes = fdllm_kv8_attention_workspace(cache, T, heads, dtype, max_q, max_len)
+        if ws_bytes:
+            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
+            ws_ptr = workspace.data_ptr()
+    else:
+        if workspace.get_device() != dev or not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous and on the cache's device")
+        ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    a = _KV8_ATTENTION.pack(
+        _type_code(dtype), T, heads, max_q, max_len, hd ** -0.5 if scale is None else scale, q_ptr,
+        q_token, q_head, _vector("starts", starts, n + 1, i32, dev),
+        _vector("lens", lens, n, i32, dev), out_ptr, out_token, out_head, ws_ptr, ws_bytes,
+        0 if status is None else _vector("status", status, 1, i32, dev))
+    _enqueue(load_library().fdllm_kv8_attention, dev, stream, cache._ref, a)
     return out
 
 
@@ -610,19 +615,18 @@ def fdllm_kv8_attention_workspace(cache: Kv8Cache, n_tokens: int, n_heads: int, 
                                   max_q: int = 0, max_len: int = 0) -> int:
     """Bytes of workspace for an attention call of this shape (remembered by
     the cache object)."""
-    import torch
     key = (n_tokens, n_heads, dtype, max_q, max_len)
     need = cache._workspace.get(key)
     if need is None:
-        a = FdllmKv8AttentionArgs(_type_code(torch.empty(0, dtype=dtype)), n_tokens, n_heads, max_q,
-                                  max_len, 1.0)
-        n = ctypes.c_size_t()
-        lib = load_library()
-        _check(_enqueue(cache.device, 0, lambda s: lib.fdllm_kv8_attention_workspace(
-            ctypes.byref(cache.struct), ctypes.byref(a), ctypes.byref(n))), None)
+        import torch
+        a = FdllmKv8AttentionArgs(_type_code(dtype), n_tokens, n_heads, max_q, max_len, 1.0)
+        size = ctypes.c_size_t()
+        with torch.cuda.device(cache.device):
+            _check(load_library().fdllm_kv8_attention_workspace(cache._ref, ctypes.byref(a),
+                                                                ctypes.byref(size)), None)
         if len(cache._workspace) >= 256:
             cache._workspace.clear()
-        need = cache._workspace[key] = n.value
+        need = cache._workspace[key] = size.value
     return need
 
 
@@ -633,31 +637,25 @@ def fdllm_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None
     top_k: int32 [rows] or None.  Returns (tok int32 [rows], prob float32
     [rows])."""
     import torch
-    if logits.dim() != 2 or (logits.stride(1) != 1 and logits.shape[1] > 1):
+    shape, st, dev, f32 = logits.shape, logits.stride(), logits.get_device(), torch.float32
+    if len(shape) != 2 or (st[1] != 1 and shape[1] > 1):
         raise ValueError("logits must be [rows, vocab] with contiguous rows")
-    rows, vocab = logits.shape
-    dev = logits.get_device()
     if dev < 0:
         raise ValueError("logits must be on a CUDA device")
-    f32 = torch.float32
-    _vector("u", u, rows, torch.float64)
-    _vector("temperature", temperature, rows, f32)
-    _vector("top_k", top_k, rows, torch.int32)
-    _vector("top_p", top_p, rows, f32)
-    _vector("min_p", min_p, rows, f32)
-    _vector("tok", tok, rows, torch.int32)
-    _vector("prob", prob, rows, f32)
-    _same_device(dev, u=u, temperature=temperature, top_k=top_k, top_p=top_p, min_p=min_p, tok=tok,
-                 prob=prob)
+    rows, vocab = shape
     if tok is None:
         tok = torch.empty(rows, dtype=torch.int32, device=logits.device)
     if prob is None:
         prob = torch.empty(rows, dtype=f32, device=logits.device)
-    a = FdllmSampleArgs(logits.data_ptr(), logits.stride(0) if rows > 1 else vocab,
-                        _type_code(logits), rows, vocab, mask_id, _ptr(temperature), _ptr(top_k),
-                        _ptr(top_p), _ptr(min_p), u.data_ptr(), tok.data_ptr(), prob.data_ptr())
-    lib = load_library()
-    _check(_enqueue(dev, stream, lambda s: lib.fdllm_sample(ctypes.byref(a), s)), None)
+    a = _SAMPLE.pack(
+        logits.data_ptr(), st[0] if rows > 1 else vocab, _type_code(logits.dtype), rows, vocab, mask_id,
+        0 if temperature is None else _vector("temperature", temperature, rows, f32, dev),
+        0 if top_k is None else _vector("top_k", top_k, rows, torch.int32, dev),
+        0 if top_p is None else _vector("top_p", top_p, rows, f32, dev),
+        0 if min_p is None else _vector("min_p", min_p, rows, f32, dev),
+        _vector("u", u, rows, torch.float64, dev), _vector("tok", tok, rows, torch.int32, dev),
+        _vector("prob", prob, rows, f32, dev))
+    _enqueue(load_library().fdllm_sample, dev, stream, a)
     return tok, prob
 
 

@@ -134,6 +134,7 @@ def test_struct_sizes_match_the_header(tmp_path):
                      (fdllm.FdllmKv8AttentionArgs, "status"), (fdllm.FdllmSampleArgs, "prob")):
         want += [ctypes.sizeof(st), getattr(st, last).offset]
     assert got == want
+    assert [x.size for x in (fdllm._KV8_APPEND, fdllm._KV8_ATTENTION, fdllm._SAMPLE)] == want[2::2]
 
 
 def test_binding_refuses_cpu_tensors_and_wrong_shapes():
