@@ -61,6 +61,8 @@ HEADS = [(4, 4, 32), (8, 2, 64), (8, 8, 128), (28, 4, 128), (16, 1, 128), (6, 2,
     ([32], [577]),                               # a diffusion block
     ([3, 0, 17, 1], [63, 64, 65, 1300]),         # pages, an idle slot
     ([70], [129]),                               # several row tiles
+    ([8, 2, 40], [700, 0, 128]),                 # up to 64 and 128 rows a K/V head
+    ([150], [333]),                              # prompt-sized
 ])
 def test_attention(dtype, hq, hkv, hd, rows, lens):
     g = torch.Generator().manual_seed(sum(rows) + 7 * sum(lens) + hq + hd)
