@@ -455,7 +455,7 @@ Plan plan(const fdllm_kv8& c, const fdllm_kv8_attention_args& a, int num_sms) {
   const double pages = (double)c.n_seqs * c.n_kv_heads * ((rows + p.tile_rows - 1) / p.tile_rows) *
                        (RUN_START + (len + PAGE - 1) / PAGE);
   const double most = (tc ? tc_ctas_per_sm(p.tile_rows) : 2) * (double)num_sms;
-  p.n_cta = (int)std::min(most, std::ceil(pages / (RUN_START + MIN_PAGES)));
+  p.n_cta = (int)std::min(most, std::ceil(pages / MIN_PAGES));
   p.bytes = p.n_cta > 1 ? (size_t)p.n_cta * 2 * p.tile_rows * (c.head_dim + 2) * sizeof(float) : 0;
   return p;
 }

@@ -24,7 +24,7 @@ namespace kv8 {
 
 constexpr int PAGE = FDLLM_KV8_PAGE;
 constexpr int RUN_START = 3;
-constexpr int MIN_PAGES = 2;         // of a share, at least
+constexpr int MIN_PAGES = 2;         // of a share, at least (counting run starts)
 constexpr float W_EXP = 8.0f;        // largest softmax weights are about 2^W_EXP
 constexpr float M_SLACK = 7.0f;      // the reference moves when the max passes it by this
 constexpr float LOG2E = 1.4426950408889634f;
@@ -57,35 +57,41 @@ FD_DEV Seq seq_of(const AttnP& P, int i, int tile_rows) {
   s.work = (int64_t)s.tiles * P.c.n_kv_heads * s.span;
   return s;
 }
-// Sum of all sequences' work, by a warp.
-FD_DEV int64_t total_work(const AttnP& P, int tile_rows) {
+// The work of sequences i0 + lane, summed up to each lane, by a warp.
+FD_DEV int64_t scan_work(const AttnP& P, int tile_rows, int i0, int64_t* own) {
   const int lane = threadIdx.x & 31;
-  int64_t t = 0;
-  for (int i = lane; i < P.c.n_seqs; i += 32) t += seq_of(P, i, tile_rows).work;
+  int64_t w = i0 + lane < P.c.n_seqs ? seq_of(P, i0 + lane, tile_rows).work : 0;
+  *own = w;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, w, o);
+    if (lane >= o) w += y;
+  }
+  return w;
+}
+// All sequences' work; the first 32 sequences' scan stays in upto, own.
+FD_DEV int64_t total_work(const AttnP& P, int tile_rows, int64_t* upto, int64_t* own) {
+  *upto = scan_work(P, tile_rows, 0, own);
+  int64_t t = __shfl_sync(0xffffffffu, *upto, 31);
+  for (int i0 = 32; i0 < P.c.n_seqs; i0 += 32) {
+    int64_t w;
+    t += __shfl_sync(0xffffffffu, scan_work(P, tile_rows, i0, &w), 31);
+  }
   return t;
 }
 // The sequence that holds position x < total, by a warp; *off: the place
-// within it.
-FD_DEV int find_seq(const AttnP& P, int tile_rows, int64_t x, int64_t* off) {
-  const int lane = threadIdx.x & 31;
+// within it.  upto, own: from total_work.
+FD_DEV int find_seq(const AttnP& P, int tile_rows, int64_t x, int64_t upto, int64_t own, int64_t* off) {
   int64_t base = 0;
-  for (int i0 = 0;; i0 += 32) {
-    const int64_t w = i0 + lane < P.c.n_seqs ? seq_of(P, i0 + lane, tile_rows).work : 0;
-    int64_t upto = w;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, upto, o);
-      if (lane >= o) upto += y;
-    }
+  for (int i0 = 0;;) {
     const uint32_t hit = __ballot_sync(0xffffffffu, base + upto > x);
     if (hit || i0 + 32 >= P.c.n_seqs) {
       const int l = hit ? __ffs(hit) - 1 : 0;
-      *off = x - base - __shfl_sync(0xffffffffu, upto - w, l);
+      *off = x - base - __shfl_sync(0xffffffffu, upto - own, l);
       return i0 + l;
     }
     base += __shfl_sync(0xffffffffu, upto, 31);
+    upto = scan_work(P, tile_rows, i0 += 32, &own);
   }
 }
 // Division of what nearly always fits 32 bits.
@@ -99,7 +105,7 @@ struct Shares {
 };
 FD_DEV Shares shares_of(const AttnP& P, int64_t total) {
   Shares s;
-  s.n = max((int64_t)1, min((int64_t)P.n_cta, total / (MIN_PAGES + RUN_START)));
+  s.n = max((int64_t)1, min((int64_t)P.n_cta, total / MIN_PAGES));
   s.each = div64(total, s.n);
   s.rest = total - s.each * s.n;
   return s;
@@ -119,13 +125,14 @@ struct Walk {
     tile_rows = rows_of_tile;
     x = x_end = off = 0;
     seq = 0;
-    const int64_t total = total_work(P, tile_rows);
+    int64_t upto, own;
+    const int64_t total = total_work(P, tile_rows, &upto, &own);
     const Shares sh = shares_of(P, total);
     if (blockIdx.x >= sh.n) return;
     x = sh.begin(blockIdx.x);
     x_end = sh.begin(blockIdx.x + 1);
     if (x >= x_end) return;
-    seq = find_seq(P, tile_rows, x, &off);
+    seq = find_seq(P, tile_rows, x, upto, own, &off);
     sq = seq_of(P, seq, tile_rows);
     const int p = (int)(off - div64(off, sq.span) * sq.span);
     if (!P.part_o && p > 0) {   // whole runs: those that start in the share
@@ -219,12 +226,13 @@ template <typename T, int HD, int R>
 __global__ void __launch_bounds__(JOIN_WARPS * 32) kv8_join_kernel(const AttnP P) {
   const fdllm_kv8_attention_args& a = P.a;
   const int lane = threadIdx.x & 31;
-  const Shares sh = shares_of(P, total_work(P, R));
+  int64_t upto, own;
+  const Shares sh = shares_of(P, total_work(P, R, &upto, &own));
   const int64_t c = blockIdx.x + 1;
   bool mine = c < sh.n;
   int64_t off = 0;
   const int64_t x = mine ? sh.begin(c) : 0;
-  const int seq = mine ? find_seq(P, R, x, &off) : 0;
+  const int seq = mine ? find_seq(P, R, x, upto, own, &off) : 0;
   const Seq sq = seq_of(P, seq, R);
   const int run = (int)div64(off, sq.span), p = (int)(off - (int64_t)run * sq.span);
   mine = mine && p > RUN_START && sh.begin(c - 1) <= x - p + RUN_START;

@@ -49,7 +49,8 @@ struct TcLay {
   // scales of a tile, by its parity: ks, log2 vs, 1 / vs of 8 blocks
   static constexpr int SC_OFF = Q_OFF + NQ * MAT;
   static constexpr int ML_OFF = SC_OFF + 2 * 3 * NB * 4;   // copies' (max, sum) [128]
-  static constexpr int BAR_OFF = ML_OFF + 128 * 8;
+  static constexpr int RF_OFF = ML_OFF + 128 * 8;          // row factors
+  static constexpr int BAR_OFF = RF_OFF + NQ * 128 * 4;
   static constexpr int MISC_OFF = BAR_OFF + 32 * 8;
   static constexpr int SMEM = MISC_OFF + 16 + 1024;   // slack for 1024-byte alignment
   static constexpr int THREADS = 128 * NQ + CONV;
@@ -66,6 +67,14 @@ FD_DEV void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+// (a, b) = (a, b) * f + g, one instruction.
+FD_DEV void fma2(float& a, float& b, float f, float g) {
+  asm("{\n\t.reg .b64 x, y, z;\n\t"
+      "mov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %2};\n\tmov.b64 z, {%3, %3};\n\t"
+      "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "+f"(a), "+f"(b)
+      : "f"(f), "f"(g));
 }
 // 16 TMEM columns of this warp's lanes.
 FD_DEV void tmem_st16(uint32_t taddr, const uint32_t* v) {
@@ -144,6 +153,7 @@ __global__ void __launch_bounds__(TcLay<HD, NQ>::THREADS, NQ == 1 ? 2 : 1)
     const uint32_t o_col = s_col + NQ * 128;
     uint8_t* qs = smem + L::Q_OFF + q * L::MAT;
     float2* ml = reinterpret_cast<float2*>(smem + L::ML_OFF);
+    float* rfs = reinterpret_cast<float*>(smem + L::RF_OFF);
     const uint32_t kb = smem_u32(smem + L::K_OFF), vb = smem_u32(smem + L::V_OFF), qb = smem_u32(qs);
     // the MMAs of this row tile, by warp 0 of its four: S of tile n; w V of tile n
     auto scores = [&](int n) {
@@ -151,11 +161,12 @@ __global__ void __launch_bounds__(TcLay<HD, NQ>::THREADS, NQ == 1 ? 2 : 1)
       wait(&k_full[st], (n / L::STAGES) & 1);
       if (ok && lane == 0) {
         tc_fence_after();
+        // a step along K moves the descriptors' start address (in 16 bytes)
+        const uint64_t qd = smem_desc_sw128(qb), kd = smem_desc_sw128(kb + st * L::MAT);
 #pragma unroll
         for (int k = 0; k < HD / 16; ++k) {
-          const uint32_t off = (k >> 2) * L::SUB + (k & 3) * 32;
-          tc_mma(tmem + q * 128, smem_desc_sw128(qb + off), smem_desc_sw128(kb + st * L::MAT + off),
-                 idesc_f32acc(KEYS, true), k > 0);
+          const uint32_t off = ((k >> 2) * L::SUB + (k & 3) * 32) >> 4;
+          tc_mma(tmem + q * 128, qd + off, kd + off, idesc_f32acc(KEYS, true), k > 0);
         }
         tc_commit(&s_full[q]);
         tc_commit(&k_free[st]);
@@ -167,10 +178,10 @@ __global__ void __launch_bounds__(TcLay<HD, NQ>::THREADS, NQ == 1 ? 2 : 1)
       wait(&v_full[st], (n / L::STAGES) & 1);
       if (ok && lane == 0) {
         tc_fence_after();
+        const uint64_t vd = smem_desc_sw128_mn(vb + st * L::MAT, L::SUB, 1024);
 #pragma unroll
         for (int k = 0; k < KEYS / 16; ++k)
-          tc_mma_ts(tmem + (NQ + q) * 128, tmem + q * 128 + k * 8,
-                    smem_desc_sw128_mn(vb + st * L::MAT + k * 2048, L::SUB, 1024),
+          tc_mma_ts(tmem + (NQ + q) * 128, tmem + q * 128 + k * 8, vd + (k * 2048 >> 4),
                     idesc_f32acc_bmn(HD, true), !first || k > 0);
         tc_commit(&v_free[st]);
         if (last) tc_commit(&o_full[q]);
@@ -182,41 +193,50 @@ __global__ void __launch_bounds__(TcLay<HD, NQ>::THREADS, NQ == 1 ? 2 : 1)
       const int rows = walk.sq.rows, rr = sg.row0 + r;
       const int k_lo = sg.p_lo * PAGE, k_hi = min(walk.sq.len, sg.p_hi * PAGE);
       const int tiles = (k_hi - k_lo + KEYS - 1) / KEYS;
-      // ---- q row, scaled by a power of two, into the swizzled A tile
-      float rf;
+      // ---- q, scaled per row by a power of two, into the swizzled A tile: HD / 8
+      // lanes a row, 16 bytes each; every warp a quarter of the rows, all copies
       {
-        uint4 raw[HD / 8];
-        const bool have = rr < rows;
-        const T* src = reinterpret_cast<const T*>(a.q) +
-                       (int64_t)(walk.sq.r_lo + (have ? rr / rep : 0)) * a.q_strides[0] +
-                       (int64_t)(sg.g * rep + (have ? rr % rep : 0)) * a.q_strides[1];
+        constexpr int LR = HD / 8, RPW = 128 / C / 4, STEP = 32 / LR, N = RPW / STEP;
+        const int ch = lane % LR, row_a = quad * RPW + lane / LR;   // row of the MMA tile
+        const int first = sg.row0 + q * 128 + row_a;
+        int token = first / rep, head = first % rep;
+        uint4 raw[N];
 #pragma unroll
-        for (int j = 0; j < HD / 8; ++j)
-          raw[j] = have ? reinterpret_cast<const uint4*>(src)[j] : make_uint4(0, 0, 0, 0);
-        float top = 0.0f;
+        for (int j = 0; j < N; ++j) {
+          raw[j] = make_uint4(0, 0, 0, 0);
+          if (first + j * STEP < rows)
+            raw[j] = *reinterpret_cast<const uint4*>(
+                reinterpret_cast<const T*>(a.q) + (int64_t)(walk.sq.r_lo + token) * a.q_strides[0] +
+                (int64_t)(sg.g * rep + head) * a.q_strides[1] + ch * 8);
+          for (head += STEP; head >= rep; head -= rep) ++token;
+        }
 #pragma unroll
-        for (int j = 0; j < HD / 8; ++j) {
+        for (int j = 0; j < N; ++j) {
           const T* e = reinterpret_cast<const T*>(&raw[j]);
+          float top = 0.0f;
 #pragma unroll
           for (int m = 0; m < 8; ++m) top = fmaxf(top, fabsf(to_f<T>(e[m])));
-        }
-        const int up = q_shift(top);
-        const float mul = exp2_int(up);
-        rf = a.scale * LOG2E * exp2_int(-up);
 #pragma unroll
-        for (int j = 0; j < HD / 8; ++j) {
-          const T* e = reinterpret_cast<const T*>(&raw[j]);
+          for (int o = LR / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+          const int up = q_shift(top), row = row_a + j * STEP;
+          const float mul = exp2_int(up);
           uint32_t h[4];
 #pragma unroll
           for (int m = 0; m < 4; ++m)
             h[m] = pack_h2(to_f<T>(e[2 * m]) * mul, to_f<T>(e[2 * m + 1]) * mul);
-          *reinterpret_cast<uint4*>(qs + (j >> 3) * L::SUB + i * 128 + (((j & 7) ^ (i & 7)) << 4)) =
-              make_uint4(h[0], h[1], h[2], h[3]);
+#pragma unroll
+          for (int k = 0; k < C; ++k) {
+            const int at = k * (128 / C) + row;
+            *reinterpret_cast<uint4*>(qs + (ch >> 3) * L::SUB + at * 128 + (((ch & 7) ^ (at & 7)) << 4)) =
+                make_uint4(h[0], h[1], h[2], h[3]);
+          }
+          if (ch == 0) rfs[q * 128 + row] = a.scale * LOG2E * exp2_int(-up);
         }
         fence_proxy_async_smem();
         named_bar(1 + q, 128);
         if (quad == 0 && tiles > 0) scores(n_tile);
       }
+      const float rf = rfs[r];
       float M = -INFINITY, l = 0.0f;
       for (int t = 0; t < tiles; ++t, ++n_tile) {
         const int k0 = k_lo + t * KEYS + copy * NC;   // first key of this thread's columns
@@ -229,19 +249,27 @@ __global__ void __launch_bounds__(TcLay<HD, NQ>::THREADS, NQ == 1 ? 2 : 1)
           const bool tail = k0 + NC > k_hi;
           const uint32_t col = s_col + copy * NC;
           float v[32], mx = -INFINITY;
-#pragma unroll
-          for (int c0 = 0; c0 < NC; c0 += 32) {
+          // t of 32 columns from c0 on, shifted by add; columns behind the run's
+          // last key are -inf
+          auto read = [&](int c0, float add) {
             tmem_ld32(col + c0, v);
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
-              const float f = rf * sc[c0 / 16 + b], lv = sc[NB + c0 / 16 + b];
+              const float f = rf * sc[c0 / 16 + b], g = sc[NB + c0 / 16 + b] + add;
 #pragma unroll
-              for (int j = 16 * b; j < 16 * b + 16; ++j) {
-                v[j] = fmaf(v[j], f, lv);
-                if (tail && k0 + c0 + j >= k_hi) v[j] = -INFINITY;
-                mx = fmaxf(mx, v[j]);
-              }
+              for (int j = 16 * b; j < 16 * b + 16; j += 2) fma2(v[j], v[j + 1], f, g);
             }
+            if (tail) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (k0 + c0 + j >= k_hi) v[j] = -INFINITY;
+            }
+          };
+#pragma unroll
+          for (int c0 = 0; c0 < NC; c0 += 32) {
+            read(c0, 0.0f);
+#pragma unroll
+            for (int j = 0; j < 32; j += 2) mx = fmaxf(fmaxf(mx, v[j]), v[j + 1]);
           }
           float alpha = 1.0f;
           const bool move = mx > M + M_SLACK || (M == -INFINITY && mx > -INFINITY);
@@ -255,23 +283,17 @@ __global__ void __launch_bounds__(TcLay<HD, NQ>::THREADS, NQ == 1 ? 2 : 1)
           for (int c0 = 0; c0 < NC; c0 += 32) {
             uint32_t w[16];
             if (NC > 32) {   // the registers hold one chunk only: read the scores again
-              tmem_ld32(col + c0, v);
+              read(c0, ref);
+            } else {
 #pragma unroll
-              for (int b = 0; b < 2; ++b) {
-                const float f = rf * sc[c0 / 16 + b], lv = sc[NB + c0 / 16 + b];
-#pragma unroll
-                for (int j = 16 * b; j < 16 * b + 16; ++j) {
-                  v[j] = fmaf(v[j], f, lv);
-                  if (tail && k0 + c0 + j >= k_hi) v[j] = -INFINITY;
-                }
-              }
+              for (int j = 0; j < 32; ++j) v[j] += ref;
             }
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
               float part = 0.0f;
 #pragma unroll
               for (int j = 16 * b; j < 16 * b + 16; j += 2) {
-                const float e0 = ex2(v[j] + ref), e1 = ex2(v[j + 1] + ref);
+                const float e0 = ex2(v[j]), e1 = ex2(v[j + 1]);
                 part += e0 + e1;
                 w[j / 2] = pack_h2(e0, e1);
               }
@@ -404,96 +426,103 @@ __global__ void __launch_bounds__(TcLay<HD, NQ>::THREADS, NQ == 1 ? 2 : 1)
   } else {
     // ================================================== converters
     const int ct = tid - 128 * NQ;
-    constexpr int RB = HD / 16;              // 16-byte chunks of a key
-    constexpr int PER = KEYS * RB / CONV;    // chunks of a thread
+    constexpr int HALVES = HD / 64;            // 64-byte halves of a key
+    constexpr int PER = KEYS / 32 * HALVES;    // 16-byte chunks of a thread
+    // 4 lanes take 64 bytes of a key: the 8 lanes of a store then have an
+    // even and an odd row, whose swizzled chunks are on different banks
+    const int row0 = ct >> 2, ch = ct & 3;
     int n_tile = 0;
     while (walk.next(P, &sg)) {
       const int32_t* table = c.page_table + (int64_t)sg.seq * c.table_stride;
       const int k_lo = sg.p_lo * PAGE, k_hi = min(walk.sq.len, sg.p_hi * PAGE);
       const int tiles = (k_hi - k_lo + KEYS - 1) / KEYS;
       uint4 kr[PER], vr[PER];
-      int page0 = -1, page1 = -1;
-      // page ids of tile t; -1: none, or outside the pool
-      auto page_at = [&](int k) {
-        if (k >= k_hi) return -1;
-        const int p = table[k / PAGE];
-        if (p >= 0 && p < c.n_pages) return p;
-        if (ct == 0 && a.status) atomicOr(a.status, FDLLM_KV8_BAD_PAGE);
-        return -1;
-      };
-      auto pages_of = [&](int t) {
-        page0 = page_at(k_lo + t * KEYS);
-        page1 = page_at(k_lo + t * KEYS + PAGE);
+      float ks = 0.0f, vs = -1.0f;             // scales of block ct (vs < 0: no key)
+      int page0 = -1, page1 = -1, next0 = -1, next1 = -1;
+      // page id of key k, as the table has it; -1 behind the run's end
+      auto page_at = [&](int k) { return k < k_hi ? table[k / PAGE] : -1; };
+      auto next_pages = [&](int t) {   // of tile t, from the ids asked for one tile before
+        page0 = next0;
+        page1 = next1;
+        const int k = k_lo + t * KEYS;
+        if (k < k_hi && (page0 < 0 || page0 >= c.n_pages || (k + PAGE < k_hi && (page1 < 0 || page1 >= c.n_pages)))) {
+          if (ct == 0 && a.status) atomicOr(a.status, FDLLM_KV8_BAD_PAGE);
+        }
+        if (page0 >= c.n_pages) page0 = -1;
+        if (page1 >= c.n_pages) page1 = -1;
+        next0 = page_at(k + KEYS);
+        next1 = page_at(k + KEYS + PAGE);
       };
       auto load = [&](const int8_t* pool, uint4* x) {
+        const int8_t* base = pool + ((int64_t)sg.g * PAGE + row0) * HD + ch * 16;
+        const int8_t* p0 = base + (int64_t)page0 * c.page_stride;
+        const int8_t* p1 = base + (int64_t)page1 * c.page_stride;
 #pragma unroll
         for (int j = 0; j < PER; ++j) {
-          const int id = j * CONV + ct, row = id / RB, ch = id % RB;
-          const int pg = row < PAGE ? page0 : page1;
-          x[j] = pg < 0 ? make_uint4(0, 0, 0, 0)
-                        : __ldg(reinterpret_cast<const uint4*>(
-                              pool + (int64_t)pg * c.page_stride +
-                              ((int64_t)sg.g * PAGE + row % PAGE) * HD + ch * 16));
+          const int rg = j / HALVES, h = j % HALVES;   // rows 32 rg + row0
+          const bool have = (rg < 2 ? page0 : page1) >= 0;
+          x[j] = make_uint4(0, 0, 0, 0);
+          if (have)
+            x[j] = __ldg(reinterpret_cast<const uint4*>((rg < 2 ? p0 : p1) + (rg & 1) * 32 * HD + h * 64));
         }
       };
-      // 16 codes to two 16-byte chunks; lanes of the row's upper half store
-      // theirs in the other order, so that 8 lanes touch every bank once
-      auto put = [&](uint8_t* mat, const uint4* x) {
+      auto load_scales = [&](int t) {
+        if (ct < NB) {
+          const int pg = ct < NB / 2 ? page0 : page1;
+          ks = 0.0f;
+          vs = -1.0f;
+          if (pg >= 0 && k_lo + t * KEYS + ct * 16 < k_hi) {
+            const int64_t so = (int64_t)pg * c.scale_stride + sg.g * 4 + ct % 4;
+            ks = c.k_scale[so];
+            vs = fmaxf(c.v_scale[so], 0.0f);
+          }
+        }
+      };
+      auto put = [&](uint8_t* mat, const uint4* x) {   // 16 codes: two 16-byte chunks
 #pragma unroll
         for (int j = 0; j < PER; ++j) {
-          const int id = j * CONV + ct, row = id / RB, ch = id % RB;
-          uint32_t h[8];
+          const int row = j / HALVES * 32 + row0;
           const uint32_t u[4] = {x[j].x ^ 0x80808080u, x[j].y ^ 0x80808080u, x[j].z ^ 0x80808080u,
                                  x[j].w ^ 0x80808080u};
+          uint32_t h[8];
 #pragma unroll
           for (int m = 0; m < 4; ++m) {
             h[2 * m] = codes_h2<0x4140>(u[m]);
             h[2 * m + 1] = codes_h2<0x4342>(u[m]);
           }
-          uint8_t* dst = mat + (ch >> 2) * L::SUB + row * 128;
-          const int first = HD == 128 ? ch >> 2 : 0, c2 = (ch & 3) * 2;
-#pragma unroll
-          for (int s = 0; s < 2; ++s) {
-            const bool up = (s ^ first) != 0;
-            *reinterpret_cast<uint4*>(dst + (((c2 + up) ^ (row & 7)) << 4)) =
-                up ? make_uint4(h[4], h[5], h[6], h[7]) : make_uint4(h[0], h[1], h[2], h[3]);
-          }
+          uint8_t* dst = mat + j % HALVES * L::SUB + row * 128;
+          *reinterpret_cast<uint4*>(dst + ((2 * ch ^ (row & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+          *reinterpret_cast<uint4*>(dst + (((2 * ch + 1) ^ (row & 7)) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
         }
       };
       if (tiles > 0) {
-        pages_of(0);
+        next0 = page_at(k_lo);
+        next1 = page_at(k_lo + PAGE);
+        next_pages(0);
         load(c.k, kr);
+        load_scales(0);
         load(c.v, vr);
       }
       for (int t = 0; t < tiles; ++t, ++n_tile) {
         const int st = n_tile % L::STAGES, use = n_tile / L::STAGES;
-        // scales of the 8 blocks (dead ones: no weight)
-        float ks = 0.0f, lv = -INFINITY, iv = 0.0f;
-        if (ct < NB) {
-          const int k = k_lo + t * KEYS + ct * 16, pg = ct < NB / 2 ? page0 : page1;
-          if (k < k_hi && pg >= 0) {
-            const int64_t so = (int64_t)pg * c.scale_stride + sg.g * 4 + ct % 4;
-            ks = c.k_scale[so];
-            const float raw = c.v_scale[so], vs = raw < VS_MIN ? VS_MIN : raw;
-            lv = __log2f(vs);
-            iv = __fdividef(1.0f, vs);
-          }
-        }
         if (use > 0) wait(&k_free[st], (use - 1) & 1);
-        if (n_tile >= 2) wait(&sc_free[n_tile & 1], (n_tile / 2 - 1) & 1);
-        if (ct < NB) {
-          float* sc = reinterpret_cast<float*>(smem + L::SC_OFF) + (n_tile & 1) * 3 * NB + ct;
-          sc[0] = ks;
-          sc[NB] = lv;
-          sc[2 * NB] = iv;
-          mbar_arrive(&sc_full[n_tile & 1]);
-        }
         put(smem + L::K_OFF + st * L::MAT, kr);
         fence_proxy_async_smem();
         mbar_arrive(&k_full[st]);
+        if (n_tile >= 2) wait(&sc_free[n_tile & 1], (n_tile / 2 - 1) & 1);
+        if (ct < NB) {
+          float* sc = reinterpret_cast<float*>(smem + L::SC_OFF) + (n_tile & 1) * 3 * NB + ct;
+          const float v = fmaxf(vs, VS_MIN);
+          sc[0] = ks;
+          sc[NB] = vs < 0.0f ? -INFINITY : __log2f(v);
+          sc[2 * NB] = vs < 0.0f ? 0.0f : __fdividef(1.0f, v);
+          mbar_arrive(&sc_full[n_tile & 1]);
+        }
+        // the next tile's loads; V's registers hold this one's until it is stored
         if (t + 1 < tiles) {
-          pages_of(t + 1);
+          next_pages(t + 1);
           load(c.k, kr);
+          load_scales(t + 1);
         }
         if (use > 0) wait(&v_free[st], (use - 1) & 1);
         put(smem + L::V_OFF + st * L::MAT, vr);
