@@ -79,7 +79,8 @@ struct Lay {
   static constexpr int Q_TERM = R * HD * 2;
   static constexpr int FAC_OFF = Q_OFF + Q_TERM * (TWO ? 2 : 1);
   static constexpr int ML_OFF = FAC_OFF + R * 4;
-  static constexpr int SMEM = ML_OFF + (2 * AT_WARPS + 1) * R * 4;
+  static constexpr int WALK_OFF = ML_OFF + (2 * AT_WARPS + 1) * R * 4;
+  static constexpr int SMEM = WALK_OFF + AT_WARPS * (int)sizeof(Walk);
   static constexpr int CB = HD / 4 < 16 ? HD / 4 : 16;     // bytes of a key's row per lane and load
   static constexpr int NH = HD / (4 * CB);
   static constexpr int NW = CB / 4;
@@ -121,12 +122,12 @@ __global__ void __launch_bounds__(AT_WARPS * 32, 2) kv8_attn_kernel(const AttnP 
 
   pdl_trigger();   // the join may be set up; it waits for this grid's end
   report_lengths(P);
-  Walk walk;
-  walk.start(P, R);
+  Walk* walk = reinterpret_cast<Walk*>(smem + L_::WALK_OFF) + warp;
+  walk_start(walk, P, R);
   Segment sg;
-  while (walk.next(P, &sg)) {
-    const int g = sg.g, rows = walk.sq.rows, r_lo = walk.sq.r_lo;
-    const int k_lo = sg.p_lo * PAGE, k_hi = min(walk.sq.len, sg.p_hi * PAGE);
+  while (walk_next(walk, P, R, &sg)) {
+    const int g = sg.g, rows = sg.rows, r_lo = sg.r_lo;
+    const int k_lo = sg.p_lo * PAGE, k_hi = min(sg.len, sg.p_hi * PAGE);
     const int n_tiles = (k_hi - k_lo + TILE - 1) / TILE;
     const int my = n_tiles > warp ? (n_tiles - warp + AT_WARPS - 1) / AT_WARPS : 0;
     const int32_t* table = c.page_table + (int64_t)sg.seq * c.table_stride;

@@ -111,27 +111,32 @@ FD_DEV Shares shares_of(const AttnP& P, int64_t total) {
   return s;
 }
 
-// One CTA's part of a run: pages [p_lo, p_hi) of sequence seq.
+// One CTA's part of a run: pages [p_lo, p_hi) of sequence seq, whose rows
+// start at token r_lo.
 struct Segment {
-  int seq, g, row0, p_lo, p_hi;
+  int seq, g, row0, p_lo, p_hi, r_lo, rows, len;
   bool whole;
 };
-// Walks a share; every warp that needs the segments has its own.
+// Walks a share: in shared memory, one for each warp that needs the segments
+// (its state would cost the loops' registers).
 struct Walk {
   int64_t x, x_end, off;
-  int seq, tile_rows;
+  int seq;
   Seq sq;
-  FD_DEV void start(const AttnP& P, int rows_of_tile) {
-    tile_rows = rows_of_tile;
-    x = x_end = off = 0;
-    seq = 0;
-    int64_t upto, own;
-    const int64_t total = total_work(P, tile_rows, &upto, &own);
-    const Shares sh = shares_of(P, total);
-    if (blockIdx.x >= sh.n) return;
+  Segment sg;
+};
+// By a warp, with start and next.
+FD_DEV void walk_start(Walk* w, const AttnP& P, int tile_rows) {
+  int64_t upto, own, x = 0, x_end = 0, off = 0;
+  const int64_t total = total_work(P, tile_rows, &upto, &own);
+  const Shares sh = shares_of(P, total);
+  int seq = 0;
+  Seq sq{};
+  if (blockIdx.x < sh.n) {
     x = sh.begin(blockIdx.x);
     x_end = sh.begin(blockIdx.x + 1);
-    if (x >= x_end) return;
+  }
+  if (x < x_end) {
     seq = find_seq(P, tile_rows, x, upto, own, &off);
     sq = seq_of(P, seq, tile_rows);
     const int p = (int)(off - div64(off, sq.span) * sq.span);
@@ -143,27 +148,54 @@ struct Walk {
       off -= p;
     }
   }
-  FD_DEV bool next(const AttnP& P, Segment* s) {
-    if (x >= x_end) return false;
-    while (off >= sq.work) {
-      off -= sq.work;
-      sq = seq_of(P, ++seq, tile_rows);
-    }
-    const int run = (int)div64(off, sq.span), p = (int)(off - (int64_t)run * sq.span);
-    int q = sq.span;
-    if (P.part_o && x_end - x < sq.span - p) q = p + (int)(x_end - x);
-    if (q <= RUN_START) return false;   // the next share takes the run from its start
-    x += q - p;
-    off += q - p;
-    s->seq = seq;
-    s->g = run / sq.tiles;
-    s->row0 = run % sq.tiles * tile_rows;
-    s->p_lo = max(0, p - RUN_START);
-    s->p_hi = min(sq.pages, q - RUN_START);
-    s->whole = p == 0 && q == sq.span;
-    return true;
+  if ((threadIdx.x & 31) == 0) {
+    w->x = x;
+    w->x_end = x_end;
+    w->off = off;
+    w->seq = seq;
+    w->sq = sq;
   }
-};
+  __syncwarp();
+}
+// The next segment, or false at the share's end.
+FD_DEV bool walk_next(Walk* w, const AttnP& P, int tile_rows, Segment* s) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) {
+    int64_t x = w->x, off = w->off;
+    Seq sq = w->sq;
+    Segment n{};
+    n.seq = -1;
+    if (x < w->x_end) {
+      while (off >= sq.work) {
+        off -= sq.work;
+        sq = seq_of(P, ++w->seq, tile_rows);
+      }
+      const int run = (int)div64(off, sq.span), p = (int)(off - (int64_t)run * sq.span);
+      int q = sq.span;
+      if (P.part_o && w->x_end - x < sq.span - p) q = p + (int)(w->x_end - x);
+      x += q - p;
+      off += q - p;
+      if (q > RUN_START) {   // else the next share takes the run from its start
+        n.seq = w->seq;
+        n.g = run / sq.tiles;
+        n.row0 = run % sq.tiles * tile_rows;
+        n.p_lo = max(0, p - RUN_START);
+        n.p_hi = min(sq.pages, q - RUN_START);
+        n.r_lo = sq.r_lo;
+        n.rows = sq.rows;
+        n.len = sq.len;
+        n.whole = p == 0 && q == sq.span;
+      }
+    }
+    w->x = x;
+    w->off = off;
+    w->sq = sq;
+    w->sg = n;
+  }
+  __syncwarp();
+  *s = w->sg;
+  return s->seq >= 0;
+}
 
 FD_DEV float ex2(float x) {
   float y;

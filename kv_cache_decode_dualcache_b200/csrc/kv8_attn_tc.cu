@@ -4,22 +4,27 @@
 // CTA for all of its rows.
 //
 // The CTA's MMA tile has NQ x 128 rows.  Tiles of up to 32 (64) query rows
-// fill 128 rows with 4 (2) copies: copy i of a row takes columns [128 / C i,
-// 128 / C (i + 1)) of every 128-key tile, with statistics of its own, and
-// leaves zero weights in the others' columns, so that the softmax runs on all
-// four warps and the copies' outputs add up at the end.  The idle part of
-// the MMAs costs nothing: with so few rows the kernel waits for the cache.
+// fill 128 rows with C = 4 (2) copies: copy i of a row takes the i-th part of
+// the columns of every tile of 64 keys, with statistics of its own, and leaves
+// zero weights in the others' columns, so that the softmax runs on all four
+// warps; the copies' outputs add up at the end.  The idle part of the MMAs
+// costs nothing: with so few rows the kernel waits for the cache.
 //
 // Roles: 4 warps a row tile for the softmax (a thread per MMA row: q, weights,
-// output; the first one's lane 0 issues the tile's MMAs), 4 converter warps (K
-// and V codes from global memory through registers into 128-byte-swizzled
-// fp16 tiles, the blocks' scales beside them).  Per tile of 128 keys:
-//   S = Q K^T        tcgen05, Q and K in shared memory, S in TMEM
+// output; the first one's lane 0 issues the tile's MMAs), 4 converter warps.
+// A page is a tile: its codes of K (and V) of a head are contiguous and come
+// by one bulk copy each into a ring of int8 units; the converters turn them
+// into 128-byte-swizzled fp16 tiles, the blocks' scales beside them.
+//   S = Q K^T        tcgen05, Q in TMEM, K in shared memory, S in TMEM
 //   w = 2^(S f + log2 vs - M + 8), written over S as packed fp16
-//   O += w V         tcgen05, w from TMEM, V MN-major from shared memory
+//   O += w V         tcgen05, w in TMEM, V MN-major from shared memory
 // with the statistics of kv8_attn.cu.  A tile's w V and the next tile's S are
 // issued together; with two row tiles (NQ = 2) one tile's softmax runs behind
 // the other's products, with one two CTAs share an SM and hide each other's.
+// What shaped this: with shared memory in use there is next to no L1, so
+// loads through registers and spilled registers both starve (loads in flight
+// need L1 lines, spills go to L2); hence the bulk copies, and 64-key tiles,
+// whose scores fit a thread's registers.
 //
 // Every wait is bounded (WAIT_LIMIT_NS); a role whose wait ran out keeps
 // walking its loops without waiting or touching TMEM, so that all barriers
@@ -33,31 +38,46 @@ namespace {
 
 using namespace kv8;
 
-constexpr int KEYS = 128;            // keys of a tile: two pages
+constexpr int KEYS = PAGE;           // keys of a tile
 constexpr int NB = KEYS / FDLLM_KV8_BLOCK;
 constexpr int CONV = 128;            // converter threads
+constexpr int CONV_BAR = 5;          // named barrier of the converters
 
 template <int HD, int NQ>
 struct TcLay {
   static constexpr int KH = HD / 64;                  // 64-dim sub-tiles (128-byte rows)
-  static constexpr int SUB = KEYS * 128;              // [128 rows][64 dims] fp16
-  static constexpr int MAT = KH * SUB;                // K, V or 128 rows of Q
-  static constexpr int STAGES = NQ;
-  static constexpr int K_OFF = 0;
-  static constexpr int V_OFF = K_OFF + STAGES * MAT;
-  static constexpr int Q_OFF = V_OFF + STAGES * MAT;
-  // scales of a tile, by its parity: ks, log2 vs, 1 / vs of 8 blocks
-  static constexpr int SC_OFF = Q_OFF + NQ * MAT;
-  static constexpr int ML_OFF = SC_OFF + 2 * 3 * NB * 4;   // copies' (max, sum) [128]
-  static constexpr int RF_OFF = ML_OFF + 128 * 8;          // row factors
-  static constexpr int BAR_OFF = RF_OFF + NQ * 128 * 4;
-  static constexpr int MISC_OFF = BAR_OFF + 32 * 8;
-  static constexpr int SMEM = MISC_OFF + 16 + 1024;   // slack for 1024-byte alignment
+  static constexpr int SUB = KEYS * 128;              // [64 keys][64 dims] fp16
+  static constexpr int MAT = KH * SUB;                // fp16 K or V of a tile
+  static constexpr int UNIT = KEYS * HD;              // int8 K or V of a tile
+  static constexpr int RING = NQ == 1 ? 4 : 8;        // units
+  static constexpr int K_OFF = 0;                     // two tiles
+  static constexpr int V_OFF = K_OFF + 2 * MAT;
+  static constexpr int RING_OFF = V_OFF + 2 * MAT;
+  static constexpr int DIMS = 16;                     // dims of an exchange round
+  static constexpr int XROW = DIMS + 4;
+  static constexpr int X_OFF = RING_OFF + RING * UNIT;
+  // scales of a tile, by its parity: ks, log2 vs, 1 / vs of 4 blocks
+  static constexpr int SC_OFF = X_OFF + NQ * 128 * XROW * 4;
+  static constexpr int ML_OFF = SC_OFF + 2 * 3 * NB * 4;   // rows' (max, sum)
+  static constexpr int BAR_OFF = ML_OFF + NQ * 128 * 8;
+  static constexpr int MISC_OFF = BAR_OFF + (16 + RING) * 8;
+  static constexpr int PAGE_OFF = MISC_OFF + 16;           // the units' pages
   static constexpr int THREADS = 128 * NQ + CONV;
-  static constexpr uint32_t TMEM_COLS = 256 * NQ;     // S: 128, O: 128 columns a row tile
+  static constexpr int WALK_OFF = (PAGE_OFF + RING * 4 + 15) / 16 * 16;
+  static constexpr int SMEM = WALK_OFF + THREADS / 32 * (int)sizeof(Walk) + 1024;   // slack for
+                                                                                    // 1024-byte alignment
+  static constexpr uint32_t TMEM_COLS = 256 * NQ;     // a row tile: S 64, Q 64, O 128
   static_assert(SMEM <= (NQ == 1 ? 115712 : 232448), "shared memory layout");
 };
 
+// bytes (a multiple of 16) from global to shared memory, both 16-byte aligned.
+FD_DEV void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
 // D (+)= A B with A in TMEM (row i in lane i, two fp16 a column).
 FD_DEV void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
                       uint32_t accumulate) {
@@ -76,14 +96,52 @@ FD_DEV void fma2(float& a, float& b, float f, float g) {
       : "+f"(a), "+f"(b)
       : "f"(f), "f"(g));
 }
-// 16 TMEM columns of this warp's lanes.
-FD_DEV void tmem_st16(uint32_t taddr, const uint32_t* v) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
-      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
-      : "memory");
+// N TMEM columns of this warp's lanes; tmem_wait_st follows the stores.
+template <int N> FD_DEV void tmem_ld(uint32_t taddr, float* v) {
+  if constexpr (N == 64) {
+    tmem_ld64(taddr, v);
+  } else if constexpr (N == 32) {
+    tmem_ld32(taddr, v);
+  } else {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+  }
+}
+template <int N> FD_DEV void tmem_st(uint32_t taddr, const uint32_t* v) {
+  if constexpr (N == 32) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+        "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]),
+        "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]),
+        "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]),
+        "r"(v[30]), "r"(v[31])
+        : "memory");
+  } else if constexpr (N == 16) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+        "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+  } else {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
+                 "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]),
+                 "r"(v[7])
+                 : "memory");
+  }
 }
 FD_DEV void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -97,21 +155,22 @@ __global__ void __launch_bounds__(TcLay<HD, NQ>::THREADS, NQ == 1 ? 2 : 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::BAR_OFF);
-  uint64_t* k_full = bars;             // [STAGES]
+  uint64_t* k_full = bars;             // [2]: fp16 tiles, by tile parity
   uint64_t* k_free = bars + 2;
   uint64_t* v_full = bars + 4;
   uint64_t* v_free = bars + 6;
   uint64_t* s_full = bars + 8;         // [NQ]
   uint64_t* o_full = bars + 10;        // [NQ]
-  uint64_t* sc_full = bars + 12;       // [2]: by tile parity
+  uint64_t* sc_full = bars + 12;       // [2]: scales, by tile parity
   uint64_t* sc_free = bars + 14;
+  uint64_t* unit_full = bars + 16;     // [RING]
   uint32_t* misc = reinterpret_cast<uint32_t*>(smem + L::MISC_OFF);
   int* err = reinterpret_cast<int*>(misc + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 2);
+  volatile int* unit_page = reinterpret_cast<volatile int*>(smem + L::PAGE_OFF);   // -1: none
   const fdllm_kv8& c = P.c;
   const fdllm_kv8_attention_args& a = P.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int rep = a.n_heads / c.n_kv_heads;
 
   pdl_trigger();   // the join may be set up; it waits for this grid's end
   if (tid == 0) {
@@ -125,6 +184,7 @@ __global__ void __launch_bounds__(TcLay<HD, NQ>::THREADS, NQ == 1 ? 2 : 1)
       mbar_init(&sc_full[i], NB);
       mbar_init(&sc_free[i], 128 * NQ);
     }
+    for (int i = 0; i < L::RING; ++i) mbar_init(&unit_full[i], 1);
     *err = 0;
     *abort_flag = 0;
     fence_mbar_init();
@@ -135,8 +195,8 @@ __global__ void __launch_bounds__(TcLay<HD, NQ>::THREADS, NQ == 1 ? 2 : 1)
   tc_fence_after();
   const uint32_t tmem = misc[0];
   report_lengths(P);
-  Walk walk;
-  walk.start(P, R);
+  Walk* walk = reinterpret_cast<Walk*>(smem + L::WALK_OFF) + warp;
+  walk_start(walk, P, R);
   Segment sg;
   bool ok = true;
   // a warp's wait: all lanes agree
@@ -147,96 +207,87 @@ __global__ void __launch_bounds__(TcLay<HD, NQ>::THREADS, NQ == 1 ? 2 : 1)
 
   if (warp < 4 * NQ) {
     // ================================================== softmax
+    const int rep = a.n_heads / c.n_kv_heads;
     const int q = warp >> 2, quad = warp & 3, i = quad * 32 + lane;   // MMA row of tile q
-    const int r = q * 128 + i % R, copy = NQ == 1 ? i / R : 0;        // row of the run, its copy
-    const uint32_t s_col = tmem + ((uint32_t)(quad * 32) << 16) + q * 128;
-    const uint32_t o_col = s_col + NQ * 128;
-    uint8_t* qs = smem + L::Q_OFF + q * L::MAT;
-    float2* ml = reinterpret_cast<float2*>(smem + L::ML_OFF);
-    float* rfs = reinterpret_cast<float*>(smem + L::RF_OFF);
-    const uint32_t kb = smem_u32(smem + L::K_OFF), vb = smem_u32(smem + L::V_OFF), qb = smem_u32(qs);
+    const int r = q * 128 + i % (128 / C), copy = i / (128 / C);      // row of the run, its copy
+    const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+    const uint32_t s_mma = tmem + q * 64, q_mma = tmem + NQ * 64 + q * 64, o_mma = tmem + NQ * 128 + q * 128;
+    const uint32_t s_col = s_mma + lanes, o_col = o_mma + lanes;
+    const uint32_t kb = smem_u32(smem + L::K_OFF), vb = smem_u32(smem + L::V_OFF);
     // the MMAs of this row tile, by warp 0 of its four: S of tile n; w V of tile n
     auto scores = [&](int n) {
-      const int st = n % L::STAGES;
-      wait(&k_full[st], (n / L::STAGES) & 1);
+      const int st = n & 1;
+      wait(&k_full[st], (n >> 1) & 1);
       if (ok && lane == 0) {
         tc_fence_after();
-        // a step along K moves the descriptors' start address (in 16 bytes)
-        const uint64_t qd = smem_desc_sw128(qb), kd = smem_desc_sw128(kb + st * L::MAT);
+        // a step along K moves the descriptor's start address (in 16 bytes)
+        const uint64_t kd = smem_desc_sw128(kb + st * L::MAT);
 #pragma unroll
-        for (int k = 0; k < HD / 16; ++k) {
-          const uint32_t off = ((k >> 2) * L::SUB + (k & 3) * 32) >> 4;
-          tc_mma(tmem + q * 128, qd + off, kd + off, idesc_f32acc(KEYS, true), k > 0);
-        }
+        for (int k = 0; k < HD / 16; ++k)
+          tc_mma_ts(s_mma, q_mma + k * 8, kd + (((k >> 2) * L::SUB + (k & 3) * 32) >> 4),
+                    idesc_f32acc(KEYS, true), k > 0);
         tc_commit(&s_full[q]);
         tc_commit(&k_free[st]);
       }
       __syncwarp();
     };
     auto products = [&](int n, bool first, bool last) {
-      const int st = n % L::STAGES;
-      wait(&v_full[st], (n / L::STAGES) & 1);
+      const int st = n & 1;
+      wait(&v_full[st], (n >> 1) & 1);
       if (ok && lane == 0) {
         tc_fence_after();
         const uint64_t vd = smem_desc_sw128_mn(vb + st * L::MAT, L::SUB, 1024);
 #pragma unroll
         for (int k = 0; k < KEYS / 16; ++k)
-          tc_mma_ts(tmem + (NQ + q) * 128, tmem + q * 128 + k * 8, vd + (k * 2048 >> 4),
-                    idesc_f32acc_bmn(HD, true), !first || k > 0);
+          tc_mma_ts(o_mma, s_mma + k * 8, vd + (k * 2048 >> 4), idesc_f32acc_bmn(HD, true),
+                    !first || k > 0);
         tc_commit(&v_free[st]);
         if (last) tc_commit(&o_full[q]);
       }
       __syncwarp();
     };
     int n_tile = 0, n_seg = 0;
-    while (walk.next(P, &sg)) {
-      const int rows = walk.sq.rows, rr = sg.row0 + r;
-      const int k_lo = sg.p_lo * PAGE, k_hi = min(walk.sq.len, sg.p_hi * PAGE);
+    while (walk_next(walk, P, R, &sg)) {
+      const int rr = sg.row0 + r;
+      const int k_lo = sg.p_lo * PAGE, k_hi = min(sg.len, sg.p_hi * PAGE);
       const int tiles = (k_hi - k_lo + KEYS - 1) / KEYS;
-      // ---- q, scaled per row by a power of two, into the swizzled A tile: HD / 8
-      // lanes a row, 16 bytes each; every warp a quarter of the rows, all copies
+      // ---- this row of q, scaled by a power of two, into TMEM as packed fp16
+      float rf;
       {
-        constexpr int LR = HD / 8, RPW = 128 / C / 4, STEP = 32 / LR, N = RPW / STEP;
-        const int ch = lane % LR, row_a = quad * RPW + lane / LR;   // row of the MMA tile
-        const int first = sg.row0 + q * 128 + row_a;
-        int token = first / rep, head = first % rep;
-        uint4 raw[N];
+        const bool have = rr < sg.rows;
+        const uint4* src = reinterpret_cast<const uint4*>(
+            reinterpret_cast<const T*>(a.q) + (int64_t)(sg.r_lo + (have ? rr / rep : 0)) * a.q_strides[0] +
+            (int64_t)(sg.g * rep + (have ? rr % rep : 0)) * a.q_strides[1]);
+        uint4 raw[HD / 8];
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-          raw[j] = make_uint4(0, 0, 0, 0);
-          if (first + j * STEP < rows)
-            raw[j] = *reinterpret_cast<const uint4*>(
-                reinterpret_cast<const T*>(a.q) + (int64_t)(walk.sq.r_lo + token) * a.q_strides[0] +
-                (int64_t)(sg.g * rep + head) * a.q_strides[1] + ch * 8);
-          for (head += STEP; head >= rep; head -= rep) ++token;
-        }
+        for (int j = 0; j < HD / 8; ++j) raw[j] = have ? src[j] : make_uint4(0, 0, 0, 0);
+        float top = 0.0f;
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
+        for (int j = 0; j < HD / 8; ++j) {
           const T* e = reinterpret_cast<const T*>(&raw[j]);
-          float top = 0.0f;
 #pragma unroll
           for (int m = 0; m < 8; ++m) top = fmaxf(top, fabsf(to_f<T>(e[m])));
-#pragma unroll
-          for (int o = LR / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-          const int up = q_shift(top), row = row_a + j * STEP;
-          const float mul = exp2_int(up);
-          uint32_t h[4];
-#pragma unroll
-          for (int m = 0; m < 4; ++m)
-            h[m] = pack_h2(to_f<T>(e[2 * m]) * mul, to_f<T>(e[2 * m + 1]) * mul);
-#pragma unroll
-          for (int k = 0; k < C; ++k) {
-            const int at = k * (128 / C) + row;
-            *reinterpret_cast<uint4*>(qs + (ch >> 3) * L::SUB + at * 128 + (((ch & 7) ^ (at & 7)) << 4)) =
-                make_uint4(h[0], h[1], h[2], h[3]);
-          }
-          if (ch == 0) rfs[q * 128 + row] = a.scale * LOG2E * exp2_int(-up);
         }
-        fence_proxy_async_smem();
+        const int up = q_shift(top);
+        const float mul = exp2_int(up);
+        rf = a.scale * LOG2E * exp2_int(-up);
+#pragma unroll
+        for (int j0 = 0; j0 < HD / 8; j0 += 8) {   // 64 dims: 32 columns
+          uint32_t h[32];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const T* e = reinterpret_cast<const T*>(&raw[j0 + j]);
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+              h[4 * j + m] = pack_h2(to_f<T>(e[2 * m]) * mul, to_f<T>(e[2 * m + 1]) * mul);
+          }
+          if (ok) tmem_st<32>(q_mma + lanes + j0 * 4, h);
+        }
+        if (ok) tmem_wait_st();
+        tc_fence_before();
         named_bar(1 + q, 128);
         if (quad == 0 && tiles > 0) scores(n_tile);
       }
-      const float rf = rfs[r];
       float M = -INFINITY, l = 0.0f;
       for (int t = 0; t < tiles; ++t, ++n_tile) {
         const int k0 = k_lo + t * KEYS + copy * NC;   // first key of this thread's columns
@@ -246,31 +297,21 @@ __global__ void __launch_bounds__(TcLay<HD, NQ>::THREADS, NQ == 1 ? 2 : 1)
         wait(&sc_full[n_tile & 1], (n_tile >> 1) & 1);
         if (ok) {
           tc_fence_after();
-          const bool tail = k0 + NC > k_hi;
-          const uint32_t col = s_col + copy * NC;
-          float v[32], mx = -INFINITY;
-          // t of 32 columns from c0 on, shifted by add; columns behind the run's
-          // last key are -inf
-          auto read = [&](int c0, float add) {
-            tmem_ld32(col + c0, v);
+          float v[NC], mx = -INFINITY;
+          tmem_ld<NC>(s_col + copy * NC, v);
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-              const float f = rf * sc[c0 / 16 + b], g = sc[NB + c0 / 16 + b] + add;
+          for (int b = 0; b < NC / 16; ++b) {
+            const float f = rf * sc[b], g = sc[NB + b];
 #pragma unroll
-              for (int j = 16 * b; j < 16 * b + 16; j += 2) fma2(v[j], v[j + 1], f, g);
-            }
-            if (tail) {
-#pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (k0 + c0 + j >= k_hi) v[j] = -INFINITY;
-            }
-          };
-#pragma unroll
-          for (int c0 = 0; c0 < NC; c0 += 32) {
-            read(c0, 0.0f);
-#pragma unroll
-            for (int j = 0; j < 32; j += 2) mx = fmaxf(fmaxf(mx, v[j]), v[j + 1]);
+            for (int j = 16 * b; j < 16 * b + 16; j += 2) fma2(v[j], v[j + 1], f, g);
           }
+          if (k0 + NC > k_hi) {
+#pragma unroll
+            for (int j = 0; j < NC; ++j)
+              if (k0 + j >= k_hi) v[j] = -INFINITY;
+          }
+#pragma unroll
+          for (int j = 0; j < NC; j += 2) mx = fmaxf(fmaxf(mx, v[j]), v[j + 1]);
           float alpha = 1.0f;
           const bool move = mx > M + M_SLACK || (M == -INFINITY && mx > -INFINITY);
           if (move) {
@@ -279,45 +320,37 @@ __global__ void __launch_bounds__(TcLay<HD, NQ>::THREADS, NQ == 1 ? 2 : 1)
           }
           const float ref = W_EXP - (M == -INFINITY ? 0.0f : M);
           float sum = 0.0f;
+          uint32_t w[NC / 2];
 #pragma unroll
-          for (int c0 = 0; c0 < NC; c0 += 32) {
-            uint32_t w[16];
-            if (NC > 32) {   // the registers hold one chunk only: read the scores again
-              read(c0, ref);
-            } else {
+          for (int b = 0; b < NC / 16; ++b) {
+            float part[2] = {0.0f, 0.0f};
 #pragma unroll
-              for (int j = 0; j < 32; ++j) v[j] += ref;
+            for (int j = 16 * b; j < 16 * b + 16; j += 2) {
+              const float e0 = ex2(v[j] + ref), e1 = ex2(v[j + 1] + ref);
+              part[0] += e0;
+              part[1] += e1;
+              w[j / 2] = pack_h2(e0, e1);
             }
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-              float part = 0.0f;
-#pragma unroll
-              for (int j = 16 * b; j < 16 * b + 16; j += 2) {
-                const float e0 = ex2(v[j]), e1 = ex2(v[j + 1]);
-                part += e0 + e1;
-                w[j / 2] = pack_h2(e0, e1);
-              }
-              sum = fmaf(part, sc[2 * NB + c0 / 16 + b], sum);
-            }
-            // w goes over the scores' first 64 columns, which chunks c0 / 2
-            // and below of this row have been read by now
-            tmem_st16(s_col + (copy * NC + c0) / 2, w);
+            sum = fmaf(part[0] + part[1], sc[2 * NB + b], sum);
           }
+          // over the scores' first 32 columns (this warp has read its lanes)
+          tmem_st<NC / 2>(s_col + copy * (NC / 2), w);
           if constexpr (C > 1) {
-            const uint32_t zero[16] = {};
+            const uint32_t zero[8] = {};
 #pragma unroll
-            for (int o = 0; o < 64; o += 16)
-              if (o / (NC / 2) != copy) tmem_st16(s_col + o, zero);
+            for (int o = 0; o < KEYS / 2; o += 8)
+              if (o / (NC / 2) != copy) tmem_st<8>(s_col + o, zero);
           }
           l = fmaf(l, alpha, sum);
           if (t > 0 && __any_sync(0xffffffffu, move)) {
             // S of this tile came after the products before it: O is still
-#pragma unroll
+#pragma unroll 1
             for (int c0 = 0; c0 < HD; c0 += 32) {
-              tmem_ld32(o_col + c0, v);
+              float o[32];
+              tmem_ld32(o_col + c0, o);
 #pragma unroll
-              for (int j = 0; j < 32; ++j) v[j] *= alpha;
-              tmem_st32(o_col + c0, v);
+              for (int j = 0; j < 32; ++j) o[j] *= alpha;
+              tmem_st32(o_col + c0, o);
             }
           }
           tmem_wait_st();
@@ -330,95 +363,62 @@ __global__ void __launch_bounds__(TcLay<HD, NQ>::THREADS, NQ == 1 ? 2 : 1)
           if (t + 1 < tiles) scores(n_tile + 1);
         }
       }
-      // ---- the run's output, or its part
+      // ---- the run's output, or its part: the copies of a row add up, scaled to
+      // their common reference, DIMS dims at a time
       const bool have_o = tiles > 0 && wait(&o_full[q], n_seg & 1);
       tc_fence_after();
       if (tiles > 0) ++n_seg;
-      const int64_t slot = ((int64_t)blockIdx.x * 2 + (sg.p_lo == 0)) * R;
-      auto emit = [&](int row, int d, const float* x, float inv) {   // 8 dims of a row
-        const int rw = sg.row0 + row;
-        if (rw >= rows) return;
-        if (!sg.whole) {
-          float* dst = P.part_o + (slot + row) * HD + d;
-          *reinterpret_cast<float4*>(dst) = make_float4(x[0], x[1], x[2], x[3]);
-          *reinterpret_cast<float4*>(dst + 4) = make_float4(x[4], x[5], x[6], x[7]);
-        } else {
-          T* dst = reinterpret_cast<T*>(a.out) + (int64_t)(walk.sq.r_lo + rw / rep) * a.out_strides[0] +
-                   (int64_t)(sg.g * rep + rw % rep) * a.out_strides[1] + d;
-          uint4 u;
-          T* e = reinterpret_cast<T*>(&u);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) e[j] = from_f<T>(x[j] * inv);
-          *reinterpret_cast<uint4*>(dst) = u;
-        }
-      };
-      if constexpr (C == 1) {
-        const float inv = M == -INFINITY ? 0.0f : 1.0f / l;
-        if (!sg.whole && rr < rows) P.part_ml[slot + r] = make_float2(M, l);
-#pragma unroll
-        for (int c0 = 0; c0 < HD; c0 += 32) {
-          float v[32];
-          if (have_o) tmem_ld32(o_col + c0, v);
-#pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = have_o ? v[j] : 0.0f;
-#pragma unroll
-          for (int j = 0; j < 32; j += 8) emit(r, c0 + j, v + j, inv);
-        }
-      } else {
-        // the copies of a row add up, scaled to their common reference, DIMS
-        // dims at a time through the area of Q (no product reads it any more)
-        constexpr int DIMS = HD / 4, XROW = DIMS + 4;
-        static_assert(128 * XROW * 4 <= L::MAT, "the exchange exceeds the Q area");
-        float* xo = reinterpret_cast<float*>(qs);
+      {
+        constexpr int RQ = 128 / C, DIMS = L::DIMS, XROW = L::XROW, LR = DIMS / 4;
+        const int64_t slot = ((int64_t)blockIdx.x * 2 + (sg.p_lo == 0)) * R;
+        float* xo = reinterpret_cast<float*>(smem + L::X_OFF) + q * 128 * XROW;
+        float2* ml = reinterpret_cast<float2*>(smem + L::ML_OFF) + q * 128;
         ml[i] = make_float2(M, l);
-        named_bar(1, 128);
-        float mx = -INFINITY;
+        named_bar(1 + q, 128);
+        const int row = i % RQ;
+        float mx = -INFINITY, sum = 0.0f;
 #pragma unroll
-        for (int k = 0; k < C; ++k) mx = fmaxf(mx, ml[k * R + r].x);
-        const float fac = M == -INFINITY ? 0.0f : ex2(M - mx);
-        // this thread adds up 8 dims of row orow
-        constexpr int PER = 128 / R;                 // threads a row
-        const int orow = i / PER;
-        float omx = -INFINITY, osum = 0.0f;
-#pragma unroll
-        for (int k = 0; k < C; ++k) omx = fmaxf(omx, ml[k * R + orow].x);
+        for (int k = 0; k < C; ++k) mx = fmaxf(mx, ml[k * RQ + row].x);
 #pragma unroll
         for (int k = 0; k < C; ++k) {
-          const float2 m = ml[k * R + orow];
-          osum += m.x == -INFINITY ? 0.0f : m.y * ex2(m.x - omx);
+          const float2 m = ml[k * RQ + row];
+          sum += m.x == -INFINITY ? 0.0f : m.y * ex2(m.x - mx);
         }
-        const float inv = omx == -INFINITY ? 0.0f : 1.0f / osum;
-        if (!sg.whole && i % PER == 0 && sg.row0 + orow < rows)
-          P.part_ml[slot + orow] = make_float2(omx, osum);
+        // a whole row is divided by its sum here, a partial one by the join
+        float fac = M == -INFINITY ? 0.0f : ex2(M - mx);
+        if (sg.whole) fac *= mx == -INFINITY ? 0.0f : 1.0f / sum;
+        if (!sg.whole && copy == 0 && rr < sg.rows) P.part_ml[slot + r] = make_float2(mx, sum);
+#pragma unroll 1
+        for (int c0 = 0; c0 < HD; c0 += DIMS) {
+          float v[DIMS];
+          if (have_o) tmem_ld<DIMS>(o_col + c0, v);
 #pragma unroll
-        for (int c0 = 0; c0 < HD; c0 += 32) {
-          float v[32];
-          if (have_o) tmem_ld32(o_col + c0, v);
+          for (int j = 0; j < DIMS; j += 4)
+            *reinterpret_cast<float4*>(xo + i * XROW + j) =
+                have_o ? make_float4(v[j] * fac, v[j + 1] * fac, v[j + 2] * fac, v[j + 3] * fac)
+                       : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          named_bar(1 + q, 128);
+          // LR lanes a row
+          for (int at = i / LR; at < RQ; at += 128 / LR) {
+            const int d = i % LR * 4, rw = sg.row0 + q * 128 + at;
+            if (rw >= sg.rows) break;
+            float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-          for (int s0 = 0; s0 < 32; s0 += DIMS) {
-#pragma unroll
-            for (int j = 0; j < DIMS; j += 4)
-              *reinterpret_cast<float4*>(xo + i * XROW + j) =
-                  have_o ? make_float4(v[s0 + j] * fac, v[s0 + j + 1] * fac, v[s0 + j + 2] * fac,
-                                       v[s0 + j + 3] * fac)
-                         : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            named_bar(1, 128);
-            for (int d = i % PER * 8; d < DIMS; d += PER * 8) {
-              float x[8] = {};
-#pragma unroll
-              for (int k = 0; k < C; ++k)
-#pragma unroll
-                for (int j = 0; j < 8; j += 4) {
-                  const float4 u = *reinterpret_cast<const float4*>(xo + (k * R + orow) * XROW + d + j);
-                  x[j] += u.x;
-                  x[j + 1] += u.y;
-                  x[j + 2] += u.z;
-                  x[j + 3] += u.w;
-                }
-              emit(orow, c0 + s0 + d, x, inv);
+            for (int k = 0; k < C; ++k) {
+              const float4 u = *reinterpret_cast<const float4*>(xo + (k * RQ + at) * XROW + d);
+              x.x += u.x;
+              x.y += u.y;
+              x.z += u.z;
+              x.w += u.w;
             }
-            named_bar(1, 128);
+            if (sg.whole)
+              store4(reinterpret_cast<T*>(a.out) + (int64_t)(sg.r_lo + rw / rep) * a.out_strides[0] +
+                         (int64_t)(sg.g * rep + rw % rep) * a.out_strides[1] + c0 + d,
+                     x.x, x.y, x.z, x.w);
+            else
+              *reinterpret_cast<float4*>(P.part_o + (slot + q * 128 + at) * HD + c0 + d) = x;
           }
+          named_bar(1 + q, 128);
         }
       }
       tc_fence_before();   // O has been read before the next run's first product
@@ -427,109 +427,114 @@ __global__ void __launch_bounds__(TcLay<HD, NQ>::THREADS, NQ == 1 ? 2 : 1)
     // ================================================== converters
     const int ct = tid - 128 * NQ;
     constexpr int HALVES = HD / 64;            // 64-byte halves of a key
-    constexpr int PER = KEYS / 32 * HALVES;    // 16-byte chunks of a thread
+    constexpr int PER = KEYS / 32 * HALVES;    // 16-byte chunks of a thread and unit
     // 4 lanes take 64 bytes of a key: the 8 lanes of a store then have an
     // even and an odd row, whose swizzled chunks are on different banks
     const int row0 = ct >> 2, ch = ct & 3;
+    uint8_t* ring = smem + L::RING_OFF;
     int n_tile = 0;
-    while (walk.next(P, &sg)) {
+    uint32_t n_unit = 0;                       // units consumed; unit u of a run: K, V of tile u / 2
+    while (walk_next(walk, P, R, &sg)) {
       const int32_t* table = c.page_table + (int64_t)sg.seq * c.table_stride;
-      const int k_lo = sg.p_lo * PAGE, k_hi = min(walk.sq.len, sg.p_hi * PAGE);
-      const int tiles = (k_hi - k_lo + KEYS - 1) / KEYS;
-      uint4 kr[PER], vr[PER];
-      float ks = 0.0f, vs = -1.0f;             // scales of block ct (vs < 0: no key)
-      int page0 = -1, page1 = -1, next0 = -1, next1 = -1;
-      // page id of key k, as the table has it; -1 behind the run's end
-      auto page_at = [&](int k) { return k < k_hi ? table[k / PAGE] : -1; };
-      auto next_pages = [&](int t) {   // of tile t, from the ids asked for one tile before
-        page0 = next0;
-        page1 = next1;
-        const int k = k_lo + t * KEYS;
-        if (k < k_hi && (page0 < 0 || page0 >= c.n_pages || (k + PAGE < k_hi && (page1 < 0 || page1 >= c.n_pages)))) {
-          if (ct == 0 && a.status) atomicOr(a.status, FDLLM_KV8_BAD_PAGE);
-        }
-        if (page0 >= c.n_pages) page0 = -1;
-        if (page1 >= c.n_pages) page1 = -1;
-        next0 = page_at(k + KEYS);
-        next1 = page_at(k + KEYS + PAGE);
-      };
-      auto load = [&](const int8_t* pool, uint4* x) {
-        const int8_t* base = pool + ((int64_t)sg.g * PAGE + row0) * HD + ch * 16;
-        const int8_t* p0 = base + (int64_t)page0 * c.page_stride;
-        const int8_t* p1 = base + (int64_t)page1 * c.page_stride;
-#pragma unroll
-        for (int j = 0; j < PER; ++j) {
-          const int rg = j / HALVES, h = j % HALVES;   // rows 32 rg + row0
-          const bool have = (rg < 2 ? page0 : page1) >= 0;
-          x[j] = make_uint4(0, 0, 0, 0);
-          if (have)
-            x[j] = __ldg(reinterpret_cast<const uint4*>((rg < 2 ? p0 : p1) + (rg & 1) * 32 * HD + h * 64));
-        }
-      };
-      auto load_scales = [&](int t) {
-        if (ct < NB) {
-          const int pg = ct < NB / 2 ? page0 : page1;
-          ks = 0.0f;
-          vs = -1.0f;
-          if (pg >= 0 && k_lo + t * KEYS + ct * 16 < k_hi) {
-            const int64_t so = (int64_t)pg * c.scale_stride + sg.g * 4 + ct % 4;
-            ks = c.k_scale[so];
-            vs = fmaxf(c.v_scale[so], 0.0f);
+      const int tiles = max(0, sg.p_hi - sg.p_lo);
+      // page ids of 32 tiles, one a lane of the first warp (which copies and
+      // fetches the scales)
+      int ids = -1, ids_at = -32;
+      auto page_of = [&](int t) {
+        if (t >= ids_at + 32 || t < ids_at) {
+          ids_at = t;
+          const int at = sg.p_lo + t + lane;
+          ids = at < sg.p_hi ? table[at] : -1;
+          if (at < sg.p_hi && (ids < 0 || ids >= c.n_pages)) {
+            ids = -1;
+            if (a.status) atomicOr(a.status, FDLLM_KV8_BAD_PAGE);
           }
         }
+        return __shfl_sync(0xffffffffu, ids, t - ids_at);
       };
-      auto put = [&](uint8_t* mat, const uint4* x) {   // 16 codes: two 16-byte chunks
+      auto copy_unit = [&](int u) {   // by the first warp
+        const int page = page_of(u >> 1), slot = (n_unit + u) % L::RING;
+        if (lane == 0) {
+          unit_page[slot] = page;
+          if (page < 0) {
+            mbar_arrive(&unit_full[slot]);
+          } else {
+            mbar_arrive_expect_tx(&unit_full[slot], L::UNIT);
+            bulk_load(ring + slot * L::UNIT,
+                      (u & 1 ? c.v : c.k) + (int64_t)page * c.page_stride + (int64_t)sg.g * L::UNIT,
+                      L::UNIT, &unit_full[slot]);
+          }
+        }
+        __syncwarp();
+      };
+      float ks = 0.0f, vs = -1.0f;   // scales of block ct of the next tile (vs < 0: no key)
+      auto load_scales = [&](int t) {
+        const int page = unit_page[(n_unit + 2 * t) % L::RING];   // on its way by now
+        ks = 0.0f;
+        vs = -1.0f;
+        if (ct < NB && page >= 0 && (sg.p_lo + t) * PAGE + ct * 16 < sg.len) {
+          const int64_t so = (int64_t)page * c.scale_stride + sg.g * 4 + ct;
+          ks = c.k_scale[so];
+          vs = fmaxf(c.v_scale[so], 0.0f);
+        }
+      };
+      const int units = 2 * tiles;
+      if (ct < 32) {
+        for (int u = 0; u < min(units, L::RING); ++u) copy_unit(u);
+        if (tiles > 0) load_scales(0);
+      }
+      for (int u = 0; u < units; ++u) {
+        const uint32_t n = n_unit + u;
+        const int slot = n % L::RING, st = n_tile & 1, use = n_tile >> 1;
+        wait(&unit_full[slot], (n / L::RING) & 1);
+        uint4 x[PER];
+        const bool none = unit_page[slot] < 0;
 #pragma unroll
-        for (int j = 0; j < PER; ++j) {
+        for (int j = 0; j < PER; ++j)
+          x[j] = none ? make_uint4(0, 0, 0, 0)
+                      : *reinterpret_cast<const uint4*>(ring + slot * L::UNIT + (j / HALVES * 32 + row0) * HD +
+                                                        j % HALVES * 64 + ch * 16);
+        uint64_t* free_bar = u & 1 ? &v_free[st] : &k_free[st];
+        if (use > 0) wait(free_bar, (use - 1) & 1);
+        uint8_t* mat = smem + (u & 1 ? L::V_OFF : L::K_OFF) + st * L::MAT;
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {   // 16 codes: two 16-byte chunks
           const int row = j / HALVES * 32 + row0;
-          const uint32_t u[4] = {x[j].x ^ 0x80808080u, x[j].y ^ 0x80808080u, x[j].z ^ 0x80808080u,
+          const uint32_t y[4] = {x[j].x ^ 0x80808080u, x[j].y ^ 0x80808080u, x[j].z ^ 0x80808080u,
                                  x[j].w ^ 0x80808080u};
           uint32_t h[8];
 #pragma unroll
           for (int m = 0; m < 4; ++m) {
-            h[2 * m] = codes_h2<0x4140>(u[m]);
-            h[2 * m + 1] = codes_h2<0x4342>(u[m]);
+            h[2 * m] = codes_h2<0x4140>(y[m]);
+            h[2 * m + 1] = codes_h2<0x4342>(y[m]);
           }
           uint8_t* dst = mat + j % HALVES * L::SUB + row * 128;
           *reinterpret_cast<uint4*>(dst + ((2 * ch ^ (row & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
           *reinterpret_cast<uint4*>(dst + (((2 * ch + 1) ^ (row & 7)) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
         }
-      };
-      if (tiles > 0) {
-        next0 = page_at(k_lo);
-        next1 = page_at(k_lo + PAGE);
-        next_pages(0);
-        load(c.k, kr);
-        load_scales(0);
-        load(c.v, vr);
-      }
-      for (int t = 0; t < tiles; ++t, ++n_tile) {
-        const int st = n_tile % L::STAGES, use = n_tile / L::STAGES;
-        if (use > 0) wait(&k_free[st], (use - 1) & 1);
-        put(smem + L::K_OFF + st * L::MAT, kr);
         fence_proxy_async_smem();
-        mbar_arrive(&k_full[st]);
-        if (n_tile >= 2) wait(&sc_free[n_tile & 1], (n_tile / 2 - 1) & 1);
-        if (ct < NB) {
-          float* sc = reinterpret_cast<float*>(smem + L::SC_OFF) + (n_tile & 1) * 3 * NB + ct;
-          const float v = fmaxf(vs, VS_MIN);
-          sc[0] = ks;
-          sc[NB] = vs < 0.0f ? -INFINITY : __log2f(v);
-          sc[2 * NB] = vs < 0.0f ? 0.0f : __fdividef(1.0f, v);
-          mbar_arrive(&sc_full[n_tile & 1]);
+        mbar_arrive(u & 1 ? &v_full[st] : &k_full[st]);
+        named_bar(CONV_BAR, CONV);   // every thread has read the unit
+        if (ct < 32) {
+          if (u + L::RING < units) copy_unit(u + L::RING);
+          if ((u & 1) == 0) {
+            // this tile's scales, then the next one's on their way
+            if (n_tile >= 2) wait(&sc_free[st], (use - 1) & 1);
+            if (ct < NB) {
+              float* sc = reinterpret_cast<float*>(smem + L::SC_OFF) + st * 3 * NB + ct;
+              const float v = fmaxf(vs, VS_MIN);
+              sc[0] = ks;
+              sc[NB] = vs < 0.0f ? -INFINITY : __log2f(v);
+              sc[2 * NB] = vs < 0.0f ? 0.0f : __fdividef(1.0f, v);
+              mbar_arrive(&sc_full[st]);
+            }
+            __syncwarp();
+            if ((u >> 1) + 1 < tiles) load_scales((u >> 1) + 1);
+          }
         }
-        // the next tile's loads; V's registers hold this one's until it is stored
-        if (t + 1 < tiles) {
-          next_pages(t + 1);
-          load(c.k, kr);
-          load_scales(t + 1);
-        }
-        if (use > 0) wait(&v_free[st], (use - 1) & 1);
-        put(smem + L::V_OFF + st * L::MAT, vr);
-        fence_proxy_async_smem();
-        mbar_arrive(&v_full[st]);
-        if (t + 1 < tiles) load(c.v, vr);
+        n_tile += u & 1;
       }
+      n_unit += units;
     }
   }
   tc_fence_before();
