@@ -15,12 +15,13 @@
 // A page is a tile: its codes of K (and V) of a head are contiguous and come
 // by one bulk copy each into a ring of int8 units; the converters turn them
 // into 128-byte-swizzled fp16 tiles, the blocks' scales beside them.
-//   S = Q K^T        tcgen05, Q in TMEM, K in shared memory, S in TMEM
+//   S = Q K^T        tcgen05, Q and K in shared memory, S in TMEM (two buffers)
 //   w = 2^(S f + log2 vs - M + 8), written over S as packed fp16
 //   O += w V         tcgen05, w in TMEM, V MN-major from shared memory
-// with the statistics of kv8_attn.cu.  A tile's w V and the next tile's S are
-// issued together; with two row tiles (NQ = 2) one tile's softmax runs behind
-// the other's products, with one two CTAs share an SM and hide each other's.
+// with the statistics of kv8_attn.cu.  S of tile t + 1 is done before the softmax
+// of tile t is, so that the chain from tile to tile is the softmax alone; w V
+// of tile t and S of tile t + 2 are issued behind it.  With one row tile (NQ =
+// 1) two CTAs share an SM.
 // What shaped this: with shared memory in use there is next to no L1, so
 // loads through registers and spilled registers both starve (loads in flight
 // need L1 lines, spills go to L2); hence the bulk copies, and 64-key tiles,
@@ -50,23 +51,27 @@ struct TcLay {
   static constexpr int MAT = KH * SUB;                // fp16 K or V of a tile
   static constexpr int UNIT = KEYS * HD;              // int8 K or V of a tile
   static constexpr int RING = NQ == 1 ? 4 : 8;        // units
-  static constexpr int K_OFF = 0;                     // two tiles
-  static constexpr int V_OFF = K_OFF + 2 * MAT;
-  static constexpr int RING_OFF = V_OFF + 2 * MAT;
+  static constexpr int STAGES = NQ;                   // fp16 tiles of K, and of V
+  static constexpr int Q_SUB = 128 * 128;             // [128 rows][64 dims] fp16
+  static constexpr int K_OFF = 0;
+  static constexpr int V_OFF = K_OFF + STAGES * MAT;
+  static constexpr int Q_OFF = V_OFF + STAGES * MAT;
+  static constexpr int RING_OFF = Q_OFF + NQ * KH * Q_SUB;
   static constexpr int DIMS = 16;                     // dims of an exchange round
   static constexpr int XROW = DIMS + 4;
   static constexpr int X_OFF = RING_OFF + RING * UNIT;
-  // scales of a tile, by its parity: ks, log2 vs, 1 / vs of 4 blocks
+  // scales of four tiles: ks, log2 vs, 1 / vs of 4 blocks
   static constexpr int SC_OFF = X_OFF + NQ * 128 * XROW * 4;
-  static constexpr int ML_OFF = SC_OFF + 2 * 3 * NB * 4;   // rows' (max, sum)
-  static constexpr int BAR_OFF = ML_OFF + NQ * 128 * 8;
-  static constexpr int MISC_OFF = BAR_OFF + (16 + RING) * 8;
+  static constexpr int ML_OFF = SC_OFF + 4 * 3 * NB * 4;   // rows' (max, sum)
+  static constexpr int RF_OFF = ML_OFF + NQ * 128 * 8;     // row factors
+  static constexpr int BAR_OFF = RF_OFF + NQ * 128 * 4;
+  static constexpr int MISC_OFF = BAR_OFF + (22 + RING) * 8;
   static constexpr int PAGE_OFF = MISC_OFF + 16;           // the units' pages
   static constexpr int THREADS = 128 * NQ + CONV;
   static constexpr int WALK_OFF = (PAGE_OFF + RING * 4 + 15) / 16 * 16;
   static constexpr int SMEM = WALK_OFF + THREADS / 32 * (int)sizeof(Walk) + 1024;   // slack for
                                                                                     // 1024-byte alignment
-  static constexpr uint32_t TMEM_COLS = 256 * NQ;     // a row tile: S 64, Q 64, O 128
+  static constexpr uint32_t TMEM_COLS = 256 * NQ;     // a row tile: S 2 x 64, O 128
   static_assert(SMEM <= (NQ == 1 ? 115712 : 232448), "shared memory layout");
 };
 
@@ -155,15 +160,15 @@ __global__ void __launch_bounds__(TcLay<HD, NQ>::THREADS, NQ == 1 ? 2 : 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::BAR_OFF);
-  uint64_t* k_full = bars;             // [2]: fp16 tiles, by tile parity
+  uint64_t* k_full = bars;             // [STAGES]: fp16 tiles
   uint64_t* k_free = bars + 2;
   uint64_t* v_full = bars + 4;
   uint64_t* v_free = bars + 6;
-  uint64_t* s_full = bars + 8;         // [NQ]
-  uint64_t* o_full = bars + 10;        // [NQ]
-  uint64_t* sc_full = bars + 12;       // [2]: scales, by tile parity
-  uint64_t* sc_free = bars + 14;
-  uint64_t* unit_full = bars + 16;     // [RING]
+  uint64_t* s_full = bars + 8;         // [NQ][2], by tile parity
+  uint64_t* pv_done = bars + 12;       // [NQ]
+  uint64_t* sc_full = bars + 14;       // [4]: scales
+  uint64_t* sc_free = bars + 18;
+  uint64_t* unit_full = bars + 22;     // [RING]
   uint32_t* misc = reinterpret_cast<uint32_t*>(smem + L::MISC_OFF);
   int* err = reinterpret_cast<int*>(misc + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 2);
@@ -180,7 +185,10 @@ __global__ void __launch_bounds__(TcLay<HD, NQ>::THREADS, NQ == 1 ? 2 : 1)
       mbar_init(&v_full[i], CONV);
       mbar_init(&v_free[i], NQ);
       mbar_init(&s_full[i], 1);
-      mbar_init(&o_full[i], 1);
+      mbar_init(&s_full[2 + i], 1);
+      mbar_init(&pv_done[i], 1);
+    }
+    for (int i = 0; i < 4; ++i) {
       mbar_init(&sc_full[i], NB);
       mbar_init(&sc_free[i], 128 * NQ);
     }
@@ -211,94 +219,111 @@ __global__ void __launch_bounds__(TcLay<HD, NQ>::THREADS, NQ == 1 ? 2 : 1)
     const int q = warp >> 2, quad = warp & 3, i = quad * 32 + lane;   // MMA row of tile q
     const int r = q * 128 + i % (128 / C), copy = i / (128 / C);      // row of the run, its copy
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;
-    const uint32_t s_mma = tmem + q * 64, q_mma = tmem + NQ * 64 + q * 64, o_mma = tmem + NQ * 128 + q * 128;
+    const uint32_t s_mma = tmem + q * 128, o_mma = tmem + NQ * 128 + q * 128;   // S: two buffers
     const uint32_t s_col = s_mma + lanes, o_col = o_mma + lanes;
     const uint32_t kb = smem_u32(smem + L::K_OFF), vb = smem_u32(smem + L::V_OFF);
+    uint8_t* qs = smem + L::Q_OFF + q * L::KH * L::Q_SUB;
+    float* rfs = reinterpret_cast<float*>(smem + L::RF_OFF) + q * 128;
     // the MMAs of this row tile, by warp 0 of its four: S of tile n; w V of tile n
     auto scores = [&](int n) {
-      const int st = n & 1;
-      wait(&k_full[st], (n >> 1) & 1);
+      const int st = n % L::STAGES;
+      wait(&k_full[st], (n / L::STAGES) & 1);
       if (ok && lane == 0) {
         tc_fence_after();
-        // a step along K moves the descriptor's start address (in 16 bytes)
-        const uint64_t kd = smem_desc_sw128(kb + st * L::MAT);
+        // a step along K moves the descriptors' start address (in 16 bytes)
+        const uint64_t qd = smem_desc_sw128(smem_u32(qs)), kd = smem_desc_sw128(kb + st * L::MAT);
 #pragma unroll
         for (int k = 0; k < HD / 16; ++k)
-          tc_mma_ts(s_mma, q_mma + k * 8, kd + (((k >> 2) * L::SUB + (k & 3) * 32) >> 4),
-                    idesc_f32acc(KEYS, true), k > 0);
-        tc_commit(&s_full[q]);
+          tc_mma(s_mma + (n & 1) * 64, qd + (((k >> 2) * L::Q_SUB + (k & 3) * 32) >> 4),
+                 kd + (((k >> 2) * L::SUB + (k & 3) * 32) >> 4), idesc_f32acc(KEYS, true), k > 0);
+        tc_commit(&s_full[2 * q + (n & 1)]);
         tc_commit(&k_free[st]);
       }
       __syncwarp();
     };
-    auto products = [&](int n, bool first, bool last) {
-      const int st = n & 1;
-      wait(&v_full[st], (n >> 1) & 1);
+    auto products = [&](int n, bool first) {
+      const int st = n % L::STAGES;
+      wait(&v_full[st], (n / L::STAGES) & 1);
       if (ok && lane == 0) {
         tc_fence_after();
         const uint64_t vd = smem_desc_sw128_mn(vb + st * L::MAT, L::SUB, 1024);
 #pragma unroll
         for (int k = 0; k < KEYS / 16; ++k)
-          tc_mma_ts(o_mma, s_mma + k * 8, vd + (k * 2048 >> 4), idesc_f32acc_bmn(HD, true),
-                    !first || k > 0);
+          tc_mma_ts(o_mma, s_mma + (n & 1) * 64 + k * 8, vd + (k * 2048 >> 4),
+                    idesc_f32acc_bmn(HD, true), !first || k > 0);
+        tc_commit(&pv_done[q]);
         tc_commit(&v_free[st]);
-        if (last) tc_commit(&o_full[q]);
       }
       __syncwarp();
     };
-    int n_tile = 0, n_seg = 0;
+    int n_tile = 0;
     while (walk_next(walk, P, R, &sg)) {
       const int rr = sg.row0 + r;
       const int k_lo = sg.p_lo * PAGE, k_hi = min(sg.len, sg.p_hi * PAGE);
       const int tiles = (k_hi - k_lo + KEYS - 1) / KEYS;
-      // ---- this row of q, scaled by a power of two, into TMEM as packed fp16
-      float rf;
+      // ---- q, scaled per row by a power of two, into the swizzled A tile: HD / 8
+      // lanes a row, 16 bytes each; every warp a quarter of the rows, all copies
       {
-        const bool have = rr < sg.rows;
-        const uint4* src = reinterpret_cast<const uint4*>(
-            reinterpret_cast<const T*>(a.q) + (int64_t)(sg.r_lo + (have ? rr / rep : 0)) * a.q_strides[0] +
-            (int64_t)(sg.g * rep + (have ? rr % rep : 0)) * a.q_strides[1]);
-        uint4 raw[HD / 8];
+        constexpr int LR = HD / 8, RPW = 128 / C / 4, STEP = 32 / LR, N = RPW / STEP;
+        constexpr int B = N < 8 ? N : 8;   // rows of a lane that are loaded at once
+        const int ch = lane % LR, row_a = quad * RPW + lane / LR;   // row of the MMA tile
+        const int first = sg.row0 + q * 128 + row_a;
+        int token = first / rep, head = first % rep;
+#pragma unroll 1
+        for (int j0 = 0; j0 < N; j0 += B) {
+          uint4 raw[B];
 #pragma unroll
-        for (int j = 0; j < HD / 8; ++j) raw[j] = have ? src[j] : make_uint4(0, 0, 0, 0);
-        float top = 0.0f;
+          for (int j = 0; j < B; ++j) {
+            raw[j] = make_uint4(0, 0, 0, 0);
+            if (first + (j0 + j) * STEP < sg.rows)
+              raw[j] = *reinterpret_cast<const uint4*>(
+                  reinterpret_cast<const T*>(a.q) + (int64_t)(sg.r_lo + token) * a.q_strides[0] +
+                  (int64_t)(sg.g * rep + head) * a.q_strides[1] + ch * 8);
+            for (head += STEP; head >= rep; head -= rep) ++token;
+          }
 #pragma unroll
-        for (int j = 0; j < HD / 8; ++j) {
-          const T* e = reinterpret_cast<const T*>(&raw[j]);
+          for (int j = 0; j < B; ++j) {
+            const T* e = reinterpret_cast<const T*>(&raw[j]);
+            float top = 0.0f;
 #pragma unroll
-          for (int m = 0; m < 8; ++m) top = fmaxf(top, fabsf(to_f<T>(e[m])));
-        }
-        const int up = q_shift(top);
-        const float mul = exp2_int(up);
-        rf = a.scale * LOG2E * exp2_int(-up);
+            for (int m = 0; m < 8; ++m) top = fmaxf(top, fabsf(to_f<T>(e[m])));
 #pragma unroll
-        for (int j0 = 0; j0 < HD / 8; j0 += 8) {   // 64 dims: 32 columns
-          uint32_t h[32];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const T* e = reinterpret_cast<const T*>(&raw[j0 + j]);
+            for (int o = LR / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const int up = q_shift(top), row = row_a + (j0 + j) * STEP;
+            const float mul = exp2_int(up);
+            uint32_t h[4];
 #pragma unroll
             for (int m = 0; m < 4; ++m)
-              h[4 * j + m] = pack_h2(to_f<T>(e[2 * m]) * mul, to_f<T>(e[2 * m + 1]) * mul);
+              h[m] = pack_h2(to_f<T>(e[2 * m]) * mul, to_f<T>(e[2 * m + 1]) * mul);
+#pragma unroll
+            for (int k = 0; k < C; ++k) {
+              const int at = k * (128 / C) + row;
+              *reinterpret_cast<uint4*>(qs + (ch >> 3) * L::Q_SUB + at * 128 + (((ch & 7) ^ (at & 7)) << 4)) =
+                  make_uint4(h[0], h[1], h[2], h[3]);
+            }
+            if (ch == 0) rfs[row] = a.scale * LOG2E * exp2_int(-up);
           }
-          if (ok) tmem_st<32>(q_mma + lanes + j0 * 4, h);
         }
-        if (ok) tmem_wait_st();
-        tc_fence_before();
+        fence_proxy_async_smem();
         named_bar(1 + q, 128);
-        if (quad == 0 && tiles > 0) scores(n_tile);
+        if (quad == 0) {
+          if (tiles > 0) scores(n_tile);
+          if (tiles > 1) scores(n_tile + 1);
+        }
       }
+      const float rf = rfs[i % (128 / C)];
       float M = -INFINITY, l = 0.0f;
       for (int t = 0; t < tiles; ++t, ++n_tile) {
         const int k0 = k_lo + t * KEYS + copy * NC;   // first key of this thread's columns
-        const float* sc = reinterpret_cast<const float*>(smem + L::SC_OFF) + (n_tile & 1) * 3 * NB +
+        const float* sc = reinterpret_cast<const float*>(smem + L::SC_OFF) + (n_tile & 3) * 3 * NB +
                           copy * (NC / 16);
-        wait(&s_full[q], n_tile & 1);
-        wait(&sc_full[n_tile & 1], (n_tile >> 1) & 1);
+        wait(&s_full[2 * q + (n_tile & 1)], (n_tile >> 1) & 1);
+        wait(&sc_full[n_tile & 3], (n_tile >> 2) & 1);
         if (ok) {
           tc_fence_after();
           float v[NC], mx = -INFINITY;
-          tmem_ld<NC>(s_col + copy * NC, v);
+          const uint32_t buf = s_col + (n_tile & 1) * 64;
+          tmem_ld<NC>(buf + copy * NC, v);
 #pragma unroll
           for (int b = 0; b < NC / 16; ++b) {
             const float f = rf * sc[b], g = sc[NB + b];
@@ -334,16 +359,16 @@ __global__ void __launch_bounds__(TcLay<HD, NQ>::THREADS, NQ == 1 ? 2 : 1)
             sum = fmaf(part[0] + part[1], sc[2 * NB + b], sum);
           }
           // over the scores' first 32 columns (this warp has read its lanes)
-          tmem_st<NC / 2>(s_col + copy * (NC / 2), w);
+          tmem_st<NC / 2>(buf + copy * (NC / 2), w);
           if constexpr (C > 1) {
             const uint32_t zero[8] = {};
 #pragma unroll
             for (int o = 0; o < KEYS / 2; o += 8)
-              if (o / (NC / 2) != copy) tmem_st<8>(s_col + o, zero);
+              if (o / (NC / 2) != copy) tmem_st<8>(buf + o, zero);
           }
           l = fmaf(l, alpha, sum);
-          if (t > 0 && __any_sync(0xffffffffu, move)) {
-            // S of this tile came after the products before it: O is still
+          if (t > 0 && __any_sync(0xffffffffu, move) && wait(&pv_done[q], (n_tile - 1) & 1)) {
+            tc_fence_after();   // the products before are done: O is still
 #pragma unroll 1
             for (int c0 = 0; c0 < HD; c0 += 32) {
               float o[32];
@@ -356,18 +381,17 @@ __global__ void __launch_bounds__(TcLay<HD, NQ>::THREADS, NQ == 1 ? 2 : 1)
           tmem_wait_st();
           tc_fence_before();
         }
-        mbar_arrive(&sc_free[n_tile & 1]);
+        mbar_arrive(&sc_free[n_tile & 3]);
         named_bar(1 + q, 128);   // the tile's weights are written, O is rescaled
         if (quad == 0) {
-          products(n_tile, t == 0, t + 1 == tiles);
-          if (t + 1 < tiles) scores(n_tile + 1);
+          products(n_tile, t == 0);
+          if (t + 2 < tiles) scores(n_tile + 2);
         }
       }
       // ---- the run's output, or its part: the copies of a row add up, scaled to
       // their common reference, DIMS dims at a time
-      const bool have_o = tiles > 0 && wait(&o_full[q], n_seg & 1);
+      const bool have_o = tiles > 0 && wait(&pv_done[q], (n_tile - 1) & 1);
       tc_fence_after();
-      if (tiles > 0) ++n_seg;
       {
         constexpr int RQ = 128 / C, DIMS = L::DIMS, XROW = L::XROW, LR = DIMS / 4;
         const int64_t slot = ((int64_t)blockIdx.x * 2 + (sg.p_lo == 0)) * R;
@@ -432,11 +456,15 @@ __global__ void __launch_bounds__(TcLay<HD, NQ>::THREADS, NQ == 1 ? 2 : 1)
     // even and an odd row, whose swizzled chunks are on different banks
     const int row0 = ct >> 2, ch = ct & 3;
     uint8_t* ring = smem + L::RING_OFF;
-    int n_tile = 0;
-    uint32_t n_unit = 0;                       // units consumed; unit u of a run: K, V of tile u / 2
+    int n_tile = 0;                            // tiles and units of the runs before
+    uint32_t n_unit = 0;
     while (walk_next(walk, P, R, &sg)) {
       const int32_t* table = c.page_table + (int64_t)sg.seq * c.table_stride;
-      const int tiles = max(0, sg.p_hi - sg.p_lo);
+      // units: K 0, K 1, V 0, K 2, V 1, ..: K runs a tile ahead of V, whose tile
+      // waits for the products before
+      const int tiles = max(0, sg.p_hi - sg.p_lo), units = 2 * tiles;
+      auto is_v = [&](int u) { return u > 0 && (u == units - 1 || (u & 1) == 0); };
+      auto tile_of = [&](int u) { return u == units - 1 ? tiles - 1 : u & 1 ? (u + 1) / 2 : max(u / 2 - 1, 0); };
       // page ids of 32 tiles, one a lane of the first warp (which copies and
       // fetches the scales)
       int ids = -1, ids_at = -32;
@@ -453,7 +481,7 @@ __global__ void __launch_bounds__(TcLay<HD, NQ>::THREADS, NQ == 1 ? 2 : 1)
         return __shfl_sync(0xffffffffu, ids, t - ids_at);
       };
       auto copy_unit = [&](int u) {   // by the first warp
-        const int page = page_of(u >> 1), slot = (n_unit + u) % L::RING;
+        const int page = page_of(tile_of(u)), slot = (n_unit + u) % L::RING;
         if (lane == 0) {
           unit_page[slot] = page;
           if (page < 0) {
@@ -461,31 +489,32 @@ __global__ void __launch_bounds__(TcLay<HD, NQ>::THREADS, NQ == 1 ? 2 : 1)
           } else {
             mbar_arrive_expect_tx(&unit_full[slot], L::UNIT);
             bulk_load(ring + slot * L::UNIT,
-                      (u & 1 ? c.v : c.k) + (int64_t)page * c.page_stride + (int64_t)sg.g * L::UNIT,
+                      (is_v(u) ? c.v : c.k) + (int64_t)page * c.page_stride + (int64_t)sg.g * L::UNIT,
                       L::UNIT, &unit_full[slot]);
           }
         }
         __syncwarp();
       };
-      float ks = 0.0f, vs = -1.0f;   // scales of block ct of the next tile (vs < 0: no key)
+      float ks = 0.0f, vs = 0.0f;    // scales of block ct of the next tile, as they arrive
+      bool live = false;             // whether it has keys
       auto load_scales = [&](int t) {
-        const int page = unit_page[(n_unit + 2 * t) % L::RING];   // on its way by now
-        ks = 0.0f;
-        vs = -1.0f;
-        if (ct < NB && page >= 0 && (sg.p_lo + t) * PAGE + ct * 16 < sg.len) {
+        const int page = unit_page[(n_unit + max(2 * t - 1, 0)) % L::RING];   // K's unit is on its way by now
+        live = ct < NB && page >= 0 && (sg.p_lo + t) * PAGE + ct * 16 < sg.len;
+        if (live) {
           const int64_t so = (int64_t)page * c.scale_stride + sg.g * 4 + ct;
           ks = c.k_scale[so];
-          vs = fmaxf(c.v_scale[so], 0.0f);
+          vs = c.v_scale[so];
         }
       };
-      const int units = 2 * tiles;
       if (ct < 32) {
         for (int u = 0; u < min(units, L::RING); ++u) copy_unit(u);
         if (tiles > 0) load_scales(0);
       }
       for (int u = 0; u < units; ++u) {
         const uint32_t n = n_unit + u;
-        const int slot = n % L::RING, st = n_tile & 1, use = n_tile >> 1;
+        const bool v_unit = is_v(u);
+        const int tile = tile_of(u), nt = n_tile + tile;
+        const int slot = n % L::RING, st = nt % L::STAGES, use = nt / L::STAGES;
         wait(&unit_full[slot], (n / L::RING) & 1);
         uint4 x[PER];
         const bool none = unit_page[slot] < 0;
@@ -494,9 +523,9 @@ __global__ void __launch_bounds__(TcLay<HD, NQ>::THREADS, NQ == 1 ? 2 : 1)
           x[j] = none ? make_uint4(0, 0, 0, 0)
                       : *reinterpret_cast<const uint4*>(ring + slot * L::UNIT + (j / HALVES * 32 + row0) * HD +
                                                         j % HALVES * 64 + ch * 16);
-        uint64_t* free_bar = u & 1 ? &v_free[st] : &k_free[st];
+        uint64_t* free_bar = v_unit ? &v_free[st] : &k_free[st];
         if (use > 0) wait(free_bar, (use - 1) & 1);
-        uint8_t* mat = smem + (u & 1 ? L::V_OFF : L::K_OFF) + st * L::MAT;
+        uint8_t* mat = smem + (v_unit ? L::V_OFF : L::K_OFF) + st * L::MAT;
 #pragma unroll
         for (int j = 0; j < PER; ++j) {   // 16 codes: two 16-byte chunks
           const int row = j / HALVES * 32 + row0;
@@ -513,27 +542,28 @@ __global__ void __launch_bounds__(TcLay<HD, NQ>::THREADS, NQ == 1 ? 2 : 1)
           *reinterpret_cast<uint4*>(dst + (((2 * ch + 1) ^ (row & 7)) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
         }
         fence_proxy_async_smem();
-        mbar_arrive(u & 1 ? &v_full[st] : &k_full[st]);
+        mbar_arrive(v_unit ? &v_full[st] : &k_full[st]);
         named_bar(CONV_BAR, CONV);   // every thread has read the unit
         if (ct < 32) {
           if (u + L::RING < units) copy_unit(u + L::RING);
-          if ((u & 1) == 0) {
+          if (!v_unit) {
             // this tile's scales, then the next one's on their way
-            if (n_tile >= 2) wait(&sc_free[st], (use - 1) & 1);
+            const int at = nt & 3;
+            if (nt >= 4) wait(&sc_free[at], (nt / 4 - 1) & 1);
             if (ct < NB) {
-              float* sc = reinterpret_cast<float*>(smem + L::SC_OFF) + st * 3 * NB + ct;
+              float* sc = reinterpret_cast<float*>(smem + L::SC_OFF) + at * 3 * NB + ct;
               const float v = fmaxf(vs, VS_MIN);
-              sc[0] = ks;
-              sc[NB] = vs < 0.0f ? -INFINITY : __log2f(v);
-              sc[2 * NB] = vs < 0.0f ? 0.0f : __fdividef(1.0f, v);
-              mbar_arrive(&sc_full[st]);
+              sc[0] = live ? ks : 0.0f;
+              sc[NB] = live ? __log2f(v) : -INFINITY;
+              sc[2 * NB] = live ? __fdividef(1.0f, v) : 0.0f;
+              mbar_arrive(&sc_full[at]);
             }
             __syncwarp();
-            if ((u >> 1) + 1 < tiles) load_scales((u >> 1) + 1);
+            if (tile + 1 < tiles) load_scales(tile + 1);
           }
         }
-        n_tile += u & 1;
       }
+      n_tile += tiles;
       n_unit += units;
     }
   }
