@@ -1,7 +1,8 @@
 """Build the decoder's shared library in-tree with nvcc for sm_100a.
 
 ``python -m kv_cache_decode_dualcache_b200.build`` (or ``build()``) compiles
-``csrc/*.cu`` into ``libfdllm.so`` next to this file.  Nothing is
+``csrc/*.cu`` into ``libfdllm.so`` next to this file, and the Python binding of
+the stream-ordered operators into ``_binding.so``.  Nothing is
 JIT-compiled at import time; the binding loads the prebuilt library and fails
 loudly when it is missing.
 """
@@ -19,6 +20,9 @@ LIB = os.path.join(HERE, "libfdllm.so")
 # Self-checking variant: every device access of the GEMM / epilogue bounds-
 # checked, violations recorded and reported as FDLLM_ERR_CUDA.
 LIB_CHECKS = os.path.join(HERE, "libfdllm_checks.so")
+# Python binding of the stream-ordered operators (an extension module over
+# torch's C++ interface; host code only).
+BINDING = os.path.join(HERE, "_binding.so")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -45,8 +49,38 @@ def up_to_date(lib: str = LIB) -> bool:
     return all(os.path.getmtime(p) <= t for p in _inputs())
 
 
+def build_binding(force: bool = False, verbose: bool = False) -> str:
+    import sysconfig
+
+    src = os.path.join(HERE, "csrc", "binding.cpp")
+    inputs = (src, os.path.join(ROOT, "include", "fdllm.h"))
+    if not force and os.path.exists(BINDING) and all(
+            os.path.getmtime(p) <= os.path.getmtime(BINDING) for p in inputs):
+        return BINDING
+    import torch
+
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(_nvcc()))
+    tmp = BINDING + ".tmp"
+    cmd = ["g++", "-shared", "-fPIC", "-O2", "-std=c++17", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(root, "include"),
+           "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           "-isystem", os.path.join(cuda, "include"), src, "-o", tmp, "-L", os.path.join(root, "lib"),
+           "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda",
+           "-Wl,-rpath," + os.path.join(root, "lib")]
+    if verbose:
+        print(" ".join(cmd), file=sys.stderr)
+    r = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed on binding.cpp:\n" + r.stdout.decode(errors="replace"))
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def build(force: bool = False, verbose: bool = False, extra=None, checks: bool = False) -> str:
     lib = LIB_CHECKS if checks else LIB
+    build_binding(force, verbose)
     if not force and up_to_date(lib):
         return lib
     nvcc = _nvcc()

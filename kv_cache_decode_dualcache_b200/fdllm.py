@@ -12,7 +12,6 @@ from __future__ import annotations
 
 import ctypes
 import os
-import struct
 from dataclasses import dataclass
 from typing import Dict, Mapping, Optional
 
@@ -164,11 +163,11 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.fdllm_gemm_f16.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, i32]
     lib.fdllm_attention.argtypes = [vp, vp, vp, i32, i32, i32]
     lib.fdllm_gemm_noalloc.argtypes = [vp, vp, vp, i32, i32, i32, i32, vp]
-    lib.fdllm_kv8_append.argtypes = [vp, vp, vp]        # structs by reference or packed bytes
-    lib.fdllm_kv8_attention.argtypes = [vp, vp, vp]
+    lib.fdllm_kv8_append.argtypes = [P(FdllmKv8), P(FdllmKv8AppendArgs), vp]
+    lib.fdllm_kv8_attention.argtypes = [P(FdllmKv8), P(FdllmKv8AttentionArgs), vp]
     lib.fdllm_kv8_attention_workspace.argtypes = [P(FdllmKv8), P(FdllmKv8AttentionArgs),
                                                   P(ctypes.c_size_t)]
-    lib.fdllm_sample.argtypes = [vp, vp]
+    lib.fdllm_sample.argtypes = [P(FdllmSampleArgs), vp]
     lib.fdllm_profile_enable.argtypes = [vp, i32]
     lib.fdllm_profile_read.argtypes = [vp, P(FdllmKernelStat), i32, P(i32)]
     lib.fdllm_last_error.argtypes = [vp]
@@ -436,61 +435,26 @@ KV8_PAGE, KV8_BLOCK = 64, 16              # positions per page, positions that s
 KV8_BAD_PAGE, KV8_BAD_RANGE = 1, 2        # bits of a call's status word
 
 
-# The calls below are short, so their binding is kept short: argument structs
-# are packed in one go, checks read each tensor's attributes once.
-_KV8_APPEND = struct.Struct("@4i3P6q4P2i5P")       # FdllmKv8AppendArgs
-_KV8_ATTENTION = struct.Struct("@5ifP2q3P2qPNP")   # FdllmKv8AttentionArgs
-_SAMPLE = struct.Struct("@Pq4i7P")                 # FdllmSampleArgs
-_types = None                                      # torch dtype -> fdllm_dtype
+_ops = None
 
 
-def _type_code(dtype) -> int:
-    global _types
-    if _types is None:
-        import torch
-        _types = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
-    code = _types.get(dtype)
-    if code is None:
-        raise ValueError(f"{dtype} is not a type of this call (float32, bfloat16, float16)")
-    return code
-
-
-def _vector(name: str, t, n: int, dtype, dev: int) -> int:
-    """Address of a contiguous 1-D tensor of n elements on device dev."""
-    if t.dtype is not dtype or t.numel() != n or t.dim() != 1 or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} elements")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} must be on the same CUDA device as the other operands")
-    return t.data_ptr()
-
-
-def _rows(name: str, t, tokens: int, heads: Optional[int], hd: int, dtype, dev: int):
-    """(heads, token stride, head stride, address) of [tokens, heads, hd] rows;
-    the strides of dims of one element do not matter."""
-    shape, st = t.shape, t.stride()
-    if len(shape) != 3 or shape[2] != hd or (heads is not None and shape[1] != heads) or (
-            st[2] != 1 and shape[0] > 0):
-        raise ValueError(f"{name} must be [tokens, {heads or 'heads'}, {hd}] with contiguous vectors")
-    if shape[0] != tokens or t.dtype is not dtype:
-        raise ValueError("all rows of a call must have the same number of tokens and the same type")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} must be on the same CUDA device as the other operands")
-    return shape[1], st[0] if tokens > 1 else 0, st[1] if shape[1] > 1 else 0, t.data_ptr()
-
-
-def _enqueue(fn, dev: int, stream, *args) -> None:
-    """fn(*args, stream handle) with `dev` current; stream None = torch's
-    current stream there."""
-    import torch
-    if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(dev)
-    if torch._C._cuda_getDevice() == dev:
-        rc = fn(*args, stream)
-    else:
-        with torch.cuda.device(dev):
-            rc = fn(*args, stream)
-    if rc != FDLLM_OK:
-        _check(rc, None)
+def _load_ops():
+    """The extension module that marshals the calls below (csrc/binding.cpp),
+    bound to the loaded library's entry points.  Raises when it is missing."""
+    global _ops
+    if _ops is None:
+        import torch  # noqa: F401  (its libraries, which the module links against)
+        lib = load_library()
+        try:
+            from . import _binding
+        except ImportError as e:
+            raise RuntimeError(f"the Python binding is missing or unusable ({e}): build it with "
+                               "`python -m kv_cache_decode_dualcache_b200.build`") from e
+        _binding.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+            lib.fdllm_kv8_append, lib.fdllm_kv8_attention, lib.fdllm_kv8_attention_workspace,
+            lib.fdllm_sample)))
+        _ops = _binding
+    return _ops
 
 
 class Kv8Cache:
@@ -530,8 +494,7 @@ class Kv8Cache:
             page_table.data_ptr(), k.stride(0) if n_pages > 1 else 0,
             k_scale.stride(0) if n_pages > 1 else 0, 0 if one_row else page_table.stride(0),
             n_pages, self.n_seqs, self.max_pages, heads, hd)
-        self._ref = ctypes.byref(self.struct)
-        self._workspace: Dict[tuple, int] = {}   # bytes by shape, not memory
+        self.address = ctypes.addressof(self.struct)
 
 
 def fdllm_kv8_append(cache: Kv8Cache, k, v, starts, lens, pos=None, rope=None, q=None,
@@ -542,37 +505,11 @@ def fdllm_kv8_append(cache: Kv8Cache, k, v, starts, lens, pos=None, rope=None, q
     heads, head_dim] (see the header).  Returns (q_out, k_out, v_out): the
     rotated q (None without q) and, with stored, the rows as the cache now
     stands for them (else None, None)."""
-    import torch
-    hd, dev, n, i32, dtype, T = (cache.head_dim, cache.device, cache.n_seqs, torch.int32, k.dtype,
-                                 k.shape[0])
-    _, k_token, k_head, k_ptr = _rows("k", k, T, cache.n_kv_heads, hd, dtype, dev)
-    _, v_token, v_head, v_ptr = _rows("v", v, T, cache.n_kv_heads, hd, dtype, dev)
-    heads = q_token = q_head = q_ptr = q_out_ptr = k_out_ptr = v_out_ptr = rope_ptr = rope_len = 0
-    q_out = k_out = v_out = None
-    if q is not None:
-        heads, q_token, q_head, q_ptr = _rows("q", q, T, None, hd, dtype, dev)
-        q_out = q.new_empty(q.shape)
-        q_out_ptr = q_out.data_ptr()
-    if stored:
-        both = k.new_empty((2,) + tuple(k.shape))
-        k_out, v_out = both.unbind()
-        k_out_ptr = both.data_ptr()
-        v_out_ptr = k_out_ptr + k.numel() * k.element_size()
-    if rope is not None:
-        rope_len = rope.shape[0]
-        if rope.dtype is not torch.float32 or tuple(rope.shape[1:]) != (hd // 2, 2) or \
-                not rope.is_contiguous() or rope.get_device() != dev:
-            raise ValueError(f"rope must be contiguous float32 [positions, {hd // 2}, 2] on the "
-                             "cache's device")
-        rope_ptr = rope.data_ptr()
-    a = _KV8_APPEND.pack(
-        _type_code(dtype), T, heads, max_new, k_ptr, v_ptr, q_ptr, k_token, k_head, v_token, v_head,
-        q_token, q_head, _vector("starts", starts, n + 1, i32, dev), _vector("lens", lens, n, i32, dev),
-        0 if pos is None else _vector("pos", pos, n, i32, dev), rope_ptr, rope_len, 0, k_out_ptr,
-        v_out_ptr, q_out_ptr, 0 if lens_out is None else _vector("lens_out", lens_out, n, i32, dev),
-        0 if status is None else _vector("status", status, 1, i32, dev))
-    _enqueue(load_library().fdllm_kv8_append, dev, stream, cache._ref, a)
-    return q_out, k_out, v_out
+    r = (_ops or _load_ops()).append(cache.address, cache.device, k, v, starts, lens, pos, rope, q,
+                                     max_new, stored, lens_out, status, stream)
+    if type(r) is int:
+        _check(r, None)
+    return r
 
 
 def fdllm_kv8_attention(cache: Kv8Cache, q, starts, lens, scale: Optional[float] = None, out=None,
@@ -583,51 +520,24 @@ def fdllm_kv8_attention(cache: Kv8Cache, q, starts, lens, scale: Optional[float]
     workspace: a uint8 tensor to use instead of a fresh one (its size:
     fdllm_kv8_attention_workspace); pass one when the work is enqueued on a
     stream that is not torch's current one."""
-    import torch
-    hd, dev, n, i32, dtype, T = (cache.head_dim, cache.device, cache.n_seqs, torch.int32, q.dtype,
-                                 q.shape[0])
-    heads, q_token, q_head, q_ptr = _rows("q", q, T, None, hd, dtype, dev)
-    if out is None:
-        out = q.new_empty(q.shape)
-        out_token, out_head, out_ptr = heads * hd, hd, out.data_ptr()
-    else:
-        _, out_token, out_head, out_ptr = _rows("out", out, T, heads, hd, dtype, dev)
-    ws_ptr = ws_bytes = 0
-    if workspace is None:
-        ws_bytes = fdllm_kv8_attention_workspace(cache, T, heads, dtype, max_q, max_len)
-        if ws_bytes:
-            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
-            ws_ptr = workspace.data_ptr()
-    else:
-        if workspace.get_device() != dev or not workspace.is_contiguous():
-            raise ValueError("workspace must be contiguous and on the cache's device")
-        ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    a = _KV8_ATTENTION.pack(
-        _type_code(dtype), T, heads, max_q, max_len, hd ** -0.5 if scale is None else scale, q_ptr,
-        q_token, q_head, _vector("starts", starts, n + 1, i32, dev),
-        _vector("lens", lens, n, i32, dev), out_ptr, out_token, out_head, ws_ptr, ws_bytes,
-        0 if status is None else _vector("status", status, 1, i32, dev))
-    _enqueue(load_library().fdllm_kv8_attention, dev, stream, cache._ref, a)
-    return out
+    r = (_ops or _load_ops()).attention(cache.address, cache.device, q, starts, lens, scale, out, max_q,
+                                        max_len, workspace, status, stream)
+    if type(r) is int:
+        _check(r, None)
+    return r[0]
 
 
 def fdllm_kv8_attention_workspace(cache: Kv8Cache, n_tokens: int, n_heads: int, dtype,
                                   max_q: int = 0, max_len: int = 0) -> int:
-    """Bytes of workspace for an attention call of this shape (remembered by
-    the cache object)."""
-    key = (n_tokens, n_heads, dtype, max_q, max_len)
-    need = cache._workspace.get(key)
-    if need is None:
-        import torch
-        a = FdllmKv8AttentionArgs(_type_code(dtype), n_tokens, n_heads, max_q, max_len, 1.0)
-        size = ctypes.c_size_t()
-        with torch.cuda.device(cache.device):
-            _check(load_library().fdllm_kv8_attention_workspace(cache._ref, ctypes.byref(a),
-                                                                ctypes.byref(size)), None)
-        if len(cache._workspace) >= 256:
-            cache._workspace.clear()
-        need = cache._workspace[key] = size.value
-    return need
+    """Bytes of workspace for an attention call of this shape."""
+    import torch
+    code = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}[dtype]
+    a = FdllmKv8AttentionArgs(code, n_tokens, n_heads, max_q, max_len, 1.0)
+    size = ctypes.c_size_t()
+    with torch.cuda.device(cache.device):
+        _check(load_library().fdllm_kv8_attention_workspace(
+            ctypes.byref(cache.struct), ctypes.byref(a), ctypes.byref(size)), None)
+    return size.value
 
 
 def fdllm_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None,
@@ -636,27 +546,11 @@ def fdllm_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None
     [rows] in [0, 1); temperature, top_p, min_p: float32 [rows] or None;
     top_k: int32 [rows] or None.  Returns (tok int32 [rows], prob float32
     [rows])."""
-    import torch
-    shape, st, dev, f32 = logits.shape, logits.stride(), logits.get_device(), torch.float32
-    if len(shape) != 2 or (st[1] != 1 and shape[1] > 1):
-        raise ValueError("logits must be [rows, vocab] with contiguous rows")
-    if dev < 0:
-        raise ValueError("logits must be on a CUDA device")
-    rows, vocab = shape
-    if tok is None:
-        tok = torch.empty(rows, dtype=torch.int32, device=logits.device)
-    if prob is None:
-        prob = torch.empty(rows, dtype=f32, device=logits.device)
-    a = _SAMPLE.pack(
-        logits.data_ptr(), st[0] if rows > 1 else vocab, _type_code(logits.dtype), rows, vocab, mask_id,
-        0 if temperature is None else _vector("temperature", temperature, rows, f32, dev),
-        0 if top_k is None else _vector("top_k", top_k, rows, torch.int32, dev),
-        0 if top_p is None else _vector("top_p", top_p, rows, f32, dev),
-        0 if min_p is None else _vector("min_p", min_p, rows, f32, dev),
-        _vector("u", u, rows, torch.float64, dev), _vector("tok", tok, rows, torch.int32, dev),
-        _vector("prob", prob, rows, f32, dev))
-    _enqueue(load_library().fdllm_sample, dev, stream, a)
-    return tok, prob
+    r = (_ops or _load_ops()).sample(logits, u, temperature, top_k, top_p, min_p, mask_id, tok, prob,
+                                     stream)
+    if type(r) is int:
+        _check(r, None)
+    return r
 
 
 def fdllm_profile_enable(ctx, enable: bool = True) -> None:
