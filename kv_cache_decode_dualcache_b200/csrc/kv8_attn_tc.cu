@@ -11,17 +11,16 @@
 // costs nothing: with so few rows the kernel waits for the cache.
 //
 // Roles: 4 warps a row tile for the softmax (a thread per MMA row: q, weights,
-// output; the first one's lane 0 issues the tile's MMAs), 4 converter warps.
-// A page is a tile: its codes of K (and V) of a head are contiguous and come
-// by one bulk copy each into a ring of int8 units; the converters turn them
-// into 128-byte-swizzled fp16 tiles, the blocks' scales beside them.
+// output), 4 converter warps, one MMA warp.  A page is a tile: its codes of K
+// (and V) of a head are contiguous and come by one bulk copy each into a ring
+// of int8 units; the converters turn them into 128-byte-swizzled fp16 tiles,
+// the blocks' scales beside them.
 //   S = Q K^T        tcgen05, Q and K in shared memory, S in TMEM (two buffers)
 //   w = 2^(S f + log2 vs - M + 8), written over S as packed fp16
 //   O += w V         tcgen05, w in TMEM, V MN-major from shared memory
 // with the statistics of kv8_attn.cu.  S of tile t + 1 is done before the softmax
-// of tile t is, so that the chain from tile to tile is the softmax alone; w V
-// of tile t and S of tile t + 2 are issued behind it.  With one row tile (NQ =
-// 1) two CTAs share an SM.
+// of tile t is, so that the chain from tile to tile is the softmax alone.  Tiles
+// of up to 64 query rows leave room for two CTAs an SM.
 // What shaped this: with shared memory in use there is next to no L1, so
 // loads through registers and spilled registers both starve (loads in flight
 // need L1 lines, spills go to L2); hence the bulk copies, and 64-key tiles,
@@ -65,9 +64,9 @@ struct TcLay {
   static constexpr int ML_OFF = SC_OFF + 4 * 3 * NB * 4;   // rows' (max, sum)
   static constexpr int RF_OFF = ML_OFF + NQ * 128 * 8;     // row factors
   static constexpr int BAR_OFF = RF_OFF + NQ * 128 * 4;
-  static constexpr int MISC_OFF = BAR_OFF + (22 + RING) * 8;
+  static constexpr int MISC_OFF = BAR_OFF + (31 + RING) * 8;
   static constexpr int PAGE_OFF = MISC_OFF + 16;           // the units' pages
-  static constexpr int THREADS = 128 * NQ + CONV;
+  static constexpr int THREADS = 128 * NQ + CONV + 32;
   static constexpr int WALK_OFF = (PAGE_OFF + RING * 4 + 15) / 16 * 16;
   static constexpr int SMEM = WALK_OFF + THREADS / 32 * (int)sizeof(Walk) + 1024;   // slack for
                                                                                     // 1024-byte alignment
@@ -151,7 +150,7 @@ template <int N> FD_DEV void tmem_st(uint32_t taddr, const uint32_t* v) {
 FD_DEV void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 template <typename T, int HD, int NQ, int C>
-__global__ void __launch_bounds__(TcLay<HD, NQ>::THREADS, NQ == 1 ? 2 : 1)
+__global__ void __launch_bounds__(TcLay<HD, NQ>::THREADS, C > 1 ? 2 : 1)
     kv8_attn_tc_kernel(const AttnP P) {
   using L = TcLay<HD, NQ>;
   constexpr int R = NQ * 128 / C;      // query rows of a run
@@ -165,10 +164,14 @@ __global__ void __launch_bounds__(TcLay<HD, NQ>::THREADS, NQ == 1 ? 2 : 1)
   uint64_t* v_full = bars + 4;
   uint64_t* v_free = bars + 6;
   uint64_t* s_full = bars + 8;         // [NQ][2], by tile parity
-  uint64_t* pv_done = bars + 12;       // [NQ]
+  uint64_t* pv_done = bars + 27;       // [NQ][2], by tile parity
   uint64_t* sc_full = bars + 14;       // [4]: scales
   uint64_t* sc_free = bars + 18;
-  uint64_t* unit_full = bars + 22;     // [RING]
+  // [NQ][2], by tile parity (the softmax may be a tile ahead of the products):
+  // weights written, O rescaled
+  uint64_t* p_full = bars + 22;
+  uint64_t* q_full = bars + 26;
+  uint64_t* unit_full = bars + 31;     // [RING]
   uint32_t* misc = reinterpret_cast<uint32_t*>(smem + L::MISC_OFF);
   int* err = reinterpret_cast<int*>(misc + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 2);
@@ -181,17 +184,21 @@ __global__ void __launch_bounds__(TcLay<HD, NQ>::THREADS, NQ == 1 ? 2 : 1)
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&k_full[i], CONV);
-      mbar_init(&k_free[i], NQ);
+      mbar_init(&k_free[i], 1);
       mbar_init(&v_full[i], CONV);
-      mbar_init(&v_free[i], NQ);
+      mbar_init(&v_free[i], 1);
       mbar_init(&s_full[i], 1);
       mbar_init(&s_full[2 + i], 1);
       mbar_init(&pv_done[i], 1);
+      mbar_init(&pv_done[2 + i], 1);
+      mbar_init(&p_full[i], 128);
+      mbar_init(&p_full[2 + i], 128);
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(&sc_full[i], NB);
       mbar_init(&sc_free[i], 128 * NQ);
     }
+    mbar_init(q_full, 128 * NQ);
     for (int i = 0; i < L::RING; ++i) mbar_init(&unit_full[i], 1);
     *err = 0;
     *abort_flag = 0;
@@ -219,43 +226,10 @@ __global__ void __launch_bounds__(TcLay<HD, NQ>::THREADS, NQ == 1 ? 2 : 1)
     const int q = warp >> 2, quad = warp & 3, i = quad * 32 + lane;   // MMA row of tile q
     const int r = q * 128 + i % (128 / C), copy = i / (128 / C);      // row of the run, its copy
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;
-    const uint32_t s_mma = tmem + q * 128, o_mma = tmem + NQ * 128 + q * 128;   // S: two buffers
-    const uint32_t s_col = s_mma + lanes, o_col = o_mma + lanes;
-    const uint32_t kb = smem_u32(smem + L::K_OFF), vb = smem_u32(smem + L::V_OFF);
+    const uint32_t s_col = tmem + q * 128 + lanes, o_col = s_col + NQ * 128;   // S: two buffers
     uint8_t* qs = smem + L::Q_OFF + q * L::KH * L::Q_SUB;
     float* rfs = reinterpret_cast<float*>(smem + L::RF_OFF) + q * 128;
-    // the MMAs of this row tile, by warp 0 of its four: S of tile n; w V of tile n
-    auto scores = [&](int n) {
-      const int st = n % L::STAGES;
-      wait(&k_full[st], (n / L::STAGES) & 1);
-      if (ok && lane == 0) {
-        tc_fence_after();
-        // a step along K moves the descriptors' start address (in 16 bytes)
-        const uint64_t qd = smem_desc_sw128(smem_u32(qs)), kd = smem_desc_sw128(kb + st * L::MAT);
-#pragma unroll
-        for (int k = 0; k < HD / 16; ++k)
-          tc_mma(s_mma + (n & 1) * 64, qd + (((k >> 2) * L::Q_SUB + (k & 3) * 32) >> 4),
-                 kd + (((k >> 2) * L::SUB + (k & 3) * 32) >> 4), idesc_f32acc(KEYS, true), k > 0);
-        tc_commit(&s_full[2 * q + (n & 1)]);
-        tc_commit(&k_free[st]);
-      }
-      __syncwarp();
-    };
-    auto products = [&](int n, bool first) {
-      const int st = n % L::STAGES;
-      wait(&v_full[st], (n / L::STAGES) & 1);
-      if (ok && lane == 0) {
-        tc_fence_after();
-        const uint64_t vd = smem_desc_sw128_mn(vb + st * L::MAT, L::SUB, 1024);
-#pragma unroll
-        for (int k = 0; k < KEYS / 16; ++k)
-          tc_mma_ts(o_mma, s_mma + (n & 1) * 64 + k * 8, vd + (k * 2048 >> 4),
-                    idesc_f32acc_bmn(HD, true), !first || k > 0);
-        tc_commit(&pv_done[q]);
-        tc_commit(&v_free[st]);
-      }
-      __syncwarp();
-    };
+    auto pv_wait = [&](int n) { return wait(&pv_done[2 * q + (n & 1)], (n >> 1) & 1); };
     int n_tile = 0;
     while (walk_next(walk, P, R, &sg)) {
       const int rr = sg.row0 + r;
@@ -305,11 +279,8 @@ __global__ void __launch_bounds__(TcLay<HD, NQ>::THREADS, NQ == 1 ? 2 : 1)
           }
         }
         fence_proxy_async_smem();
-        named_bar(1 + q, 128);
-        if (quad == 0) {
-          if (tiles > 0) scores(n_tile);
-          if (tiles > 1) scores(n_tile + 1);
-        }
+        if (tiles > 0) mbar_arrive(q_full);   // runs without keys have no MMAs
+        named_bar(1 + q, 128);   // rfs
       }
       const float rf = rfs[i % (128 / C)];
       float M = -INFINITY, l = 0.0f;
@@ -367,7 +338,7 @@ __global__ void __launch_bounds__(TcLay<HD, NQ>::THREADS, NQ == 1 ? 2 : 1)
               if (o / (NC / 2) != copy) tmem_st<8>(buf + o, zero);
           }
           l = fmaf(l, alpha, sum);
-          if (t > 0 && __any_sync(0xffffffffu, move) && wait(&pv_done[q], (n_tile - 1) & 1)) {
+          if (t > 0 && __any_sync(0xffffffffu, move) && pv_wait(n_tile - 1)) {
             tc_fence_after();   // the products before are done: O is still
 #pragma unroll 1
             for (int c0 = 0; c0 < HD; c0 += 32) {
@@ -382,15 +353,11 @@ __global__ void __launch_bounds__(TcLay<HD, NQ>::THREADS, NQ == 1 ? 2 : 1)
           tc_fence_before();
         }
         mbar_arrive(&sc_free[n_tile & 3]);
-        named_bar(1 + q, 128);   // the tile's weights are written, O is rescaled
-        if (quad == 0) {
-          products(n_tile, t == 0);
-          if (t + 2 < tiles) scores(n_tile + 2);
-        }
+        mbar_arrive(&p_full[2 * q + (n_tile & 1)]);
       }
       // ---- the run's output, or its part: the copies of a row add up, scaled to
       // their common reference, DIMS dims at a time
-      const bool have_o = tiles > 0 && wait(&pv_done[q], (n_tile - 1) & 1);
+      const bool have_o = tiles > 0 && pv_wait(n_tile - 1);
       tc_fence_after();
       {
         constexpr int RQ = 128 / C, DIMS = L::DIMS, XROW = L::XROW, LR = DIMS / 4;
@@ -447,7 +414,7 @@ __global__ void __launch_bounds__(TcLay<HD, NQ>::THREADS, NQ == 1 ? 2 : 1)
       }
       tc_fence_before();   // O has been read before the next run's first product
     }
-  } else {
+  } else if (warp < 4 * NQ + CONV / 32) {
     // ================================================== converters
     const int ct = tid - 128 * NQ;
     constexpr int HALVES = HD / 64;            // 64-byte halves of a key
@@ -510,24 +477,20 @@ __global__ void __launch_bounds__(TcLay<HD, NQ>::THREADS, NQ == 1 ? 2 : 1)
         for (int u = 0; u < min(units, L::RING); ++u) copy_unit(u);
         if (tiles > 0) load_scales(0);
       }
-      for (int u = 0; u < units; ++u) {
+      auto read_unit = [&](int u, uint4* x) {
         const uint32_t n = n_unit + u;
-        const bool v_unit = is_v(u);
-        const int tile = tile_of(u), nt = n_tile + tile;
-        const int slot = n % L::RING, st = nt % L::STAGES, use = nt / L::STAGES;
+        const int slot = n % L::RING;
         wait(&unit_full[slot], (n / L::RING) & 1);
-        uint4 x[PER];
         const bool none = unit_page[slot] < 0;
 #pragma unroll
         for (int j = 0; j < PER; ++j)
           x[j] = none ? make_uint4(0, 0, 0, 0)
                       : *reinterpret_cast<const uint4*>(ring + slot * L::UNIT + (j / HALVES * 32 + row0) * HD +
                                                         j % HALVES * 64 + ch * 16);
-        uint64_t* free_bar = v_unit ? &v_free[st] : &k_free[st];
-        if (use > 0) wait(free_bar, (use - 1) & 1);
-        uint8_t* mat = smem + (v_unit ? L::V_OFF : L::K_OFF) + st * L::MAT;
+      };
+      auto put = [&](uint8_t* mat, const uint4* x) {   // 16 codes: two 16-byte chunks
 #pragma unroll
-        for (int j = 0; j < PER; ++j) {   // 16 codes: two 16-byte chunks
+        for (int j = 0; j < PER; ++j) {
           const int row = j / HALVES * 32 + row0;
           const uint32_t y[4] = {x[j].x ^ 0x80808080u, x[j].y ^ 0x80808080u, x[j].z ^ 0x80808080u,
                                  x[j].w ^ 0x80808080u};
@@ -542,14 +505,28 @@ __global__ void __launch_bounds__(TcLay<HD, NQ>::THREADS, NQ == 1 ? 2 : 1)
           *reinterpret_cast<uint4*>(dst + (((2 * ch + 1) ^ (row & 7)) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
         }
         fence_proxy_async_smem();
-        mbar_arrive(v_unit ? &v_full[st] : &k_full[st]);
-        named_bar(CONV_BAR, CONV);   // every thread has read the unit
+      };
+      int u = 0;
+      for (int j = 0; tiles > 0 && j <= tiles; ++j) {   // K of tile j, V of tile j - 1
+        uint4 xk[PER], xv[PER];
+        const bool has_k = j < tiles, has_v = j > 0;
+        const int u0 = u, nk = n_tile + j, nv = nk - 1;
+        if (has_k) read_unit(u++, xk);
+        if (has_v) read_unit(u++, xv);
+        if (has_k) {
+          const int st = nk % L::STAGES, use = nk / L::STAGES;
+          if (use > 0) wait(&k_free[st], (use - 1) & 1);
+          put(smem + L::K_OFF + st * L::MAT, xk);
+          mbar_arrive(&k_full[st]);
+        }
+        named_bar(CONV_BAR, CONV);   // every thread has read the units
         if (ct < 32) {
-          if (u + L::RING < units) copy_unit(u + L::RING);
-          if (!v_unit) {
+          for (int w = u0; w < u; ++w)
+            if (w + L::RING < units) copy_unit(w + L::RING);
+          if (has_k) {
             // this tile's scales, then the next one's on their way
-            const int at = nt & 3;
-            if (nt >= 4) wait(&sc_free[at], (nt / 4 - 1) & 1);
+            const int at = nk & 3;
+            if (nk >= 4) wait(&sc_free[at], (nk / 4 - 1) & 1);
             if (ct < NB) {
               float* sc = reinterpret_cast<float*>(smem + L::SC_OFF) + at * 3 * NB + ct;
               const float v = fmaxf(vs, VS_MIN);
@@ -559,12 +536,70 @@ __global__ void __launch_bounds__(TcLay<HD, NQ>::THREADS, NQ == 1 ? 2 : 1)
               mbar_arrive(&sc_full[at]);
             }
             __syncwarp();
-            if (tile + 1 < tiles) load_scales(tile + 1);
+            if (j + 1 < tiles) load_scales(j + 1);
           }
+        }
+        if (has_v) {
+          const int st = nv % L::STAGES, use = nv / L::STAGES;
+          if (use > 0) wait(&v_free[st], (use - 1) & 1);
+          put(smem + L::V_OFF + st * L::MAT, xv);
+          mbar_arrive(&v_full[st]);
         }
       }
       n_tile += tiles;
       n_unit += units;
+    }
+  } else {
+    // ================================================== MMA
+    const uint32_t kb = smem_u32(smem + L::K_OFF), vb = smem_u32(smem + L::V_OFF);
+    const uint32_t qb = smem_u32(smem + L::Q_OFF);
+    int n_tile = 0, n_seg = 0;
+    while (walk_next(walk, P, R, &sg)) {
+      const int tiles = max(0, sg.p_hi - sg.p_lo);
+      if (tiles > 0) wait(q_full, n_seg++ & 1);
+      for (int t = 0; tiles > 0 && t <= tiles; ++t) {
+        // S of tile t, then w V of tile t - 1 (whose weights lie in S's other buffer)
+        if (t < tiles) {
+          const int n = n_tile + t, st = n % L::STAGES;
+          wait(&k_full[st], (n / L::STAGES) & 1);
+          if (ok && lane == 0) {
+            tc_fence_after();
+            // a step along K moves the descriptors' start address (in 16 bytes)
+            const uint64_t kd = smem_desc_sw128(kb + st * L::MAT);
+#pragma unroll
+            for (int q = 0; q < NQ; ++q) {
+              const uint64_t qd = smem_desc_sw128(qb + q * L::KH * L::Q_SUB);
+#pragma unroll
+              for (int k = 0; k < HD / 16; ++k)
+                tc_mma(tmem + q * 128 + (n & 1) * 64, qd + (((k >> 2) * L::Q_SUB + (k & 3) * 32) >> 4),
+                       kd + (((k >> 2) * L::SUB + (k & 3) * 32) >> 4), idesc_f32acc(KEYS, true), k > 0);
+              tc_commit(&s_full[2 * q + (n & 1)]);
+            }
+            tc_commit(&k_free[st]);
+          }
+          __syncwarp();
+        }
+        if (t > 0) {
+          const int n = n_tile + t - 1, st = n % L::STAGES;
+          wait(&v_full[st], (n / L::STAGES) & 1);
+          const uint64_t vd = smem_desc_sw128_mn(vb + st * L::MAT, L::SUB, 1024);
+#pragma unroll
+          for (int q = 0; q < NQ; ++q) {
+            wait(&p_full[2 * q + (n & 1)], (n >> 1) & 1);
+            if (ok && lane == 0) {
+              tc_fence_after();
+#pragma unroll
+              for (int k = 0; k < KEYS / 16; ++k)
+                tc_mma_ts(tmem + NQ * 128 + q * 128, tmem + q * 128 + (n & 1) * 64 + k * 8,
+                          vd + (k * 2048 >> 4), idesc_f32acc_bmn(HD, true), t > 1 || k > 0);
+              tc_commit(&pv_done[2 * q + (n & 1)]);
+              if (q == NQ - 1) tc_commit(&v_free[st]);
+            }
+            __syncwarp();
+          }
+        }
+      }
+      n_tile += tiles;
     }
   }
   tc_fence_before();
@@ -600,7 +635,7 @@ cudaError_t launch_tc_hd(const AttnP& P, int rows, cudaStream_t st) {
 namespace kv8 {
 
 int tc_tile_rows(int64_t rows) { return rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 128 ? 128 : 256; }
-int tc_ctas_per_sm(int tile_rows) { return tile_rows == 256 ? 1 : 2; }
+int tc_ctas_per_sm(int tile_rows) { return tile_rows > 64 ? 1 : 2; }
 
 cudaError_t launch_attn_tc(const AttnP& P, int rows, cudaStream_t st) {
   if (P.a.dtype == FDLLM_DTYPE_BF16)
