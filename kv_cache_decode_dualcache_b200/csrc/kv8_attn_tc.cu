@@ -11,10 +11,10 @@
 // costs nothing: with so few rows the kernel waits for the cache.
 //
 // Roles: 4 warps a row tile for the softmax (a thread per MMA row: q, weights,
-// output), 4 converter warps, one MMA warp.  A page is a tile: its codes of K
-// (and V) of a head are contiguous and come by one bulk copy each into a ring
-// of int8 units; the converters turn them into 128-byte-swizzled fp16 tiles,
-// the blocks' scales beside them.
+// output), 4 converter warps, one MMA warp, one copy warp.  A page is a tile:
+// its codes of K (and V) of a head are contiguous and come by one bulk copy
+// each into a ring of int8 units; the converters turn them into
+// 128-byte-swizzled fp16 tiles, and the copy warp fetches the blocks' scales.
 //   S = Q K^T        tcgen05, Q and K in shared memory, S in TMEM (two buffers)
 //   w = 2^(S f + log2 vs - M + 8), written over S as packed fp16
 //   O += w V         tcgen05, w in TMEM, V MN-major from shared memory
@@ -41,7 +41,6 @@ using namespace kv8;
 constexpr int KEYS = PAGE;           // keys of a tile
 constexpr int NB = KEYS / FDLLM_KV8_BLOCK;
 constexpr int CONV = 128;            // converter threads
-constexpr int CONV_BAR = 5;          // named barrier of the converters
 
 template <int HD, int NQ>
 struct TcLay {
@@ -64,9 +63,9 @@ struct TcLay {
   static constexpr int ML_OFF = SC_OFF + 4 * 3 * NB * 4;   // rows' (max, sum)
   static constexpr int RF_OFF = ML_OFF + NQ * 128 * 8;     // row factors
   static constexpr int BAR_OFF = RF_OFF + NQ * 128 * 4;
-  static constexpr int MISC_OFF = BAR_OFF + (31 + RING) * 8;
+  static constexpr int MISC_OFF = BAR_OFF + (31 + 2 * RING) * 8;
   static constexpr int PAGE_OFF = MISC_OFF + 16;           // the units' pages
-  static constexpr int THREADS = 128 * NQ + CONV + 32;
+  static constexpr int THREADS = 128 * NQ + CONV + 64;
   static constexpr int WALK_OFF = (PAGE_OFF + RING * 4 + 15) / 16 * 16;
   static constexpr int SMEM = WALK_OFF + THREADS / 32 * (int)sizeof(Walk) + 1024;   // slack for
                                                                                     // 1024-byte alignment
@@ -172,6 +171,7 @@ __global__ void __launch_bounds__(TcLay<HD, NQ>::THREADS, C > 1 ? 2 : 1)
   uint64_t* p_full = bars + 22;
   uint64_t* q_full = bars + 26;
   uint64_t* unit_full = bars + 31;     // [RING]
+  uint64_t* unit_free = unit_full + L::RING;
   uint32_t* misc = reinterpret_cast<uint32_t*>(smem + L::MISC_OFF);
   int* err = reinterpret_cast<int*>(misc + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 2);
@@ -199,7 +199,10 @@ __global__ void __launch_bounds__(TcLay<HD, NQ>::THREADS, C > 1 ? 2 : 1)
       mbar_init(&sc_free[i], 128 * NQ);
     }
     mbar_init(q_full, 128 * NQ);
-    for (int i = 0; i < L::RING; ++i) mbar_init(&unit_full[i], 1);
+    for (int i = 0; i < L::RING; ++i) {
+      mbar_init(&unit_full[i], 1);
+      mbar_init(&unit_free[i], CONV);
+    }
     *err = 0;
     *abort_flag = 0;
     fence_mbar_init();
@@ -422,61 +425,11 @@ __global__ void __launch_bounds__(TcLay<HD, NQ>::THREADS, C > 1 ? 2 : 1)
     // 4 lanes take 64 bytes of a key: the 8 lanes of a store then have an
     // even and an odd row, whose swizzled chunks are on different banks
     const int row0 = ct >> 2, ch = ct & 3;
-    uint8_t* ring = smem + L::RING_OFF;
+    const uint8_t* ring = smem + L::RING_OFF;
     int n_tile = 0;                            // tiles and units of the runs before
     uint32_t n_unit = 0;
     while (walk_next(walk, P, R, &sg)) {
-      const int32_t* table = c.page_table + (int64_t)sg.seq * c.table_stride;
-      // units: K 0, K 1, V 0, K 2, V 1, ..: K runs a tile ahead of V, whose tile
-      // waits for the products before
-      const int tiles = max(0, sg.p_hi - sg.p_lo), units = 2 * tiles;
-      auto is_v = [&](int u) { return u > 0 && (u == units - 1 || (u & 1) == 0); };
-      auto tile_of = [&](int u) { return u == units - 1 ? tiles - 1 : u & 1 ? (u + 1) / 2 : max(u / 2 - 1, 0); };
-      // page ids of 32 tiles, one a lane of the first warp (which copies and
-      // fetches the scales)
-      int ids = -1, ids_at = -32;
-      auto page_of = [&](int t) {
-        if (t >= ids_at + 32 || t < ids_at) {
-          ids_at = t;
-          const int at = sg.p_lo + t + lane;
-          ids = at < sg.p_hi ? table[at] : -1;
-          if (at < sg.p_hi && (ids < 0 || ids >= c.n_pages)) {
-            ids = -1;
-            if (a.status) atomicOr(a.status, FDLLM_KV8_BAD_PAGE);
-          }
-        }
-        return __shfl_sync(0xffffffffu, ids, t - ids_at);
-      };
-      auto copy_unit = [&](int u) {   // by the first warp
-        const int page = page_of(tile_of(u)), slot = (n_unit + u) % L::RING;
-        if (lane == 0) {
-          unit_page[slot] = page;
-          if (page < 0) {
-            mbar_arrive(&unit_full[slot]);
-          } else {
-            mbar_arrive_expect_tx(&unit_full[slot], L::UNIT);
-            bulk_load(ring + slot * L::UNIT,
-                      (is_v(u) ? c.v : c.k) + (int64_t)page * c.page_stride + (int64_t)sg.g * L::UNIT,
-                      L::UNIT, &unit_full[slot]);
-          }
-        }
-        __syncwarp();
-      };
-      float ks = 0.0f, vs = 0.0f;    // scales of block ct of the next tile, as they arrive
-      bool live = false;             // whether it has keys
-      auto load_scales = [&](int t) {
-        const int page = unit_page[(n_unit + max(2 * t - 1, 0)) % L::RING];   // K's unit is on its way by now
-        live = ct < NB && page >= 0 && (sg.p_lo + t) * PAGE + ct * 16 < sg.len;
-        if (live) {
-          const int64_t so = (int64_t)page * c.scale_stride + sg.g * 4 + ct;
-          ks = c.k_scale[so];
-          vs = c.v_scale[so];
-        }
-      };
-      if (ct < 32) {
-        for (int u = 0; u < min(units, L::RING); ++u) copy_unit(u);
-        if (tiles > 0) load_scales(0);
-      }
+      const int tiles = max(0, sg.p_hi - sg.p_lo);
       auto read_unit = [&](int u, uint4* x) {
         const uint32_t n = n_unit + u;
         const int slot = n % L::RING;
@@ -487,6 +440,7 @@ __global__ void __launch_bounds__(TcLay<HD, NQ>::THREADS, C > 1 ? 2 : 1)
           x[j] = none ? make_uint4(0, 0, 0, 0)
                       : *reinterpret_cast<const uint4*>(ring + slot * L::UNIT + (j / HALVES * 32 + row0) * HD +
                                                         j % HALVES * 64 + ch * 16);
+        mbar_arrive(&unit_free[slot]);
       };
       auto put = [&](uint8_t* mat, const uint4* x) {   // 16 codes: two 16-byte chunks
 #pragma unroll
@@ -510,7 +464,7 @@ __global__ void __launch_bounds__(TcLay<HD, NQ>::THREADS, C > 1 ? 2 : 1)
       for (int j = 0; tiles > 0 && j <= tiles; ++j) {   // K of tile j, V of tile j - 1
         uint4 xk[PER], xv[PER];
         const bool has_k = j < tiles, has_v = j > 0;
-        const int u0 = u, nk = n_tile + j, nv = nk - 1;
+        const int nk = n_tile + j, nv = nk - 1;
         if (has_k) read_unit(u++, xk);
         if (has_v) read_unit(u++, xv);
         if (has_k) {
@@ -518,26 +472,6 @@ __global__ void __launch_bounds__(TcLay<HD, NQ>::THREADS, C > 1 ? 2 : 1)
           if (use > 0) wait(&k_free[st], (use - 1) & 1);
           put(smem + L::K_OFF + st * L::MAT, xk);
           mbar_arrive(&k_full[st]);
-        }
-        named_bar(CONV_BAR, CONV);   // every thread has read the units
-        if (ct < 32) {
-          for (int w = u0; w < u; ++w)
-            if (w + L::RING < units) copy_unit(w + L::RING);
-          if (has_k) {
-            // this tile's scales, then the next one's on their way
-            const int at = nk & 3;
-            if (nk >= 4) wait(&sc_free[at], (nk / 4 - 1) & 1);
-            if (ct < NB) {
-              float* sc = reinterpret_cast<float*>(smem + L::SC_OFF) + at * 3 * NB + ct;
-              const float v = fmaxf(vs, VS_MIN);
-              sc[0] = live ? ks : 0.0f;
-              sc[NB] = live ? __log2f(v) : -INFINITY;
-              sc[2 * NB] = live ? __fdividef(1.0f, v) : 0.0f;
-              mbar_arrive(&sc_full[at]);
-            }
-            __syncwarp();
-            if (j + 1 < tiles) load_scales(j + 1);
-          }
         }
         if (has_v) {
           const int st = nv % L::STAGES, use = nv / L::STAGES;
@@ -547,7 +481,82 @@ __global__ void __launch_bounds__(TcLay<HD, NQ>::THREADS, C > 1 ? 2 : 1)
         }
       }
       n_tile += tiles;
-      n_unit += units;
+      n_unit += 2 * tiles;
+    }
+  } else if (warp == 4 * NQ + CONV / 32) {
+    // ================================================== copies
+    uint8_t* ring = smem + L::RING_OFF;
+    int n_tile = 0;
+    uint32_t n_unit = 0;
+    // scales of block `lane` of the last tile asked for, on their way
+    float ks = 0.0f, vs = 0.0f;
+    bool live = false;
+    auto store_scales = [&](int n) {
+      const int at = n & 3;
+      if (n >= 4) wait(&sc_free[at], (n / 4 - 1) & 1);
+      if (lane < NB) {
+        float* sc = reinterpret_cast<float*>(smem + L::SC_OFF) + at * 3 * NB + lane;
+        const float v = fmaxf(vs, VS_MIN);
+        sc[0] = live ? ks : 0.0f;
+        sc[NB] = live ? __log2f(v) : -INFINITY;
+        sc[2 * NB] = live ? __fdividef(1.0f, v) : 0.0f;
+        mbar_arrive(&sc_full[at]);
+      }
+      __syncwarp();
+    };
+    while (walk_next(walk, P, R, &sg)) {
+      const int32_t* table = c.page_table + (int64_t)sg.seq * c.table_stride;
+      // units: K 0, K 1, V 0, K 2, V 1, ..: K runs a tile ahead of V, whose tile
+      // waits for the products before
+      const int tiles = max(0, sg.p_hi - sg.p_lo), units = 2 * tiles;
+      int ids = -1, ids_at = 0, before = -1;   // page ids of 32 tiles from ids_at on, one a lane
+      for (int u = 0; u < units; ++u, ++n_unit) {
+        const bool is_v = u > 0 && (u == units - 1 || (u & 1) == 0);
+        const int t = u == units - 1 ? tiles - 1 : u & 1 ? (u + 1) / 2 : max(u / 2 - 1, 0);
+        int page = before;                     // V's page is that of the K unit before the last
+        if (!is_v) {
+          if (t == 0 || t >= ids_at + 32) {
+            before = __shfl_sync(0xffffffffu, ids, 31);
+            ids_at = t;
+            const int at = sg.p_lo + t + lane;
+            ids = at < sg.p_hi ? table[at] : -1;
+            if (at < sg.p_hi && (ids < 0 || ids >= c.n_pages)) {
+              ids = -1;
+              if (a.status) atomicOr(a.status, FDLLM_KV8_BAD_PAGE);
+            }
+          } else {
+            before = __shfl_sync(0xffffffffu, ids, t - ids_at - 1);
+          }
+          page = __shfl_sync(0xffffffffu, ids, t - ids_at);
+        } else if (u == units - 1) {
+          page = __shfl_sync(0xffffffffu, ids, t - ids_at);
+        }
+        const int slot = n_unit % L::RING;
+        if (n_unit >= L::RING) wait(&unit_free[slot], (n_unit / L::RING - 1) & 1);
+        if (ok && lane == 0) {
+          unit_page[slot] = page;
+          if (page < 0) {
+            mbar_arrive(&unit_full[slot]);
+          } else {
+            mbar_arrive_expect_tx(&unit_full[slot], L::UNIT);
+            bulk_load(ring + slot * L::UNIT,
+                      (is_v ? c.v : c.k) + (int64_t)page * c.page_stride + (int64_t)sg.g * L::UNIT,
+                      L::UNIT, &unit_full[slot]);
+          }
+        }
+        __syncwarp();
+        if (!is_v) {   // the scales of the tile before have arrived by now
+          if (t > 0) store_scales(n_tile + t - 1);
+          live = lane < NB && page >= 0 && (sg.p_lo + t) * PAGE + lane * 16 < sg.len;
+          if (live) {
+            const int64_t so = (int64_t)page * c.scale_stride + sg.g * 4 + lane;
+            ks = c.k_scale[so];
+            vs = c.v_scale[so];
+          }
+        }
+      }
+      if (tiles > 0) store_scales(n_tile + tiles - 1);
+      n_tile += tiles;
     }
   } else {
     // ================================================== MMA
