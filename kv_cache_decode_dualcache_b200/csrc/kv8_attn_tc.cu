@@ -11,7 +11,8 @@
 // costs nothing: with so few rows the kernel waits for the cache.
 //
 // Roles: 4 warps a row tile for the softmax (a thread per MMA row: q, weights,
-// output), 4 converter warps, one MMA warp, one copy warp.  A page is a tile:
+// output), 4 converter warps, one copy warp, an MMA warp
+// a row tile.  A page is a tile:
 // its codes of K (and V) of a head are contiguous and come by one bulk copy
 // each into a ring of int8 units; the converters turn them into
 // 128-byte-swizzled fp16 tiles, and the copy warp fetches the blocks' scales.
@@ -65,7 +66,7 @@ struct TcLay {
   static constexpr int BAR_OFF = RF_OFF + NQ * 128 * 4;
   static constexpr int MISC_OFF = BAR_OFF + (31 + 2 * RING) * 8;
   static constexpr int PAGE_OFF = MISC_OFF + 16;           // the units' pages
-  static constexpr int THREADS = 128 * NQ + CONV + 64;
+  static constexpr int THREADS = 128 * NQ + CONV + 32 + 32 * NQ;
   static constexpr int WALK_OFF = (PAGE_OFF + RING * 4 + 15) / 16 * 16;
   static constexpr int SMEM = WALK_OFF + THREADS / 32 * (int)sizeof(Walk) + 1024;   // slack for
                                                                                     // 1024-byte alignment
@@ -184,9 +185,9 @@ __global__ void __launch_bounds__(TcLay<HD, NQ>::THREADS, C > 1 ? 2 : 1)
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&k_full[i], CONV);
-      mbar_init(&k_free[i], 1);
+      mbar_init(&k_free[i], NQ);
       mbar_init(&v_full[i], CONV);
-      mbar_init(&v_free[i], 1);
+      mbar_init(&v_free[i], NQ);
       mbar_init(&s_full[i], 1);
       mbar_init(&s_full[2 + i], 1);
       mbar_init(&pv_done[i], 1);
@@ -559,9 +560,10 @@ __global__ void __launch_bounds__(TcLay<HD, NQ>::THREADS, C > 1 ? 2 : 1)
       n_tile += tiles;
     }
   } else {
-    // ================================================== MMA
+    // ================================================== MMA, a warp a row tile
+    const int q = warp - (4 * NQ + CONV / 32 + 1);
     const uint32_t kb = smem_u32(smem + L::K_OFF), vb = smem_u32(smem + L::V_OFF);
-    const uint32_t qb = smem_u32(smem + L::Q_OFF);
+    const uint64_t qd = smem_desc_sw128(smem_u32(smem + L::Q_OFF) + q * L::KH * L::Q_SUB);
     int n_tile = 0, n_seg = 0;
     while (walk_next(walk, P, R, &sg)) {
       const int tiles = max(0, sg.p_hi - sg.p_lo);
@@ -576,14 +578,10 @@ __global__ void __launch_bounds__(TcLay<HD, NQ>::THREADS, C > 1 ? 2 : 1)
             // a step along K moves the descriptors' start address (in 16 bytes)
             const uint64_t kd = smem_desc_sw128(kb + st * L::MAT);
 #pragma unroll
-            for (int q = 0; q < NQ; ++q) {
-              const uint64_t qd = smem_desc_sw128(qb + q * L::KH * L::Q_SUB);
-#pragma unroll
-              for (int k = 0; k < HD / 16; ++k)
-                tc_mma(tmem + q * 128 + (n & 1) * 64, qd + (((k >> 2) * L::Q_SUB + (k & 3) * 32) >> 4),
-                       kd + (((k >> 2) * L::SUB + (k & 3) * 32) >> 4), idesc_f32acc(KEYS, true), k > 0);
-              tc_commit(&s_full[2 * q + (n & 1)]);
-            }
+            for (int k = 0; k < HD / 16; ++k)
+              tc_mma(tmem + q * 128 + (n & 1) * 64, qd + (((k >> 2) * L::Q_SUB + (k & 3) * 32) >> 4),
+                     kd + (((k >> 2) * L::SUB + (k & 3) * 32) >> 4), idesc_f32acc(KEYS, true), k > 0);
+            tc_commit(&s_full[2 * q + (n & 1)]);
             tc_commit(&k_free[st]);
           }
           __syncwarp();
@@ -591,21 +589,18 @@ __global__ void __launch_bounds__(TcLay<HD, NQ>::THREADS, C > 1 ? 2 : 1)
         if (t > 0) {
           const int n = n_tile + t - 1, st = n % L::STAGES;
           wait(&v_full[st], (n / L::STAGES) & 1);
-          const uint64_t vd = smem_desc_sw128_mn(vb + st * L::MAT, L::SUB, 1024);
+          wait(&p_full[2 * q + (n & 1)], (n >> 1) & 1);
+          if (ok && lane == 0) {
+            tc_fence_after();
+            const uint64_t vd = smem_desc_sw128_mn(vb + st * L::MAT, L::SUB, 1024);
 #pragma unroll
-          for (int q = 0; q < NQ; ++q) {
-            wait(&p_full[2 * q + (n & 1)], (n >> 1) & 1);
-            if (ok && lane == 0) {
-              tc_fence_after();
-#pragma unroll
-              for (int k = 0; k < KEYS / 16; ++k)
-                tc_mma_ts(tmem + NQ * 128 + q * 128, tmem + q * 128 + (n & 1) * 64 + k * 8,
-                          vd + (k * 2048 >> 4), idesc_f32acc_bmn(HD, true), t > 1 || k > 0);
-              tc_commit(&pv_done[2 * q + (n & 1)]);
-              if (q == NQ - 1) tc_commit(&v_free[st]);
-            }
-            __syncwarp();
+            for (int k = 0; k < KEYS / 16; ++k)
+              tc_mma_ts(tmem + NQ * 128 + q * 128, tmem + q * 128 + (n & 1) * 64 + k * 8,
+                        vd + (k * 2048 >> 4), idesc_f32acc_bmn(HD, true), t > 1 || k > 0);
+            tc_commit(&pv_done[2 * q + (n & 1)]);
+            tc_commit(&v_free[st]);
           }
+          __syncwarp();
         }
       }
       n_tile += tiles;
