@@ -11,8 +11,8 @@
 // costs nothing: with so few rows the kernel waits for the cache.
 //
 // Roles: 4 warps a row tile for the softmax (a thread per MMA row: q, weights,
-// output), 4 converter warps, one copy warp, an MMA warp
-// a row tile.  A page is a tile:
+// output), 2 converter warps for K and 2 for V, one copy warp, an MMA warp a
+// row tile.  A page is a tile:
 // its codes of K (and V) of a head are contiguous and come by one bulk copy
 // each into a ring of int8 units; the converters turn them into
 // 128-byte-swizzled fp16 tiles, and the copy warp fetches the blocks' scales.
@@ -41,7 +41,7 @@ using namespace kv8;
 
 constexpr int KEYS = PAGE;           // keys of a tile
 constexpr int NB = KEYS / FDLLM_KV8_BLOCK;
-constexpr int CONV = 128;            // converter threads
+constexpr int CONV = 64;             // converter threads of K, and of V
 
 template <int HD, int NQ>
 struct TcLay {
@@ -49,7 +49,8 @@ struct TcLay {
   static constexpr int SUB = KEYS * 128;              // [64 keys][64 dims] fp16
   static constexpr int MAT = KH * SUB;                // fp16 K or V of a tile
   static constexpr int UNIT = KEYS * HD;              // int8 K or V of a tile
-  static constexpr int RING = NQ == 1 ? 4 : 8;        // units
+  static constexpr int DEPTH = NQ == 1 ? 2 : 4;       // tiles in the ring, K and V a unit each
+  static constexpr int RING = 2 * DEPTH;
   static constexpr int STAGES = NQ;                   // fp16 tiles of K, and of V
   static constexpr int Q_SUB = 128 * 128;             // [128 rows][64 dims] fp16
   static constexpr int K_OFF = 0;
@@ -66,7 +67,7 @@ struct TcLay {
   static constexpr int BAR_OFF = RF_OFF + NQ * 128 * 4;
   static constexpr int MISC_OFF = BAR_OFF + (31 + 2 * RING) * 8;
   static constexpr int PAGE_OFF = MISC_OFF + 16;           // the units' pages
-  static constexpr int THREADS = 128 * NQ + CONV + 32 + 32 * NQ;
+  static constexpr int THREADS = 128 * NQ + 2 * CONV + 32 + 32 * NQ;
   static constexpr int WALK_OFF = (PAGE_OFF + RING * 4 + 15) / 16 * 16;
   static constexpr int SMEM = WALK_OFF + THREADS / 32 * (int)sizeof(Walk) + 1024;   // slack for
                                                                                     // 1024-byte alignment
@@ -418,35 +419,24 @@ __global__ void __launch_bounds__(TcLay<HD, NQ>::THREADS, C > 1 ? 2 : 1)
       }
       tc_fence_before();   // O has been read before the next run's first product
     }
-  } else if (warp < 4 * NQ + CONV / 32) {
+  } else if (warp < 4 * NQ + 2 * CONV / 32) {
     // ================================================== converters
-    const int ct = tid - 128 * NQ;
-    constexpr int HALVES = HD / 64;            // 64-byte halves of a key
-    constexpr int PER = KEYS / 32 * HALVES;    // 16-byte chunks of a thread and unit
+    const int is_v = tid >= 128 * NQ + CONV, ct = tid - 128 * NQ - (is_v ? CONV : 0);
+    constexpr int HALVES = HD / 64;                // 64-byte halves of a key
+    constexpr int ROWS = CONV / 4;
+    constexpr int PER = KEYS / ROWS * HALVES;      // 16-byte chunks of a thread and unit
     // 4 lanes take 64 bytes of a key: the 8 lanes of a store then have an
     // even and an odd row, whose swizzled chunks are on different banks
     const int row0 = ct >> 2, ch = ct & 3;
     const uint8_t* ring = smem + L::RING_OFF;
-    int n_tile = 0;                            // tiles and units of the runs before
-    uint32_t n_unit = 0;
+    uint64_t *full = is_v ? v_full : k_full, *free = is_v ? v_free : k_free;
+    int n_tile = 0;                                // tiles of the runs before
     while (walk_next(walk, P, R, &sg)) {
-      const int tiles = max(0, sg.p_hi - sg.p_lo);
-      auto read_unit = [&](int u, uint4* x) {
-        const uint32_t n = n_unit + u;
-        const int slot = n % L::RING;
-        wait(&unit_full[slot], (n / L::RING) & 1);
-        const bool none = unit_page[slot] < 0;
-#pragma unroll
-        for (int j = 0; j < PER; ++j)
-          x[j] = none ? make_uint4(0, 0, 0, 0)
-                      : *reinterpret_cast<const uint4*>(ring + slot * L::UNIT + (j / HALVES * 32 + row0) * HD +
-                                                        j % HALVES * 64 + ch * 16);
-        mbar_arrive(&unit_free[slot]);
-      };
+      const int end = n_tile + max(0, sg.p_hi - sg.p_lo);
       auto put = [&](uint8_t* mat, const uint4* x) {   // 16 codes: two 16-byte chunks
 #pragma unroll
         for (int j = 0; j < PER; ++j) {
-          const int row = j / HALVES * 32 + row0;
+          const int row = j / HALVES * ROWS + row0;
           const uint32_t y[4] = {x[j].x ^ 0x80808080u, x[j].y ^ 0x80808080u, x[j].z ^ 0x80808080u,
                                  x[j].w ^ 0x80808080u};
           uint32_t h[8];
@@ -461,34 +451,27 @@ __global__ void __launch_bounds__(TcLay<HD, NQ>::THREADS, C > 1 ? 2 : 1)
         }
         fence_proxy_async_smem();
       };
-      int u = 0;
-      for (int j = 0; tiles > 0 && j <= tiles; ++j) {   // K of tile j, V of tile j - 1
-        uint4 xk[PER], xv[PER];
-        const bool has_k = j < tiles, has_v = j > 0;
-        const int nk = n_tile + j, nv = nk - 1;
-        if (has_k) read_unit(u++, xk);
-        if (has_v) read_unit(u++, xv);
-        if (has_k) {
-          const int st = nk % L::STAGES, use = nk / L::STAGES;
-          if (use > 0) wait(&k_free[st], (use - 1) & 1);
-          put(smem + L::K_OFF + st * L::MAT, xk);
-          mbar_arrive(&k_full[st]);
-        }
-        if (has_v) {
-          const int st = nv % L::STAGES, use = nv / L::STAGES;
-          if (use > 0) wait(&v_free[st], (use - 1) & 1);
-          put(smem + L::V_OFF + st * L::MAT, xv);
-          mbar_arrive(&v_full[st]);
-        }
+      for (; n_tile < end; ++n_tile) {
+        const int st = n_tile % L::STAGES, use = n_tile / L::STAGES;
+        const int slot = n_tile % L::DEPTH * 2 + is_v;
+        wait(&unit_full[slot], (n_tile / L::DEPTH) & 1);
+        const bool none = unit_page[slot] < 0;
+        uint4 x[PER];
+#pragma unroll
+        for (int j = 0; j < PER; ++j)
+          x[j] = none ? make_uint4(0, 0, 0, 0)
+                      : *reinterpret_cast<const uint4*>(ring + slot * L::UNIT + (j / HALVES * ROWS + row0) * HD +
+                                                        j % HALVES * 64 + ch * 16);
+        mbar_arrive(&unit_free[slot]);
+        if (use > 0) wait(&free[st], (use - 1) & 1);
+        put(smem + (is_v ? L::V_OFF : L::K_OFF) + st * L::MAT, x);
+        mbar_arrive(&full[st]);
       }
-      n_tile += tiles;
-      n_unit += 2 * tiles;
     }
-  } else if (warp == 4 * NQ + CONV / 32) {
+  } else if (warp == 4 * NQ + 2 * CONV / 32) {
     // ================================================== copies
     uint8_t* ring = smem + L::RING_OFF;
     int n_tile = 0;
-    uint32_t n_unit = 0;
     // scales of block `lane` of the last tile asked for, on their way
     float ks = 0.0f, vs = 0.0f;
     bool live = false;
@@ -507,53 +490,42 @@ __global__ void __launch_bounds__(TcLay<HD, NQ>::THREADS, C > 1 ? 2 : 1)
     };
     while (walk_next(walk, P, R, &sg)) {
       const int32_t* table = c.page_table + (int64_t)sg.seq * c.table_stride;
-      // units: K 0, K 1, V 0, K 2, V 1, ..: K runs a tile ahead of V, whose tile
-      // waits for the products before
-      const int tiles = max(0, sg.p_hi - sg.p_lo), units = 2 * tiles;
-      int ids = -1, ids_at = 0, before = -1;   // page ids of 32 tiles from ids_at on, one a lane
-      for (int u = 0; u < units; ++u, ++n_unit) {
-        const bool is_v = u > 0 && (u == units - 1 || (u & 1) == 0);
-        const int t = u == units - 1 ? tiles - 1 : u & 1 ? (u + 1) / 2 : max(u / 2 - 1, 0);
-        int page = before;                     // V's page is that of the K unit before the last
-        if (!is_v) {
-          if (t == 0 || t >= ids_at + 32) {
-            before = __shfl_sync(0xffffffffu, ids, 31);
-            ids_at = t;
-            const int at = sg.p_lo + t + lane;
-            ids = at < sg.p_hi ? table[at] : -1;
-            if (at < sg.p_hi && (ids < 0 || ids >= c.n_pages)) {
-              ids = -1;
-              if (a.status) atomicOr(a.status, FDLLM_KV8_BAD_PAGE);
+      const int tiles = max(0, sg.p_hi - sg.p_lo);
+      int ids = -1;                            // page ids of 32 tiles, one a lane
+      for (int t = 0; t < tiles; ++t) {
+        if ((t & 31) == 0) {
+          const int at = sg.p_lo + t + lane;
+          ids = at < sg.p_hi ? table[at] : -1;
+          if (at < sg.p_hi && (ids < 0 || ids >= c.n_pages)) {
+            ids = -1;
+            if (a.status) atomicOr(a.status, FDLLM_KV8_BAD_PAGE);
+          }
+        }
+        const int page = __shfl_sync(0xffffffffu, ids, t & 31), n = n_tile + t;
+#pragma unroll
+        for (int is_v = 0; is_v < 2; ++is_v) {
+          const int slot = n % L::DEPTH * 2 + is_v;
+          if (n >= L::DEPTH) wait(&unit_free[slot], (n / L::DEPTH - 1) & 1);
+          if (ok && lane == 0) {
+            unit_page[slot] = page;
+            if (page < 0) {
+              mbar_arrive(&unit_full[slot]);
+            } else {
+              mbar_arrive_expect_tx(&unit_full[slot], L::UNIT);
+              bulk_load(ring + slot * L::UNIT,
+                        (is_v ? c.v : c.k) + (int64_t)page * c.page_stride + (int64_t)sg.g * L::UNIT,
+                        L::UNIT, &unit_full[slot]);
             }
-          } else {
-            before = __shfl_sync(0xffffffffu, ids, t - ids_at - 1);
           }
-          page = __shfl_sync(0xffffffffu, ids, t - ids_at);
-        } else if (u == units - 1) {
-          page = __shfl_sync(0xffffffffu, ids, t - ids_at);
+          __syncwarp();
         }
-        const int slot = n_unit % L::RING;
-        if (n_unit >= L::RING) wait(&unit_free[slot], (n_unit / L::RING - 1) & 1);
-        if (ok && lane == 0) {
-          unit_page[slot] = page;
-          if (page < 0) {
-            mbar_arrive(&unit_full[slot]);
-          } else {
-            mbar_arrive_expect_tx(&unit_full[slot], L::UNIT);
-            bulk_load(ring + slot * L::UNIT,
-                      (is_v ? c.v : c.k) + (int64_t)page * c.page_stride + (int64_t)sg.g * L::UNIT,
-                      L::UNIT, &unit_full[slot]);
-          }
-        }
-        __syncwarp();
-        if (!is_v) {   // the scales of the tile before have arrived by now
-          if (t > 0) store_scales(n_tile + t - 1);
-          live = lane < NB && page >= 0 && (sg.p_lo + t) * PAGE + lane * 16 < sg.len;
-          if (live) {
-            const int64_t so = (int64_t)page * c.scale_stride + sg.g * 4 + lane;
-            ks = c.k_scale[so];
-            vs = c.v_scale[so];
-          }
+        // the scales of the tile before have arrived by now
+        if (t > 0) store_scales(n - 1);
+        live = lane < NB && page >= 0 && (sg.p_lo + t) * PAGE + lane * 16 < sg.len;
+        if (live) {
+          const int64_t so = (int64_t)page * c.scale_stride + sg.g * 4 + lane;
+          ks = c.k_scale[so];
+          vs = c.v_scale[so];
         }
       }
       if (tiles > 0) store_scales(n_tile + tiles - 1);
@@ -561,7 +533,7 @@ __global__ void __launch_bounds__(TcLay<HD, NQ>::THREADS, C > 1 ? 2 : 1)
     }
   } else {
     // ================================================== MMA, a warp a row tile
-    const int q = warp - (4 * NQ + CONV / 32 + 1);
+    const int q = warp - (4 * NQ + 2 * CONV / 32 + 1);
     const uint32_t kb = smem_u32(smem + L::K_OFF), vb = smem_u32(smem + L::V_OFF);
     const uint64_t qd = smem_desc_sw128(smem_u32(smem + L::Q_OFF) + q * L::KH * L::Q_SUB);
     int n_tile = 0, n_seg = 0;
