@@ -76,6 +76,29 @@ FD_DEV float finite_abs(float x) {
 // to 0).
 FD_DEV int to_code(float y) { return max(-127, min(127, __float2int_rn(y))); }
 
+// max(a, |b|), NaN if either is.
+FD_DEV float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(fabsf(b)));
+  return y;
+}
+
+// Codes of 8 finite values that the scale covers (|x inv| < 127.5): added to
+// 1.5 2^23, a value is rounded to an integer (halves to even), whose low byte
+// is the code.  deq: the codes as floats.
+FD_DEV uint2 codes8(const float* x, float inv, float* deq) {
+  constexpr float MAGIC = 12582912.0f;
+  uint32_t m[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float y = __fadd_rn(__fmul_rn(x[i], inv), MAGIC);
+    deq[i] = __fsub_rn(y, MAGIC);
+    m[i] = __float_as_uint(y);
+  }
+  return make_uint2(__byte_perm(__byte_perm(m[0], m[1], 0x0040), __byte_perm(m[2], m[3], 0x0040), 0x5410),
+                    __byte_perm(__byte_perm(m[4], m[5], 0x0040), __byte_perm(m[6], m[7], 0x0040), 0x5410));
+}
+
 FD_DEV uint2 pack8(const int* q) {
   uint2 r;
   r.x = (q[0] & 255) | ((q[1] & 255) << 8) | ((q[2] & 255) << 16) | ((uint32_t)q[3] << 24);
@@ -144,7 +167,7 @@ __global__ void __launch_bounds__(APP_WARPS * 32) kv8_append_kernel(const Append
   for (int b = b_lo + blockIdx.y; b <= b_hi; b += gridDim.y) {
     const int base = b * BLK;
     float x[NP][16];   // dims d0 .. d0 + 7, then their partners
-    float top = 0.0f;
+    const int page = is_q ? 0 : c.page_table[(int64_t)seq * c.table_stride + base / FDLLM_KV8_PAGE];
 #pragma unroll
     for (int p = 0; p < NP; ++p) {
       const int at = base + p * TPP + tk;
@@ -189,7 +212,6 @@ __global__ void __launch_bounds__(APP_WARPS * 32) kv8_append_kernel(const Append
       }
       continue;
     }
-    const int page = c.page_table[(int64_t)seq * c.table_stride + base / FDLLM_KV8_PAGE];
     if (page < 0 || page >= c.n_pages) {
       if (lane == 0 && a.status) atomicOr(a.status, FDLLM_KV8_BAD_PAGE);
       continue;
@@ -201,10 +223,19 @@ __global__ void __launch_bounds__(APP_WARPS * 32) kv8_append_kernel(const Append
     // old tokens of the block that stay: before w0, or behind the new rows
     const bool any_kept = base < min(len, w0) || w1 < min(len, base + BLK);
     const float old = any_kept ? *sp : 0.0f;
+    float top = 0.0f;
 #pragma unroll
     for (int p = 0; p < NP; ++p)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) top = fmaxf(top, finite_abs(x[p][i]));
+      for (int i = 0; i < 16; ++i) top = max_nan(top, x[p][i]);
+    const bool finite = __all_sync(0xffffffffu, top <= 3.402823466e38f);
+    if (!finite) {
+      top = 0.0f;
+#pragma unroll
+      for (int p = 0; p < NP; ++p)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) top = fmaxf(top, finite_abs(x[p][i]));
+    }
     top = warp_max(top);
     float scale = fmaxf(old, __fmul_rn(top, 1.0f / 127.0f));
     if (!(scale >= TINY_SCALE)) scale = 0.0f;
@@ -219,15 +250,17 @@ __global__ void __launch_bounds__(APP_WARPS * 32) kv8_append_kernel(const Append
       uint2* lo = reinterpret_cast<uint2*>(codes + slot * HD);
       uint2* hi = reinterpret_cast<uint2*>(codes + slot * HD + H2);
       if (at >= w0 && at < w1) {
-        int q[16];
+        float y[16];
+        if (!finite) {   // infinities end at +-127, NaN at 0
 #pragma unroll
-        for (int i = 0; i < 16; ++i) q[i] = to_code(__fmul_rn(x[p][i], inv));
-        *lo = pack8(q);
-        *hi = pack8(q + 8);
+          for (int i = 0; i < 16; ++i) x[p][i] = (float)to_code(__fmul_rn(x[p][i], inv));
+        }
+        const float by = finite ? inv : 1.0f;
+        *lo = codes8(x[p], by, y);
+        *hi = codes8(x[p] + 8, by, y + 8);
         if (out) {
-          float y[16];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) y[i] = __fmul_rn((float)q[i], scale);
+          for (int i = 0; i < 16; ++i) y[i] = __fmul_rn(y[i], scale);
           T* o = out + ((int64_t)(r_lo + at - w0) * out_heads + g) * HD + d0;
           store8<T>(o, y);
           store8<T>(o + H2, y + 8);
