@@ -1,16 +1,20 @@
 // fdllm_kv8_append: rotation, 8-bit rounding and storing of new keys and
 // values into the paged cache, one launch.
 //
-// One warp takes one block of 16 positions of one head: K (rotated, rounded,
+// A warp takes one block of 16 positions of a head: K (rotated, rounded,
 // stored), V (rounded, stored) or q (rotated, written back in its type).  A
 // lane holds 8 dims and their 8 rotation partners (d + head_dim / 2) of
 // head_dim / 32 tokens in registers, so a block is read once, its maximum is
-// one warp reduction and its codes leave in 8-byte stores; nothing passes
-// through shared memory.
+// one warp reduction and its codes leave in 8-byte stores.  The (cos, sin) rows
+// lie in shared memory for all heads of the CTA, and a warp with several heads
+// loads the next one's rows while it works on one.
 //
 // Bound: the bytes of the rows (read), the codes and the optional outputs
-// (written); the (cos, sin) rows are shared by the heads of a token and come
-// from L1/L2.
+// (written).  A prompt of 8191 tokens with 32 K/V heads and 32 heads of q of 128
+// dims (474 MB, bf16): 85 us, 5.6 TB/s; 101 us with a head a warp (all of a warp's
+// loads then wait at once), 141 us with the (cos, sin) rows read through L1 by
+// every warp.  With few blocks a warp has one head: 16 blocks of 32 tokens take
+// 8.7 us so and 11.4 us with 4 heads a warp, for their loads then wait in turn.
 #include <algorithm>
 
 #include "common.cuh"
@@ -27,20 +31,31 @@ constexpr float TINY_SCALE = 7.888609052210118e-31f;  // 2^-100
 struct AppendP {
   fdllm_kv8 c;
   fdllm_kv8_append_args a;
+  int per_warp;   // heads of a warp
 };
 
-// 8 consecutive elements as float (16-byte aligned; plain loads, q_out may
-// be q itself).
-template <typename T> FD_DEV void load8(const T* p, float* x);
-template <> FD_DEV void load8<float>(const float* p, float* x) {
-  const float4 a = *reinterpret_cast<const float4*>(p);
-  const float4 b = *reinterpret_cast<const float4*>(p + 4);
-  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+// 8 consecutive elements as they lie in memory (16-byte aligned; plain loads,
+// q_out may be q itself), and as float.
+template <typename T> struct Raw8 {
+  uint4 u[sizeof(T) / 2];
+};
+template <typename T> FD_DEV Raw8<T> load8(const T* p) {
+  Raw8<T> r;
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.u[i] = reinterpret_cast<const uint4*>(p)[i];
+  return r;
 }
-template <> FD_DEV void load8<__half>(const __half* p, float* x) {
-  const uint4 u = *reinterpret_cast<const uint4*>(p);
-  const __half2* h = reinterpret_cast<const __half2*>(&u);
+FD_DEV void floats8(const Raw8<float>& r, float* x) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    x[4 * i] = __uint_as_float(r.u[i].x);
+    x[4 * i + 1] = __uint_as_float(r.u[i].y);
+    x[4 * i + 2] = __uint_as_float(r.u[i].z);
+    x[4 * i + 3] = __uint_as_float(r.u[i].w);
+  }
+}
+FD_DEV void floats8(const Raw8<__half>& r, float* x) {
+  const __half2* h = reinterpret_cast<const __half2*>(&r.u[0]);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 f = __half22float2(h[i]);
@@ -48,9 +63,8 @@ template <> FD_DEV void load8<__half>(const __half* p, float* x) {
     x[2 * i + 1] = f.y;
   }
 }
-template <> FD_DEV void load8<__nv_bfloat16>(const __nv_bfloat16* p, float* x) {
-  const uint4 u = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+FD_DEV void floats8(const Raw8<__nv_bfloat16>& r, float* x) {
+  const uint32_t w[4] = {r.u[0].x, r.u[0].y, r.u[0].z, r.u[0].w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     x[2 * i] = __uint_as_float(w[i] << 16);
@@ -118,17 +132,20 @@ FD_DEV uint2 rescale8(uint2 w, float ratio) {
 }
 
 template <typename T, int HD>
-__global__ void __launch_bounds__(APP_WARPS * 32) kv8_append_kernel(const AppendP P) {
+__global__ void __launch_bounds__(APP_WARPS * 32, 2) kv8_append_kernel(const AppendP P) {
   constexpr int LPT = HD / 16;      // lanes per token
   constexpr int TPP = 32 / LPT;     // tokens per pass
   constexpr int NP = BLK / TPP;     // passes over the block
   constexpr int H2 = HD / 2;
+  constexpr bool AHEAD = sizeof(T) * HD <= 256;   // a head ahead, where registers allow it
   const fdllm_kv8& c = P.c;
   const fdllm_kv8_append_args& a = P.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int seq = blockIdx.z;
-  const int head = blockIdx.x * APP_WARPS + warp;   // K heads, V heads, q heads
-  const int Hkv = c.n_kv_heads;
+  const int Hkv = c.n_kv_heads, heads = 2 * Hkv + (a.q ? a.n_heads : 0);
+  // the CTA's heads, of K, V, q in a row; a warp takes every APP_WARPS-th
+  const int h_lo = blockIdx.x * APP_WARPS * P.per_warp, h_hi = min(h_lo + APP_WARPS * P.per_warp, heads);
+  __shared__ float4 rope_s[BLK][H2 / 2];   // the block's (cos, sin) rows, a lane's four chunks apart
 
   const int r_lo = min(max(a.starts[seq], 0), a.n_tokens);
   const int r_hi = min(max(a.starts[seq + 1], r_lo), a.n_tokens);
@@ -149,125 +166,146 @@ __global__ void __launch_bounds__(APP_WARPS * 32) kv8_append_kernel(const Append
     if (bad && a.status) atomicOr(a.status, bad);
     if (a.lens_out) a.lens_out[seq] = n > 0 ? max(len, w1) : len;
   }
-  if (n == 0 || head >= 2 * Hkv + (a.q ? a.n_heads : 0)) return;
+  if (n == 0) return;
 
-  const bool is_q = head >= 2 * Hkv, is_v = !is_q && head >= Hkv;
-  const int g = is_q ? head - 2 * Hkv : is_v ? head - Hkv : head;
-  const T* src = reinterpret_cast<const T*>(is_q ? a.q : is_v ? a.v : a.k);
-  const int64_t* st = is_q ? a.q_strides : is_v ? a.v_strides : a.k_strides;
-  src += (int64_t)g * st[1];
-  const int64_t row_stride = st[0];
-  T* out = reinterpret_cast<T*>(is_q ? a.q_out : is_v ? a.v_out : a.k_out);
-  const int out_heads = is_q ? a.n_heads : Hkv;
-  const bool rotate = a.rope != nullptr && !is_v;
   const int sub = lane % LPT, tk = lane / LPT;
   const int d0 = 8 * sub;
 
+  const bool any_rope = a.rope != nullptr && (h_lo < Hkv || h_hi > 2 * Hkv);
   const int b_lo = w0 / BLK, b_hi = (w1 - 1) / BLK;
   for (int b = b_lo + blockIdx.y; b <= b_hi; b += gridDim.y) {
     const int base = b * BLK;
-    float x[NP][16];   // dims d0 .. d0 + 7, then their partners
-    const int page = is_q ? 0 : c.page_table[(int64_t)seq * c.table_stride + base / FDLLM_KV8_PAGE];
-#pragma unroll
-    for (int p = 0; p < NP; ++p) {
-      const int at = base + p * TPP + tk;
-      if (at >= w0 && at < w1) {
-        const T* row = src + (int64_t)(r_lo + at - w0) * row_stride + d0;
-        load8<T>(row, x[p]);
-        load8<T>(row + H2, x[p] + 8);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) x[p][i] = 0.0f;
-      }
-    }
-    if (rotate) {
+    Raw8<T> raw[NP][2];   // dims d0 .. d0 + 7, then their partners
+    auto load = [&](int head) {
+      const bool is_q = head >= 2 * Hkv, is_v = !is_q && head >= Hkv;
+      const T* src = reinterpret_cast<const T*>(is_q ? a.q : is_v ? a.v : a.k);
+      const int64_t* st = is_q ? a.q_strides : is_v ? a.v_strides : a.k_strides;
+      src += (int64_t)(is_q ? head - 2 * Hkv : is_v ? head - Hkv : head) * st[1] + d0;
 #pragma unroll
       for (int p = 0; p < NP; ++p) {
         const int at = base + p * TPP + tk;
-        if (at >= w0 && at < w1) {
-          const float4* cs = reinterpret_cast<const float4*>(a.rope + ((int64_t)at * H2 + d0) * 2);
+        if (at >= w0 && at < w1 && head < h_hi) {
+          const T* row = src + (int64_t)(r_lo + at - w0) * st[0];
+          raw[p][0] = load8<T>(row);
+          raw[p][1] = load8<T>(row + H2);
+        } else {
+          raw[p][0] = raw[p][1] = Raw8<T>{};
+        }
+      }
+    };
+    if (AHEAD) load(h_lo + warp);
+    const int page = h_lo >= 2 * Hkv ? 0 : c.page_table[(int64_t)seq * c.table_stride + base / FDLLM_KV8_PAGE];
+    if (any_rope) {
+      const float4* src = reinterpret_cast<const float4*>(a.rope + (int64_t)base * HD);
+      __syncthreads();   // the rows of the block before have been used
+      for (int i = threadIdx.x; i < BLK * H2 / 2; i += APP_WARPS * 32) {
+        const int t = i / (H2 / 2), ch = i % (H2 / 2);
+        if (base + t >= w0 && base + t < w1) rope_s[t][ch % 4 * LPT + ch / 4] = __ldg(src + i);
+      }
+      __syncthreads();
+    }
+#pragma unroll 1
+    for (int head = h_lo + warp; head < h_hi; head += APP_WARPS) {
+      const bool is_q = head >= 2 * Hkv, is_v = !is_q && head >= Hkv;
+      const int g = is_q ? head - 2 * Hkv : is_v ? head - Hkv : head;
+      T* out = reinterpret_cast<T*>(is_q ? a.q_out : is_v ? a.v_out : a.k_out);
+      const int out_heads = is_q ? a.n_heads : Hkv;
+      float x[NP][16];
+      if (!AHEAD) load(head);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float4 w = __ldg(cs + i);
-            const float cw[2] = {w.x, w.z}, sw[2] = {w.y, w.w};
+      for (int p = 0; p < NP; ++p) {
+        floats8(raw[p][0], x[p]);
+        floats8(raw[p][1], x[p] + 8);
+      }
+      if (AHEAD) load(head + APP_WARPS);   // on its way while this head is worked on
+      if (a.rope != nullptr && !is_v) {
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const float lo = x[p][2 * i + j], hi = x[p][8 + 2 * i + j];
-              x[p][2 * i + j] = __fsub_rn(__fmul_rn(lo, cw[j]), __fmul_rn(hi, sw[j]));
-              x[p][8 + 2 * i + j] = __fadd_rn(__fmul_rn(hi, cw[j]), __fmul_rn(lo, sw[j]));
+        for (int p = 0; p < NP; ++p) {
+          const int at = base + p * TPP + tk;
+          if (at >= w0 && at < w1) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float4 w = rope_s[p * TPP + tk][i * LPT + sub];
+              const float cw[2] = {w.x, w.z}, sw[2] = {w.y, w.w};
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                const float lo = x[p][2 * i + j], hi = x[p][8 + 2 * i + j];
+                x[p][2 * i + j] = __fsub_rn(__fmul_rn(lo, cw[j]), __fmul_rn(hi, sw[j]));
+                x[p][8 + 2 * i + j] = __fadd_rn(__fmul_rn(hi, cw[j]), __fmul_rn(lo, sw[j]));
+              }
             }
           }
         }
       }
-    }
-    if (is_q) {
+      if (is_q) {
 #pragma unroll
-      for (int p = 0; p < NP; ++p) {
-        const int at = base + p * TPP + tk;
-        if (at >= w0 && at < w1) {
-          T* o = out + ((int64_t)(r_lo + at - w0) * out_heads + g) * HD + d0;
-          store8<T>(o, x[p]);
-          store8<T>(o + H2, x[p] + 8);
+        for (int p = 0; p < NP; ++p) {
+          const int at = base + p * TPP + tk;
+          if (at >= w0 && at < w1) {
+            T* o = out + ((int64_t)(r_lo + at - w0) * out_heads + g) * HD + d0;
+            store8<T>(o, x[p]);
+            store8<T>(o + H2, x[p] + 8);
+          }
         }
+        continue;
       }
-      continue;
-    }
-    if (page < 0 || page >= c.n_pages) {
-      if (lane == 0 && a.status) atomicOr(a.status, FDLLM_KV8_BAD_PAGE);
-      continue;
-    }
-    const int sb = base % FDLLM_KV8_PAGE / BLK;
-    float* sp = (is_v ? c.v_scale : c.k_scale) + (int64_t)page * c.scale_stride + g * 4 + sb;
-    int8_t* codes = (is_v ? c.v : c.k) + (int64_t)page * c.page_stride +
-                    ((int64_t)g * FDLLM_KV8_PAGE + sb * BLK) * HD + d0;
-    // old tokens of the block that stay: before w0, or behind the new rows
-    const bool any_kept = base < min(len, w0) || w1 < min(len, base + BLK);
-    const float old = any_kept ? *sp : 0.0f;
-    float top = 0.0f;
-#pragma unroll
-    for (int p = 0; p < NP; ++p)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) top = max_nan(top, x[p][i]);
-    const bool finite = __all_sync(0xffffffffu, top <= 3.402823466e38f);
-    if (!finite) {
-      top = 0.0f;
+      if (page < 0 || page >= c.n_pages) {
+        if (lane == 0 && a.status) atomicOr(a.status, FDLLM_KV8_BAD_PAGE);
+        continue;
+      }
+      const int sb = base % FDLLM_KV8_PAGE / BLK;
+      float* sp = (is_v ? c.v_scale : c.k_scale) + (int64_t)page * c.scale_stride + g * 4 + sb;
+      int8_t* codes = (is_v ? c.v : c.k) + (int64_t)page * c.page_stride +
+                      ((int64_t)g * FDLLM_KV8_PAGE + sb * BLK) * HD + d0;
+      // old tokens of the block that stay: before w0, or behind the new rows
+      const bool any_kept = base < min(len, w0) || w1 < min(len, base + BLK);
+      const float old = any_kept ? *sp : 0.0f;
+      float top = 0.0f;
 #pragma unroll
       for (int p = 0; p < NP; ++p)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) top = fmaxf(top, finite_abs(x[p][i]));
-    }
-    top = warp_max(top);
-    float scale = fmaxf(old, __fmul_rn(top, 1.0f / 127.0f));
-    if (!(scale >= TINY_SCALE)) scale = 0.0f;
-    const float inv = scale > 0.0f ? __fdiv_rn(1.0f, scale) : 0.0f;
-    const bool regrid = any_kept && scale != old;
-    const float ratio = regrid && scale > 0.0f ? __fdiv_rn(old, scale) : 0.0f;
-    __syncwarp();   // every lane has read the old scale
-    if (lane == 0) *sp = scale;
+        for (int i = 0; i < 16; ++i) top = max_nan(top, x[p][i]);
+      const bool finite = __all_sync(0xffffffffu, top <= 3.402823466e38f);
+      if (!finite) {
+        top = 0.0f;
 #pragma unroll
-    for (int p = 0; p < NP; ++p) {
-      const int slot = p * TPP + tk, at = base + slot;
-      uint2* lo = reinterpret_cast<uint2*>(codes + slot * HD);
-      uint2* hi = reinterpret_cast<uint2*>(codes + slot * HD + H2);
-      if (at >= w0 && at < w1) {
-        float y[16];
-        if (!finite) {   // infinities end at +-127, NaN at 0
+        for (int p = 0; p < NP; ++p)
 #pragma unroll
-          for (int i = 0; i < 16; ++i) x[p][i] = (float)to_code(__fmul_rn(x[p][i], inv));
+          for (int i = 0; i < 16; ++i) top = fmaxf(top, finite_abs(x[p][i]));
+      }
+      top = warp_max(top);
+      float scale = fmaxf(old, __fmul_rn(top, 1.0f / 127.0f));
+      if (!(scale >= TINY_SCALE)) scale = 0.0f;
+      const float inv = scale > 0.0f ? __fdiv_rn(1.0f, scale) : 0.0f;
+      const bool regrid = any_kept && scale != old;
+      const float ratio = regrid && scale > 0.0f ? __fdiv_rn(old, scale) : 0.0f;
+      __syncwarp();   // every lane has read the old scale
+      if (lane == 0) *sp = scale;
+#pragma unroll
+      for (int p = 0; p < NP; ++p) {
+        const int slot = p * TPP + tk, at = base + slot;
+        uint2* lo = reinterpret_cast<uint2*>(codes + slot * HD);
+        uint2* hi = reinterpret_cast<uint2*>(codes + slot * HD + H2);
+        if (at >= w0 && at < w1) {
+          float y[16];
+          if (!finite) {   // infinities end at +-127, NaN at 0
+#pragma unroll
+            for (int i = 0; i < 16; ++i) x[p][i] = (float)to_code(__fmul_rn(x[p][i], inv));
+          }
+          const float by = finite ? inv : 1.0f;
+          *lo = codes8(x[p], by, y);
+          *hi = codes8(x[p] + 8, by, y + 8);
+          if (out) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) y[i] = __fmul_rn(y[i], scale);
+            T* o = out + ((int64_t)(r_lo + at - w0) * out_heads + g) * HD + d0;
+            store8<T>(o, y);
+            store8<T>(o + H2, y + 8);
+          }
+        } else if (regrid && at < len) {
+          *lo = rescale8(*lo, ratio);
+          *hi = rescale8(*hi, ratio);
         }
-        const float by = finite ? inv : 1.0f;
-        *lo = codes8(x[p], by, y);
-        *hi = codes8(x[p] + 8, by, y + 8);
-        if (out) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) y[i] = __fmul_rn(y[i], scale);
-          T* o = out + ((int64_t)(r_lo + at - w0) * out_heads + g) * HD + d0;
-          store8<T>(o, y);
-          store8<T>(o + H2, y + 8);
-        }
-      } else if (regrid && at < len) {
-        *lo = rescale8(*lo, ratio);
-        *hi = rescale8(*hi, ratio);
       }
     }
   }
@@ -324,8 +362,14 @@ extern "C" int fdllm_kv8_append(const fdllm_kv8* cache, const fdllm_kv8_append_a
   const int rows = a.max_new > 0 ? std::min(a.max_new, a.n_tokens) : a.n_tokens;
   const int64_t blocks = std::max<int64_t>(1, ((int64_t)rows + 2 * BLK - 2) / BLK);
   const int heads = 2 * P.c.n_kv_heads + (a.q ? a.n_heads : 0);
-  const dim3 grid((heads + APP_WARPS - 1) / APP_WARPS, (unsigned)std::min<int64_t>(blocks, 65535),
-                  P.c.n_seqs);
+  // Many CTAs' worth of heads: 4 to a warp, each loaded while the one before is
+  // worked on.  Few: one each, all in flight at once.
+  int sms = 0;
+  if (cudaError_t e = kv8::sm_count(&sms)) return kv8::fail(call, FDLLM_ERR_CUDA, cudaGetErrorString(e));
+  const int64_t groups = (heads + APP_WARPS - 1) / APP_WARPS;
+  P.per_warp = groups * blocks * P.c.n_seqs > 8 * (int64_t)sms ? 4 : 1;
+  const dim3 grid((unsigned)((groups + P.per_warp - 1) / P.per_warp),
+                  (unsigned)std::min<int64_t>(blocks, 65535), P.c.n_seqs);
   cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
   const cudaError_t e = a.dtype == FDLLM_DTYPE_F32    ? launch_append_t<float>(P, grid, st)
                         : a.dtype == FDLLM_DTYPE_BF16 ? launch_append_t<__nv_bfloat16>(P, grid, st)
