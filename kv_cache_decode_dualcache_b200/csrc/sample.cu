@@ -2,8 +2,9 @@
 // and min-p, drawn with a given uniform number.
 //
 // A row is split over the CTAs of a thread-block cluster and read from
-// memory once, into their shared memories; everything else happens there and
-// over distributed shared memory, in one launch without a workspace.
+// memory once, into their shared memories (or, with many long rows, into L2);
+// everything else happens there and over distributed shared memory, in one
+// launch without a workspace.
 //
 // The kept tokens are a prefix of the row sorted by (falling logit, rising
 // id).  Usually a small superset of them is known early: min-p bounds
@@ -27,6 +28,7 @@
 // Bound: the logits' bytes for many rows; for few rows the chain of cluster
 // barriers.
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -151,44 +153,84 @@ FD_DEV u64 fixed(double w) {
 FD_DEV float z_of(const Row& r, float l) { return __fmul_rn(r.m - l, r.zs); }
 FD_DEV bool below_cut(const Row& r, float l) { return r.has_cut && logit_key(l) <= r.cut_key; }
 
-// f(index, logits) for the slice's tokens, 16 bytes at a time.
-template <typename T, typename F>
-FD_DEV void for_vectors(const T* x, int n, F f) {
-  constexpr int VEC = 16 / sizeof(T);
-  const uint4* v = reinterpret_cast<const uint4*>(x);
-  for (int i = threadIdx.x; i * VEC < n; i += ST) {
-    const uint4 u = v[i];
-    const T* e = reinterpret_cast<const T*>(&u);
-    float l[VEC];
+// A CTA's tokens: a copy in shared memory, prepared when it was made, or the
+// logits themselves (16-byte aligned), prepared when they are read.
+template <typename T, bool STAGED>
+struct Slice {
+  static constexpr int VEC = 16 / sizeof(T);
+  const T* p;
+  int n, mask;    // mask: index of the masked token, out of [0, n) if it is not here
+  bool inf;       // infinite logits count as equal ones, the rest as -inf
+  FD_DEV float fix(float l, int i) const {
+    if (STAGED) return l;
+    if (i == mask) l = -INFINITY;
+    if (inf) l = l == INFINITY ? 0.0f : -INFINITY;
+    return l;
+  }
+  FD_DEV float at(int i) const { return fix(to_f<T>(p[i]), i); }
+  // logits of tokens i VEC .. i VEC + VEC - 1, -inf behind the last one
+  FD_DEV void vec(int i, float* l) const {
+    uint4 u;
+    T* e = reinterpret_cast<T*>(&u);
+    if (STAGED || (i + 1) * VEC <= n) {
+      u = reinterpret_cast<const uint4*>(p)[i];
+    } else {
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) l[j] = to_f<T>(e[j]);
-    f(i * VEC, l);
+      for (int j = 0; j < VEC; ++j) e[j] = i * VEC + j < n ? p[i * VEC + j] : from_f<T>(-INFINITY);
+    }
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) l[j] = fix(to_f<T>(e[j]), i * VEC + j);
+  }
+};
+
+// Largest of two vectors element by element, in their type; NaN never wins.
+template <typename T> FD_DEV uint4 max_vec(uint4 a, uint4 b) {
+  uint32_t* x = reinterpret_cast<uint32_t*>(&a);
+  const uint32_t* y = reinterpret_cast<const uint32_t*>(&b);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (std::is_same_v<T, float>)
+      x[i] = __float_as_uint(fmaxf(__uint_as_float(x[i]), __uint_as_float(y[i])));
+    else if constexpr (std::is_same_v<T, __half>)
+      asm("max.f16x2 %0, %0, %1;" : "+r"(x[i]) : "r"(y[i]));
+    else
+      asm("max.bf16x2 %0, %0, %1;" : "+r"(x[i]) : "r"(y[i]));
+  }
+  return a;
+}
+
+// f(index, logits) for the slice's tokens, 16 bytes at a time.
+template <typename X, typename F>
+FD_DEV void for_vectors(const X& x, F f) {
+  for (int i = threadIdx.x; i * X::VEC < x.n; i += ST) {
+    float l[X::VEC];
+    x.vec(i, l);
+    f(i * X::VEC, l);
   }
 }
 // f(index, logit) for the slice's tokens with pred(logit), for rare ones: a
 // thread first marks its hits among 32 tokens, then visits them, so that a
 // warp runs f as often as its busiest lane has hits.
-template <typename T, typename P, typename F>
-FD_DEV void for_hits(const T* x, int n, P pred, F f) {
-  constexpr int VEC = 16 / sizeof(T), G = 32 / VEC;
-  const uint4* v = reinterpret_cast<const uint4*>(x);
-  for (int i0 = threadIdx.x; i0 * VEC < n; i0 += G * ST) {
+template <typename X, typename P, typename F>
+FD_DEV void for_hits(const X& x, P pred, F f) {
+  constexpr int VEC = X::VEC, G = 32 / VEC;
+  for (int i0 = threadIdx.x; i0 * VEC < x.n; i0 += G * ST) {
     uint32_t hits = 0;
 #pragma unroll
     for (int g = 0; g < G; ++g) {
       const int i = i0 + g * ST;
-      if (i * VEC < n) {
-        const uint4 u = v[i];
-        const T* e = reinterpret_cast<const T*>(&u);
+      if (i * VEC < x.n) {
+        float l[VEC];
+        x.vec(i, l);
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) hits |= pred(to_f<T>(e[j])) ? 1u << (g * VEC + j) : 0u;
+        for (int j = 0; j < VEC; ++j) hits |= pred(l[j]) ? 1u << (g * VEC + j) : 0u;
       }
     }
     while (hits) {
       const int b = __ffs(hits) - 1;
       hits &= hits - 1;
       const int i = (i0 + (b / VEC) * ST) * VEC + b % VEC;
-      f(i, to_f<T>(x[i]));
+      f(i, x.at(i));
     }
   }
 }
@@ -198,21 +240,54 @@ FD_DEV u64 warp_sum64(u64 v) {
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
+// Every thread owns a run of ids, [tid run, tid run + run): an odd number of
+// vectors, so that the threads' reads of shared memory meet no bank twice.
+template <typename X>
+FD_DEV int run_of(const X& x) { return ((x.n + ST * X::VEC - 1) / (ST * X::VEC) | 1) * X::VEC; }
+// Sum of f(logit) over the thread's run, of tokens with pred(index, logit).
+// They are marked first, so that a warp runs f as often as its busiest lane
+// has them.
+template <typename X, typename P, typename F>
+FD_DEV u64 run_sum(const X& x, P pred, F f) {
+  constexpr int VEC = X::VEC;
+  const int run = run_of(x), i0 = threadIdx.x * run, i1 = min(i0 + run, x.n);
+  u64 sum = 0;
+  for (int j0 = i0; j0 < i1; j0 += 32) {
+    uint32_t hits = 0;
+#pragma unroll
+    for (int g = 0; g < 32; g += VEC) {
+      if (j0 + g >= i1) break;
+      float l[VEC];
+      x.vec((j0 + g) / VEC, l);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j)
+        if (pred(j0 + g + j, l[j])) hits |= 1u << (g + j);
+    }
+    while (hits) {
+      const int j = __ffs(hits) - 1;
+      hits &= hits - 1;
+      sum += f(x.at(j0 + j));
+    }
+  }
+  return sum;
+}
 // Inclusive prefix sum over the threads; *total over all of them.
-FD_DEV u64 block_scan(u64 v, Shared& s, u64* total) {
+template <typename U>
+FD_DEV U block_scan(U v, Shared& s, U* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const u64 y = __shfl_up_sync(0xffffffffu, v, o);
+    const U y = __shfl_up_sync(0xffffffffu, v, o);
     if (lane >= o) v += y;
   }
   __syncthreads();
-  if (lane == 31) s.red[warp] = v;
+  U* red = reinterpret_cast<U*>(s.red);
+  if (lane == 31) red[warp] = v;
   __syncthreads();
-  u64 t = 0;
+  U t = 0;
 #pragma unroll
   for (int i = 0; i < SW; ++i) {
-    const u64 x = s.red[i];
+    const U x = red[i];
     if (i < warp) v += x;
     t += x;
   }
@@ -268,19 +343,21 @@ template <bool MASS, typename F>
 FD_DEV u64 find_bin(Shared& s, int h, int n_cta, u64* above, F need_of) {
   // two threads a bin, each for half of the CTAs
   const int bin = threadIdx.x >> 1, half = threadIdx.x & 1;
-  u64 v = 0;
+  typedef std::conditional_t<MASS, u64, uint32_t> U;
+  U v = 0, sum;
 #pragma unroll
   for (int j = 0; j < MAX_CLUSTER / 2; ++j) {
     const int i = 2 * j + half;
     if (i >= n_cta) continue;
     v += ld_remote32(&s.hist[h][0][bin], i);
-    if (MASS)
+    if constexpr (MASS)
       v += ((u64)ld_remote32(&s.hist[h][1][bin], i) << 15) +
            ((u64)ld_remote32(&s.hist[h][2][bin], i) << 30);
   }
-  const u64 upto = block_scan(v, s, above);
+  const U upto = block_scan(v, s, &sum);
+  *above = sum;
   const u64 need = need_of(*above);
-  const u64 bin_sum = v + __shfl_xor_sync(0xffffffffu, v, 1);
+  const U bin_sum = v + __shfl_xor_sync(0xffffffffu, v, 1);
   if (half == 1 && upto - bin_sum < need && need <= upto) {
     s.bin = bin;
     s.before = upto - bin_sum;
@@ -291,8 +368,8 @@ FD_DEV u64 find_bin(Shared& s, int h, int n_cta, u64* above, F need_of) {
 }
 
 // Sets the cut to the `ties`-th token (by id) of the class with key r.cut_key.
-template <typename T>
-FD_DEV void nth_tie(Shared& s, Row& r, int ties, const T* x, int n, int id0, int n_cta, int rank,
+template <typename X>
+FD_DEV void nth_tie(Shared& s, Row& r, int ties, const X& x, int id0, int n_cta, int rank,
                     int& use) {
   r.ties = ties;
   if (r.listed) {
@@ -309,18 +386,18 @@ FD_DEV void nth_tie(Shared& s, Row& r, int ties, const T* x, int n, int id0, int
     return;
   }
   const float lc = key_logit(r.cut_key);
-  const int run = ((n + ST - 1) / ST) | 1;
-  const int i0 = min((int)threadIdx.x * run, n), i1 = min(i0 + run, n);
-  u64 mine = 0, lower, cta;
-  for (int i = i0; i < i1; ++i) mine += to_f<T>(x[i]) == lc;
+  u64 lower, cta;
+  const u64 mine = run_sum(x, [&](int, float l) { return l == lc; }, [](float) { return (u64)1; });
   u64 before = block_scan(mine, s, &cta) - mine;
   cluster_total(cta, s, n_cta, rank, use++, &lower);
   before += lower;
   if (threadIdx.x == 0) s.cut_id = -1;
   __syncthreads();
-  if (before < (u64)ties && (u64)ties <= before + mine)
-    for (int i = i0; i < i1; ++i)
-      if (to_f<T>(x[i]) == lc && ++before == (u64)ties) s.cut_id = id0 + i;
+  if (before < (u64)ties && (u64)ties <= before + mine) {
+    const int run = run_of(x), i0 = threadIdx.x * run;
+    for (int i = i0; i < min(i0 + run, x.n); ++i)
+      if (x.at(i) == lc && ++before == (u64)ties) s.cut_id = id0 + i;
+  }
   __syncthreads();
   // the CTA that holds it tells the others (ids as id + 1, none = 0)
   r.cut_id = (int)cluster_total((u64)(s.cut_id + 1), s, n_cta, rank, use++, nullptr) - 1;
@@ -332,11 +409,11 @@ struct Level {
   u64 need, above, before, upto;   // above: strictly above the cut
   int bin;                         // valid if 0 < need <= above
 };
-template <bool MASS, typename T, typename F>
-FD_DEV Level level1(Shared& s, const Row& r, const T* x, int n, int n_cta, F need_of) {
+template <bool MASS, typename X, typename F>
+FD_DEV Level level1(Shared& s, const Row& r, const X& x, int n_cta, F need_of) {
   const u64 at_cut = r.has_cut ? (u64)r.ties * (MASS ? fixed(weight(r, key_logit(r.cut_key))) : 1) : 0;
-  for_vectors(x, n, [&](int, const float* l) {
-    constexpr int VEC = 16 / sizeof(T);
+  for_vectors(x, [&](int, const float* l) {
+    constexpr int VEC = X::VEC;
     u64 w[VEC];
     if (MASS) {
 #pragma unroll
@@ -358,9 +435,9 @@ FD_DEV Level level1(Shared& s, const Row& r, const T* x, int n, int n_cta, F nee
 }
 
 // Moves the cut to the token at which the sum reaches v.need.
-template <bool MASS, typename T>
-FD_DEV void refine(Shared& s, Row& r, const Level& v, const T* x, int n, int id0, int n_cta,
-                   int rank, int& use) {
+template <bool MASS, typename X>
+FD_DEV void refine(Shared& s, Row& r, const Level& v, const X& x, int id0, int n_cta, int rank,
+                   int& use) {
   const int tid = threadIdx.x;
   auto unit = [&](float l) { return MASS ? fixed(weight(r, l)) : (u64)1; };
   if (v.need == 0 || v.need > v.above) {
@@ -378,9 +455,9 @@ FD_DEV void refine(Shared& s, Row& r, const Level& v, const T* x, int n, int id0
       r.cut_key = logit_key(r.m);
       r.has_cut = true;
       r.listed = false;
-      nth_tie(s, r, 1, x, n, id0, n_cta, rank, use);
+      nth_tie(s, r, 1, x, id0, n_cta, rank, use);
     } else if (r.has_cut && ties < r.ties) {
-      nth_tie(s, r, ties, x, n, id0, n_cta, rank, use);
+      nth_tie(s, r, ties, x, id0, n_cta, rank, use);
     }
     return;
   }
@@ -394,7 +471,7 @@ FD_DEV void refine(Shared& s, Row& r, const Level& v, const T* x, int n, int id0
   auto bin2 = [&](float l) { return (int)((z_of(r, l) - lo) * BINS); };
   if (tid == 0) s.n_list = s.n_sub = 0;
   __syncthreads();
-  for_hits(x, n, in_bin1, [&](int i, float l) {
+  for_hits(x, in_bin1, [&](int i, float l) {
     const int at = atomicAdd(&s.n_list, 1);
     if (at < CAP) s.list[at] = order_of(l, id0 + i);
   });
@@ -404,7 +481,7 @@ FD_DEV void refine(Shared& s, Row& r, const Level& v, const T* x, int n, int id0
     if (n1 <= CAP)
       for (int j = tid; j < n1; j += ST) f(s.list[j]);
     else
-      for_hits(x, n, in_bin1, [&](int i, float l) { f(order_of(l, id0 + i)); });
+      for_hits(x, in_bin1, [&](int i, float l) { f(order_of(l, id0 + i)); });
   };
   for_bin([&](u64 o) {
     const float l = order_logit(o);
@@ -468,7 +545,7 @@ FD_DEV void refine(Shared& s, Row& r, const Level& v, const T* x, int n, int id0
   const uint32_t kmax = k1;
   auto upto = [&](uint32_t k) {   // sum up to and over the bin's tokens with key >= k
     u64 t = 0;
-    for_hits(x, n, [&](float l) { return in_bin(l) && logit_key(l) >= k; },
+    for_hits(x, [&](float l) { return in_bin(l) && logit_key(l) >= k; },
              [&](int, float l) { t += unit(l); });
     return before + cluster_total(block_sum(t, s), s, n_cta, rank, use++, nullptr);
   };
@@ -481,7 +558,7 @@ FD_DEV void refine(Shared& s, Row& r, const Level& v, const T* x, int n, int id0
   r.cut_key = k0;
   r.has_cut = true;
   r.listed = false;
-  nth_tie(s, r, (int)((v.need - over + w - 1) / w), x, n, id0, n_cta, rank, use);
+  nth_tie(s, r, (int)((v.need - over + w - 1) / w), x, id0, n_cta, rank, use);
 }
 
 // Sorts a[0 .. n) (n a power of two, at most 2 ST), largest first.
@@ -628,16 +705,17 @@ FD_DEV void draw_sorted(Shared& s, const Row& r, const Filters& f, int n, u64 ne
   }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(ST, 2) sample_kernel(const fdllm_sample_args a, int slice, int n_cta) {
+template <typename T, bool STAGED>
+__global__ void __launch_bounds__(ST, STAGED ? 2 : 3) sample_kernel(const fdllm_sample_args a, int slice, int n_cta) {
   extern __shared__ __align__(16) uint8_t smem[];
   Shared& s = *reinterpret_cast<Shared*>(smem);
-  T* x = reinterpret_cast<T*>(smem + sizeof(Shared));
   static_assert(sizeof(Shared) % 16 == 0, "the slice is read 16 bytes at a time");
   const int tid = threadIdx.x, row = blockIdx.x / n_cta, rank = blockIdx.x % n_cta;
   const int id0 = rank * slice, n = max(0, min(slice, a.vocab - id0));
   const T* src = reinterpret_cast<const T*>(a.logits) + (int64_t)row * a.row_stride + id0;
   int use = 0;
+  T* copy = reinterpret_cast<T*>(smem + sizeof(Shared));
+  Slice<T, STAGED> x{STAGED ? copy : src, n, a.mask_id - id0, false};
 
   // ---- the slice (the masked token and the last vector's rest as -inf), and
   // every thread's largest logit
@@ -645,28 +723,31 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const fdllm_sample_args a
   const T none = from_f<T>(-INFINITY);
   float top = -INFINITY;
   {
-    const bool wide = (reinterpret_cast<uintptr_t>(src) & 15) == 0;
-    const int mask = a.mask_id - id0, nv = (n + VEC - 1) / VEC;
-    uint4* xv = reinterpret_cast<uint4*>(x);
+    const bool wide = !STAGED || (reinterpret_cast<uintptr_t>(src) & 15) == 0;
+    const int mask = a.mask_id - id0;
+    uint4 tops;
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) reinterpret_cast<T*>(&tops)[j] = none;
 #pragma unroll 4
-    for (int i = tid; i < nv; i += ST) {
+    for (int i = tid; i * VEC < n; i += ST) {
       uint4 u;
       T* e = reinterpret_cast<T*>(&u);
       if (wide && (i + 1) * VEC <= n) {
-        u = __ldcs(reinterpret_cast<const uint4*>(src) + i);
+        u = STAGED ? __ldcs(reinterpret_cast<const uint4*>(src) + i) : reinterpret_cast<const uint4*>(src)[i];
       } else {
 #pragma unroll
         for (int j = 0; j < VEC; ++j) e[j] = i * VEC + j < n ? src[i * VEC + j] : none;
       }
-      if (mask >= i * VEC && mask < (i + 1) * VEC) {
+      if ((uint32_t)(mask - i * VEC) < (uint32_t)VEC) {
 #pragma unroll
         for (int j = 0; j < VEC; ++j)
           if (i * VEC + j == mask) e[j] = none;
       }
-      xv[i] = u;
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) top = fmaxf(top, to_f<T>(e[j]));   // NaN never wins
+      if (STAGED) reinterpret_cast<uint4*>(copy)[i] = u;
+      tops = max_vec<T>(tops, u);
     }
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) top = fmaxf(top, to_f<T>(reinterpret_cast<const T*>(&tops)[j]));
   }
   zero_hist(s, 0);
   zero_hist(s, 1);
@@ -691,8 +772,11 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const fdllm_sample_args a
     if (i < n_cta) r.m = fmaxf(r.m, __uint_as_float(ld_remote32(&s.top, i)));
 
   if (r.m == INFINITY) {   // they share all the weight: equal logits, the rest is out
-    for (int i = tid; i < n; i += ST)
-      x[i] = from_f<T>(to_f<T>(x[i]) == INFINITY ? 0.0f : -INFINITY);
+    if (STAGED) {
+      for (int i = tid; i < n; i += ST)
+        copy[i] = from_f<T>(to_f<T>(copy[i]) == INFINITY ? 0.0f : -INFINITY);
+    }
+    x.inf = true;
     r.m = 0.0f;
     top = top == INFINITY ? 0.0f : -INFINITY;
     __syncthreads();
@@ -742,7 +826,7 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const fdllm_sample_args a
       }
       used = true;
     } else if (f.top_k == 0 && has_p) {
-      lp = level1<true>(s, r, x, n, n_cta, need_p);
+      lp = level1<true>(s, r, x, n_cta, need_p);
       if (lp.need > 0 && lp.need <= lp.above) {
         // none of the tokens up to the bin's end is lighter than its end
         gather |= (double)lp.upto / W_ONE * exp((lp.bin + 1) / (double)Z_BINS) <= CAP;
@@ -763,16 +847,14 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const fdllm_sample_args a
       for (int j = tid; j < items; j += ST) {
         const int i = s.hot[j / per] + (j % per) * ST;
         if (i * VEC >= n) continue;
-        const uint4 v = reinterpret_cast<const uint4*>(x)[i];
-        const T* e = reinterpret_cast<const T*>(&v);
+        float l[VEC];
+        x.vec(i, l);
 #pragma unroll
-        for (int q = 0; q < VEC; ++q) {
-          const float l = to_f<T>(e[q]);
-          if (z_of(r, l) < z_end) {
+        for (int q = 0; q < VEC; ++q)
+          if (z_of(r, l[q]) < z_end) {
             const int at = atomicAdd(&s.n_list, 1);
-            if (at < CAP) s.list[at] = order_of(l, id0 + i * VEC + q);
+            if (at < CAP) s.list[at] = order_of(l[q], id0 + i * VEC + q);
           }
-        }
       }
       cluster_sync();
       int n_all = 0;
@@ -797,17 +879,14 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const fdllm_sample_args a
       }
       if (f.top_k > 0) {
         __syncthreads();
-        const Level v = level1<false>(s, r, x, n, n_cta, [&](u64) { return (u64)f.top_k; });
-        refine<false>(s, r, v, x, n, id0, n_cta, rank, use);
-        if (has_p) lp = level1<true>(s, r, x, n, n_cta, need_p);
+        const Level v = level1<false>(s, r, x, n_cta, [&](u64) { return (u64)f.top_k; });
+        refine<false>(s, r, v, x, id0, n_cta, rank, use);
+        if (has_p) lp = level1<true>(s, r, x, n_cta, need_p);
       }
-      if (has_p) refine<true>(s, r, lp, x, n, id0, n_cta, rank, use);
+      if (has_p) refine<true>(s, r, lp, x, id0, n_cta, rank, use);
 
-      // ---- the draw: every thread takes a run of ids (odd: no bank conflicts)
-      const int run = ((n + ST - 1) / ST) | 1;
-      const int i0 = min(tid * run, n), i1 = min(i0 + run, n);
-      auto kept = [&](int i) {
-        const float l = to_f<T>(x[i]);
+      // ---- the draw: every thread has a run of ids
+      auto kept = [&](int i, float l) {
         bool in = z_of(r, l) < z_end;
         if (r.has_cut) {
           const uint32_t k = logit_key(l);
@@ -815,32 +894,16 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const fdllm_sample_args a
         }
         return in;
       };
-      auto kept_w = [&](int i) {
-        const double wd = weight(r, to_f<T>(x[i]));
-        return kept(i) && !(f.min_p > 0.0 && wd < f.min_p) ? fixed(wd) : (u64)0;
+      auto weigh = [&](float l) {
+        const double wd = weight(r, l);
+        return f.min_p > 0.0 && wd < f.min_p ? (u64)0 : fixed(wd);
       };
-      u64 sum = 0, lower, mine;
+      u64 lower, mine;
       int first = 0x7fffffff;
-      if (r.has_cut || z_end < (float)BINS) {   // few are kept: mark them, then weigh them
-        for (int j0 = i0; j0 < i1; j0 += 32) {
-          uint32_t hits = 0;
-#pragma unroll 8
-          for (int j = 0; j < 32; ++j)
-            if (j0 + j < i1 && kept(j0 + j)) hits |= 1u << j;
-          while (hits) {
-            const int j = __ffs(hits) - 1;
-            hits &= hits - 1;
-            const double wd = weight(r, to_f<T>(x[j0 + j]));
-            if (!(f.min_p > 0.0 && wd < f.min_p)) sum += fixed(wd);
-          }
-        }
-      } else {
-#pragma unroll 4
-        for (int i = i0; i < i1; ++i) sum += kept_w(i);
-      }
+      const u64 sum = run_sum(x, kept, weigh);
       if (f.greedy)
-        for (int i = i1 - 1; i >= i0; --i)
-          if (to_f<T>(x[i]) == r.m) first = id0 + i;
+        for (int i = tid; i < n && first == 0x7fffffff; i += ST)
+          if (x.at(i) == r.m) first = id0 + i;
       u64 before = block_scan(sum, s, &mine) - sum;
       const u64 all = cluster_total(mine, s, n_cta, rank, use++, &lower);
       if (f.greedy) {
@@ -861,15 +924,16 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const fdllm_sample_args a
         if (tid == 0) s.run1 = -1;
         __syncthreads();
         if (before <= target && target < before + sum) {   // this thread's run: a warp walks it
-          s.run0 = i0;
-          s.run1 = i1;
+          s.run0 = tid * run_of(x);
+          s.run1 = min(s.run0 + run_of(x), n);
           s.before = before;
         }
         __syncthreads();
         if (s.run1 >= 0 && tid < 32) {
           u64 base = s.before;
           for (int i = s.run0; i < s.run1; i += 32) {
-            const u64 w = i + tid < s.run1 ? kept_w(i + tid) : 0;
+            const float l = i + tid < s.run1 ? x.at(i + tid) : -INFINITY;
+            const u64 w = i + tid < s.run1 && kept(i + tid, l) ? weigh(l) : 0;
             u64 upto = w;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -880,7 +944,7 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const fdllm_sample_args a
             if (upto - w <= target && target < upto) {
               a.tok[row] = id0 + i + tid;
               if (a.prob)
-                a.prob[row] = (float)(weight(r, to_f<T>(x[i + tid])) / ((double)all / W_ONE));
+                a.prob[row] = (float)(weight(r, l) / ((double)all / W_ONE));
             }
             base = __shfl_sync(0xffffffffu, upto, 31);
           }
@@ -899,11 +963,19 @@ cudaError_t launch_sample(const fdllm_sample_args& a, cudaStream_t st) {
   auto slice_of = [&](int n) { return ((a.vocab + n - 1) / n + 15) / 16 * 16; };
   while (c < MAX_CLUSTER && (slice_of(c) * (int)sizeof(T) > SLICE_BYTES || slice_of(c) > MAX_SLICE)) c *= 2;
   while (c < MAX_CLUSTER && (int64_t)a.rows * c * 2 <= 296 && slice_of(c) >= 4096) c *= 2;
+  // Slices that need a cluster are so large that two CTAs fill an SM's shared
+  // memory.  Rows for more than two waves of those leave the logits where they
+  // are: the copy of the first pass in L2 serves the later ones, and a third CTA
+  // fits on the SM.  bf16, 126464 tokens, top_k 200, top_p 0.95, min_p 0.01: 512 rows 165 -> 131 us, 256 rows 94 -> 88, but 75 rows
+  // 46 -> 55; wide nuclei (top_p 0.9 alone), which read the slice most often, 5 to
+  // 7% slower.  32000 tokens (one CTA a row): 78 -> 98 us, so not there.
+  const bool aligned = kv8::aligned16(a.logits) && a.row_stride * (int64_t)sizeof(T) % 16 == 0;
+  const bool staged = c == 1 || (int64_t)a.rows * c <= 592 || !aligned;
   const int slice = slice_of(c);
-  const int smem = (int)sizeof(Shared) + slice * (int)sizeof(T);
-  auto kern = sample_kernel<T>;
-  static std::atomic<uint64_t> ready{0};   // devices whose limit is set
-  const cudaError_t e = kv8::allow_smem(kern, 227 << 10, ready);
+  const int smem = (int)sizeof(Shared) + (staged ? slice * (int)sizeof(T) : 0);
+  auto kern = staged ? sample_kernel<T, true> : sample_kernel<T, false>;
+  static std::atomic<uint64_t> ready[2];   // devices whose limit is set
+  const cudaError_t e = kv8::allow_smem(kern, 227 << 10, ready[staged]);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((int64_t)a.rows * c));

@@ -110,6 +110,38 @@ def test_many_rows_and_the_largest_vocabulary():
         _check(y, [0.3, 0.9])
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+def test_many_long_rows(dtype):
+    """So many long rows that they are not copied on chip: an odd vocabulary in
+    a wider buffer, rows without a live token, with infinities, NaN and ties, and
+    kept sets of every size."""
+    rows, vocab = 300, 41003
+    g = torch.Generator().manual_seed(31)
+    x = torch.full((rows, 41008), float("nan"))
+    x[:, :vocab] = _logits(g, rows, vocab, 1.5) * torch.tensor([0.01, 0.5, 1.0, 2.0])[torch.arange(rows) % 4, None]
+    x[5] = -float("inf")
+    x[6, 3:vocab:11] = float("inf")
+    x[7, :vocab] = 0.5
+    x[8, ::2] = float("nan")
+    x[9, :vocab] = -float("inf")
+    x[9, vocab - 1] = 7.0
+    x = x.to(TYPES[dtype])
+    u = torch.rand(rows, generator=g, dtype=torch.float64)
+    pick = torch.randint(0, 1 << 30, (4, rows), generator=g)
+    f = {"temperature": torch.where(pick[0] % 5 == 0, 0.0, 0.3 + (pick[0] % 1000) / 800.0),
+         "top_k": torch.where(pick[1] % 2 == 0, 0, 1 + pick[1] % 3001).to(torch.int32),
+         "top_p": torch.where(pick[2] % 2 == 0, 1.0, 0.05 + (pick[2] % 997) / 1050.0),
+         "min_p": torch.where(pick[3] % 2 == 0, 0.0, (pick[3] % 991) / 5000.0)}
+    f = {n: v.to(torch.int32 if n == "top_k" else torch.float32) for n, v in f.items()}
+    mask = vocab - 1
+    tok, prob = fdllm.fdllm_sample(x.cuda()[:, :vocab], u.cuda(), mask_id=mask, **{n: v.cuda() for n, v in f.items()})
+    for r in range(rows):
+        want, p, _ = kv8_ref.sample_row(x[r, :vocab].double().numpy(), float(u[r]), mask_id=mask,
+                                        **{n: (int if n == "top_k" else float)(v[r]) for n, v in f.items()})
+        assert int(tok[r]) == want, r
+        assert abs(float(prob[r]) - p) <= 2.0 ** -23 * p + 2.0 ** -27, r
+
+
 def test_filter_settings_at_their_ends():
     g = torch.Generator().manual_seed(2)
     x = _logits(g, 8, 700)
