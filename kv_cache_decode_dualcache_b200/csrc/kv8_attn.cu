@@ -132,6 +132,21 @@ __global__ void __launch_bounds__(AT_WARPS * 32, 2) kv8_attn_kernel(const AttnP 
     const int my = n_tiles > warp ? (n_tiles - warp + AT_WARPS - 1) / AT_WARPS : 0;
     const int32_t* table = c.page_table + (int64_t)sg.seq * c.table_stride;
 
+    // ---- q: a warp per row, lanes with 4 dims each, on its way while the page
+    // table is read; then in fragment order to shared memory
+    float qx[R / AT_WARPS][4];
+    {
+      int token = (sg.row0 + warp) / rep, head = (sg.row0 + warp) % rep;
+#pragma unroll
+      for (int j = 0; j < R / AT_WARPS; ++j) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) qx[j][i] = 0.0f;
+        if (sg.row0 + warp + j * AT_WARPS < rows && lane < HD / 4)
+          load4(reinterpret_cast<const T*>(a.q) + (int64_t)(r_lo + token) * a.q_strides[0] +
+                    (int64_t)(g * rep + head) * a.q_strides[1] + lane * 4, qx[j]);
+        for (head += AT_WARPS; head >= rep; head -= rep) ++token;
+      }
+    }
     int pages = 0;   // lane i: page of the warp's tile (issued & ~31) + i
     auto issue = [&](int i) {
       if (i < my) {
@@ -167,21 +182,6 @@ __global__ void __launch_bounds__(AT_WARPS * 32, 2) kv8_attn_kernel(const AttnP 
     };
 #pragma unroll
     for (int i = 0; i < STAGES - 1; ++i) issue(i);
-
-    // ---- q: a warp per row, lanes with 4 dims each; fragment order in shared memory
-    float qx[R / AT_WARPS][4];
-    {
-      int token = (sg.row0 + warp) / rep, head = (sg.row0 + warp) % rep;
-#pragma unroll
-      for (int j = 0; j < R / AT_WARPS; ++j) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) qx[j][i] = 0.0f;
-        if (sg.row0 + warp + j * AT_WARPS < rows && lane < HD / 4)
-          load4(reinterpret_cast<const T*>(a.q) + (int64_t)(r_lo + token) * a.q_strides[0] +
-                    (int64_t)(g * rep + head) * a.q_strides[1] + lane * 4, qx[j]);
-        for (head += AT_WARPS; head >= rep; head -= rep) ++token;
-      }
-    }
 #pragma unroll
     for (int j = 0; j < R / AT_WARPS; ++j) {
       const int r = warp + j * AT_WARPS;
