@@ -38,6 +38,11 @@ int64_t integer(PyObject* o) {
   if (v == -1 && PyErr_Occurred()) throw std::nullopt;
   return v;
 }
+int32_t integer32(PyObject* o, const char* name) {
+  const int64_t v = integer(o);
+  if (v < INT32_MIN || v > INT32_MAX) throw Refused{std::string(name) + " must fit in 32 bits"};
+  return (int32_t)v;
+}
 double number(PyObject* o) {
   const double v = PyFloat_AsDouble(o);
   if (v == -1.0 && PyErr_Occurred()) throw std::nullopt;
@@ -85,10 +90,24 @@ void* rows(const at::Tensor& t, const char* name, int64_t tokens, int64_t heads,
 at::Tensor empty(at::IntArrayRef sizes, at::ScalarType type, int dev) {
   return at::detail::empty_cuda(sizes, type, at::Device(at::kCUDA, (c10::DeviceIndex)dev), std::nullopt);
 }
-void* stream_of(PyObject* o, int dev) {
-  if (o == Py_None) return c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream();
-  return reinterpret_cast<void*>((uintptr_t)integer(o));
-}
+// The call's device and stream (None: torch's current one) while it is made.
+// Results and workspaces then come from the memory of the stream that writes
+// them: none is handed out again before the stream is past the call.
+struct OnStream {
+  c10::cuda::OptionalCUDAGuard device;
+  c10::cuda::OptionalCUDAStreamGuard stream;
+  void* handle;
+  OnStream(PyObject* o, int dev) {
+    const c10::DeviceIndex d = (c10::DeviceIndex)dev;
+    if (c10::cuda::current_device() != d) device.set_index(d);
+    handle = c10::cuda::getCurrentCUDAStream(d).stream();
+    if (o == Py_None) return;
+    void* given = reinterpret_cast<void*>((uintptr_t)integer(o));
+    if (given == handle) return;
+    handle = given;
+    stream.reset_stream(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(given), d));
+  }
+};
 
 // fn's result: a tuple, or the status of the C call as an int.
 template <typename F> PyObject* guarded(Py_ssize_t n, Py_ssize_t want, F fn) {
@@ -147,7 +166,7 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     p.v = rows(v, "v", T, c.n_kv_heads, c.head_dim, type, dev, p.v_strides);
     if (T > INT32_MAX) throw Refused{"too many tokens"};
     p.n_tokens = (int32_t)T;
-    p.max_new = (int32_t)integer(a[9]);
+    p.max_new = integer32(a[9], "max_new");
     p.starts = vector<int32_t>(a[4], "starts", c.n_seqs + 1, at::kInt, dev);
     p.lens = vector<int32_t>(a[5], "lens", c.n_seqs, at::kInt, dev);
     p.pos = vector<int32_t>(a[6], "pos", c.n_seqs, at::kInt, dev);
@@ -162,8 +181,7 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
       p.rope = static_cast<const float*>(r.data_ptr());
       p.rope_len = (int32_t)r.size(0);
     }
-    c10::cuda::OptionalCUDAGuard guard;
-    if (c10::cuda::current_device() != dev) guard.set_index((c10::DeviceIndex)dev);
+    const OnStream on(a[13], dev);
     at::Tensor q_out, k_out, v_out;
     if (a[8] != Py_None) {
       const at::Tensor& q = tensor(a[8], "q");
@@ -178,7 +196,7 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
       p.k_out = k_out.data_ptr();
       p.v_out = v_out.data_ptr();
     }
-    return status_or(c_append(&c, &p, stream_of(a[13], dev)), {&q_out, &k_out, &v_out});
+    return status_or(c_append(&c, &p, on.handle), {&q_out, &k_out, &v_out});
   });
 }
 
@@ -197,14 +215,13 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (T > INT32_MAX) throw Refused{"too many tokens"};
     p.n_tokens = (int32_t)T;
     p.n_heads = (int32_t)q.size(1);
-    p.max_q = (int32_t)integer(a[7]);
-    p.max_len = (int32_t)integer(a[8]);
+    p.max_q = integer32(a[7], "max_q");
+    p.max_len = integer32(a[8], "max_len");
     p.scale = a[5] == Py_None ? 1.0f / std::sqrt((float)c.head_dim) : (float)number(a[5]);
     p.starts = vector<int32_t>(a[3], "starts", c.n_seqs + 1, at::kInt, dev);
     p.lens = vector<int32_t>(a[4], "lens", c.n_seqs, at::kInt, dev);
     p.status = vector<int32_t>(a[10], "status", 1, at::kInt, dev);
-    c10::cuda::OptionalCUDAGuard guard;
-    if (c10::cuda::current_device() != dev) guard.set_index((c10::DeviceIndex)dev);
+    const OnStream on(a[11], dev);
     at::Tensor out, space;
     if (a[6] == Py_None) {
       out = empty(q.sizes(), type, dev);
@@ -229,7 +246,7 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
       p.workspace = w.data_ptr();
       p.workspace_bytes = (size_t)w.numel() * w.element_size();
     }
-    return status_or(c_attention(&c, &p, stream_of(a[11], dev)), {&out});
+    return status_or(c_attention(&c, &p, on.handle), {&out});
   });
 }
 
@@ -250,20 +267,19 @@ PyObject* sample(PyObject*, PyObject* const* a, Py_ssize_t n) {
     p.dtype = dtype_code(x.scalar_type());
     p.rows = (int32_t)R;
     p.vocab = (int32_t)V;
-    p.mask_id = (int32_t)integer(a[6]);
+    p.mask_id = integer32(a[6], "mask_id");
     if (a[1] == Py_None) throw Refused{"u must be a tensor"};
     p.u = vector<double>(a[1], "u", R, at::kDouble, dev);
     p.temperature = vector<float>(a[2], "temperature", R, at::kFloat, dev);
     p.top_k = vector<int32_t>(a[3], "top_k", R, at::kInt, dev);
     p.top_p = vector<float>(a[4], "top_p", R, at::kFloat, dev);
     p.min_p = vector<float>(a[5], "min_p", R, at::kFloat, dev);
-    c10::cuda::OptionalCUDAGuard guard;
-    if (c10::cuda::current_device() != dev) guard.set_index((c10::DeviceIndex)dev);
+    const OnStream on(a[9], dev);
     at::Tensor tok = a[7] == Py_None ? empty({R}, at::kInt, dev) : tensor(a[7], "tok");
     at::Tensor prob = a[8] == Py_None ? empty({R}, at::kFloat, dev) : tensor(a[8], "prob");
     p.tok = a[7] == Py_None ? static_cast<int32_t*>(tok.data_ptr()) : vector<int32_t>(a[7], "tok", R, at::kInt, dev);
     p.prob = a[8] == Py_None ? static_cast<float*>(prob.data_ptr()) : vector<float>(a[8], "prob", R, at::kFloat, dev);
-    return status_or(c_sample(&p, stream_of(a[9], dev)), {&tok, &prob});
+    return status_or(c_sample(&p, on.handle), {&tok, &prob});
   });
 }
 

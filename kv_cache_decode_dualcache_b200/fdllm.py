@@ -431,6 +431,8 @@ def fdllm_attention(ctx, q_dev, o_dev, layer: int, L: int) -> None:
 
 
 # ------------------------------------------------ 8-bit paged K/V cache, sampling
+# These calls take a CUDA stream handle (None: torch's current stream) and
+# allocate what they return as torch does under that stream.
 KV8_PAGE, KV8_BLOCK = 64, 16              # positions per page, positions that share a scale
 KV8_BAD_PAGE, KV8_BAD_RANGE = 1, 2        # bits of a call's status word
 
@@ -518,8 +520,7 @@ def fdllm_kv8_attention(cache: Kv8Cache, q, starts, lens, scale: Optional[float]
     """softmax(scale q K^T) V of every row of q [tokens, heads, head_dim] over
     its sequence's cached keys [0, lens[i]); scale None = 1 / sqrt(head_dim).
     workspace: a uint8 tensor to use instead of a fresh one (its size:
-    fdllm_kv8_attention_workspace); pass one when the work is enqueued on a
-    stream that is not torch's current one."""
+    fdllm_kv8_attention_workspace)."""
     r = (_ops or _load_ops()).attention(cache.address, cache.device, q, starts, lens, scale, out, max_q,
                                         max_len, workspace, status, stream)
     if type(r) is int:

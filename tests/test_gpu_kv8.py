@@ -96,6 +96,30 @@ def test_attention_hints_and_workspace_do_not_change_results(dtype, max_q, max_l
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("hq,hkv,hd", HEADS)
+@pytest.mark.parametrize("rows,lens", [
+    ([17], [1]), ([32], [577]), ([3, 0, 17, 1], [63, 64, 65, 1300]), ([70], [129]),
+    ([8, 2, 40], [700, 0, 128]), ([150, 33], [333, 2000])])
+def test_attention_where_contexts_may_be_long(dtype, hq, hkv, hd, rows, lens):
+    """Page tables for a million tokens, of which the sequences use little:
+    the call is laid out for long contexts."""
+    g = torch.Generator().manual_seed(sum(rows) + 5 * sum(lens) + hq + hd)
+    cache = kv8_ref.make_cache(g, lens, hkv, hd)
+    T = sum(rows)
+    q = (2 * torch.randn(T + 3, hq, hd, generator=g)).to(TYPES[dtype])
+    starts = _starts(rows)
+    d, _ = _gpu(cache)
+    table = torch.full((len(lens), 16384), -1, dtype=torch.int32, device="cuda")
+    table[:, :d["table"].shape[1]] = d["table"]
+    c = fdllm.Kv8Cache(d["k"], d["v"], d["k_scale"], d["v_scale"], table)
+    out = torch.full((T + 3, hq, hd), 7.0, dtype=q.dtype, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    fdllm.fdllm_kv8_attention(c, q.cuda(), _i32(starts), _i32(lens), out=out, status=status)
+    assert status.item() == 0
+    _check_attention(cache, q, starts, lens, hd ** -0.5, out, sentinel=7.0)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 def test_attention_strided_rows_and_starts_offset(dtype):
     """q is a slice of a fused projection, out a slice of a wider buffer, the
     first sequence does not start at row 0."""
@@ -401,6 +425,42 @@ def test_other_stream_and_captured_graph():
         want = step()
         torch.cuda.synchronize()
         assert torch.equal(got, want) and torch.equal(got_k, d["k"])
+
+
+def test_stream_argument():
+    """Calls enqueued on another stream than torch's current one, by its
+    handle: results, and workspaces, of the calls before are not handed out to
+    the current stream while the other one still works with them."""
+    g = torch.Generator().manual_seed(14)
+    lens = [20000]
+    cache = kv8_ref.make_cache(g, lens, 2, 64)
+    _, c = _gpu(cache)
+    q = torch.randn(8, 4, 64, generator=g).to(torch.bfloat16).cuda()
+    logits = torch.randn(8, 5000, generator=g).cuda()
+    u = torch.rand(8, generator=g, dtype=torch.float64).cuda()
+    starts, dl = _i32([0, 8]), _i32(lens)
+    want, want_tok = fdllm.fdllm_kv8_attention(c, q, starts, dl), fdllm.fdllm_sample(logits, u)[0]
+    for s in (torch.cuda.Stream(), torch.cuda.current_stream(), torch.cuda.default_stream()):
+        s.wait_stream(torch.cuda.current_stream())
+        for _ in range(20):
+            got = fdllm.fdllm_kv8_attention(c, q, starts, dl, stream=s.cuda_stream)
+            tok, _ = fdllm.fdllm_sample(logits, u, stream=s.cuda_stream)
+            torch.full((1 << 20,), 3.0, device="cuda")   # scribbles over freed memory of the current stream
+        torch.cuda.current_stream().wait_stream(s)
+        assert torch.equal(got, want) and torch.equal(tok, want_tok)
+
+
+def test_integers_beyond_32_bits_are_refused():
+    cache = kv8_ref.make_cache(torch.Generator().manual_seed(0), [64], 1, 64)
+    _, c = _gpu(cache)
+    q = torch.zeros(1, 1, 64, device="cuda")
+    for kw in (dict(max_q=1 << 32), dict(max_len=-(1 << 40))):
+        with pytest.raises(ValueError, match="32 bits"):
+            fdllm.fdllm_kv8_attention(c, q, _i32([0, 1]), _i32([9]), **kw)
+    with pytest.raises(ValueError, match="32 bits"):
+        fdllm.fdllm_kv8_append(c, q, q, _i32([0, 1]), _i32([9]), max_new=1 << 32)
+    with pytest.raises(ValueError, match="32 bits"):
+        fdllm.fdllm_sample(q[0], torch.zeros(1, dtype=torch.float64, device="cuda"), mask_id=1 << 32)
 
 
 def test_results_do_not_depend_on_timing():
