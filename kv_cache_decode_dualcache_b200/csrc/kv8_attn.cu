@@ -1,9 +1,18 @@
 // fdllm_kv8_attention, and its kernel for up to 16 query rows a run (and for
-// float32): attention over the 8-bit paged K/V cache on mma.sync.
+// more rows of short work, see plan): attention over the 8-bit paged K/V cache
+// on mma.sync.
 //
 // With few rows the kernel streams the cache, and operands that go straight
 // to registers spare the round trip through shared memory and TMEM that a
-// converted tile would take (kv8_attn_tc.cu takes it for more rows).  A CTA's
+// converted tile would take (kv8_attn_tc.cu takes it for more rows).
+//
+// Bound: 64 sequences' tokens over up to 8192 keys (4 K/V heads of 128 dims, 281
+// MB) take 77 us, 3.7 TB/s: 8 warps an SM with 2 stages in flight each wait for
+// instructions of their own chain (933 a tile of 32 keys) as much as for memory;
+// more warps do not fit the accumulators' registers (234 a thread).  A lone token
+// over 512 keys takes 9.5 us, a chain of latencies: the lengths (1.2), page ids
+// (0.8), q (0.8), the tile (1.3), the warps' exchange (0.8), the join's launch.
+//  A CTA's
 // 4 warps take its part of a run in tiles of 32 keys, every warp with a ring
 // of cp.async stages, softmax statistics and an output accumulator of its
 // own, so the loop has no barrier beyond the warp's; the warps' results meet
@@ -443,20 +452,34 @@ struct Plan {
   size_t bytes;
 };
 
-// Rows of a tile and the number of shares.  Up to 16 rows a K/V head, for
-// float32 and for heads of 32 dims: the kernel above; else kv8_attn_tc.cu.
+// The kernel, the rows of its tile and the number of shares.  Up to 16 rows a
+// K/V head, for float32 and for heads of 32 dims: the kernel above.  For more
+// rows, kv8_attn_tc.cu takes a page once for all of them but starts and ends
+// more slowly; a share of w pages (run starts counted in) takes about 12 + w
+// us above and 20 + 1.5 w us there.  Measured here / there: 32 rows, 32 K/V heads,
+// 2048 keys 20 / 24 us, 16 such sequences of up to 1280 keys 64 / 56 us; 56 rows,
+// 4 heads, 8192 keys 21 / 33 us, 64 such sequences of up to 4096 keys 132 / 93 us.
 Plan plan(const fdllm_kv8& c, const fdllm_kv8_attention_args& a, int num_sms) {
-  Plan p{};
   const int64_t most_q = a.max_q > 0 ? std::min(a.max_q, a.n_tokens) : a.n_tokens;
   const int64_t rows = std::max<int64_t>(1, most_q * (a.n_heads / c.n_kv_heads));
-  const bool tc = rows > R && a.dtype != FDLLM_DTYPE_F32 && c.head_dim >= 64;
-  p.tile_rows = tc ? tc_tile_rows(rows) : R;
   const int64_t table = (int64_t)c.max_pages * PAGE;
   const int64_t len = std::max<int64_t>(1, a.max_len > 0 ? std::min<int64_t>(a.max_len, table) : table);
-  const double pages = (double)c.n_seqs * c.n_kv_heads * ((rows + p.tile_rows - 1) / p.tile_rows) *
-                       (RUN_START + (len + PAGE - 1) / PAGE);
-  const double most = (tc ? tc_ctas_per_sm(p.tile_rows) : 2) * (double)num_sms;
-  p.n_cta = (int)std::min(most, std::ceil(pages / MIN_PAGES));
+  double pages = 0, share = 0;
+  Plan p{};
+  auto with = [&](int tile_rows, int ctas) {
+    pages = (double)c.n_seqs * c.n_kv_heads * ((rows + tile_rows - 1) / tile_rows) *
+            (RUN_START + (len + PAGE - 1) / PAGE);
+    p.tile_rows = tile_rows;
+    p.n_cta = (int)std::min(ctas * (double)num_sms, std::ceil(pages / MIN_PAGES));
+    share = pages / p.n_cta;
+  };
+  with(R, 2);
+  if (rows > R && a.dtype != FDLLM_DTYPE_F32 && c.head_dim >= 64) {
+    const double mma = 12.0 + share;
+    const int tile_rows = tc_tile_rows(rows);
+    with(tile_rows, tc_ctas_per_sm(tile_rows));
+    if (mma < 20.0 + 1.5 * share) with(R, 2);
+  }
   p.bytes = p.n_cta > 1 ? (size_t)p.n_cta * 2 * p.tile_rows * (c.head_dim + 2) * sizeof(float) : 0;
   return p;
 }

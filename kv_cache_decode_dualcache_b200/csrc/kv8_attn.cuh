@@ -277,26 +277,58 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) kv8_join_kernel(const AttnP P
   pdl_wait();   // by every block: this grid must not end before the one that feeds it
   if (!mine || rr >= sq.rows) return;
   auto piece = [&](int i) { return ((c - 1 + i) * 2 + (i == 0)) * R + r; };
+  // a lane holds the (max, sum) of one of 32 pieces, and V consecutive dims
+  constexpr int V = HD / 32;
   float mx = -INFINITY;
   for (int i = lane; i < n; i += 32) mx = fmaxf(mx, P.part_ml[piece(i)].x);
   mx = warp_max(mx);
-  float sum = 0.0f, acc[HD / 32];
+  float sum = 0.0f, acc[V];
 #pragma unroll
-  for (int i = 0; i < HD / 32; ++i) acc[i] = 0.0f;
-#pragma unroll 8
-  for (int i = 0; i < n; ++i) {
-    const float2 ml = P.part_ml[piece(i)];
-    const float f = ml.x == -INFINITY ? 0.0f : ex2(ml.x - mx);
-    sum = fmaf(ml.y, f, sum);
-    const float* po = P.part_o + piece(i) * HD;
+  for (int j = 0; j < V; ++j) acc[j] = 0.0f;
+  for (int i0 = 0; i0 < n; i0 += 32) {
+    float f = 0.0f;
+    if (i0 + lane < n) {
+      const float2 ml = P.part_ml[piece(i0 + lane)];
+      f = ml.x == -INFINITY ? 0.0f : ex2(ml.x - mx);
+      sum = fmaf(ml.y, f, sum);
+    }
+    const int m = min(32, n - i0);
+#pragma unroll 1
+    for (int i = 0; i < m; i += 8) {   // 8 loads in flight
+      float x[8][V];
 #pragma unroll
-    for (int j = 0; j < HD / 32; ++j) acc[j] = fmaf(po[j * 32 + lane], f, acc[j]);
+      for (int k = 0; k < 8; ++k) {
+        if (i + k >= m) break;
+        const float* po = P.part_o + piece(i0 + i + k) * HD + lane * V;
+        if constexpr (V == 4) {
+          load4(po, x[k]);
+        } else if constexpr (V == 2) {
+          const float2 u = *reinterpret_cast<const float2*>(po);
+          x[k][0] = u.x;
+          x[k][1] = u.y;
+        } else {
+          x[k][0] = *po;
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        if (i + k >= m) break;
+        const float w = __shfl_sync(0xffffffffu, f, i + k);
+#pragma unroll
+        for (int j = 0; j < V; ++j) acc[j] = fmaf(x[k][j], w, acc[j]);
+      }
+    }
   }
+  sum = warp_sum(sum);
   const float inv = mx == -INFINITY ? 0.0f : 1.0f / sum;
   T* dst = reinterpret_cast<T*>(a.out) + (int64_t)(sq.r_lo + rr / rep) * a.out_strides[0] +
-           (int64_t)(g * rep + rr % rep) * a.out_strides[1];
+           (int64_t)(g * rep + rr % rep) * a.out_strides[1] + lane * V;
+  if constexpr (V == 4) {
+    store4(dst, acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv);
+  } else {
 #pragma unroll
-  for (int j = 0; j < HD / 32; ++j) dst[j * 32 + lane] = from_f<T>(acc[j] * inv);
+    for (int j = 0; j < V; ++j) dst[j] = from_f<T>(acc[j] * inv);
+  }
 }
 
 template <typename T, int HD, int R>
