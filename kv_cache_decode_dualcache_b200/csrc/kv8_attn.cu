@@ -7,10 +7,10 @@
 // converted tile would take (kv8_attn_tc.cu takes it for more rows).
 //
 // Bound: 64 sequences' tokens over up to 8192 keys (4 K/V heads of 128 dims, 281
-// MB) take 77 us, 3.7 TB/s: 8 warps an SM with 2 stages in flight each wait for
+// MB) take 70 us, 4.0 TB/s: 8 warps an SM with 2 stages in flight each wait for
 // instructions of their own chain (933 a tile of 32 keys) as much as for memory;
 // more warps do not fit the accumulators' registers (234 a thread).  A lone token
-// over 512 keys takes 9.5 us, a chain of latencies: the lengths (1.2), page ids
+// over 512 keys takes 9.1 us, a chain of latencies: the lengths (1.2), page ids
 // (0.8), q (0.8), the tile (1.3), the warps' exchange (0.8), the join's launch.
 //  A CTA's
 // 4 warps take its part of a run in tiles of 32 keys, every warp with a ring
@@ -457,8 +457,8 @@ struct Plan {
 // rows, kv8_attn_tc.cu takes a page once for all of them but starts and ends
 // more slowly; a share of w pages (run starts counted in) takes about 12 + w
 // us above and 20 + 1.5 w us there.  Measured here / there: 32 rows, 32 K/V heads,
-// 2048 keys 20 / 24 us, 16 such sequences of up to 1280 keys 64 / 56 us; 56 rows,
-// 4 heads, 8192 keys 21 / 33 us, 64 such sequences of up to 4096 keys 132 / 93 us.
+// 2048 keys 20 / 24 us, 16 such sequences of up to 1280 keys 61 / 53 us; 56 rows,
+// 4 heads, 8192 keys 21 / 33 us, 64 such sequences of up to 4096 keys 127 / 84 us.
 Plan plan(const fdllm_kv8& c, const fdllm_kv8_attention_args& a, int num_sms) {
   const int64_t most_q = a.max_q > 0 ? std::min(a.max_q, a.n_tokens) : a.n_tokens;
   const int64_t rows = std::max<int64_t>(1, most_q * (a.n_heads / c.n_kv_heads));

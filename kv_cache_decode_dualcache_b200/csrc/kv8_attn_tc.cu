@@ -27,6 +27,14 @@
 // need L1 lines, spills go to L2); hence the bulk copies, and 64-key tiles,
 // whose scores fit a thread's registers.
 //
+// Bound: 224 rows (32 tokens, 28 heads on 4) over 131072 keys take 119 us, 505
+// TF/s: 1.4 us for a tile's 64 keys, of which its products are 0.73 at the rate of
+// a large library product; the rest is the softmax's chain (scores out of TMEM,
+// weights back, barriers).  16 sequences' blocks of 32 rows over up to 1280 keys
+// (32 K/V heads, 64 MB) take 53 us: 1.25 us a tile and CTA, which is the
+// converters' chain (unit, free tile, stores), 5.5 us to the first tile and about 6
+// us a run for q and the output.
+//
 // Every wait is bounded (WAIT_LIMIT_NS); a role whose wait ran out keeps
 // walking its loops without waiting or touching TMEM, so that all barriers
 // are still met, and FDLLM_KV8_TIMEOUT is reported.
