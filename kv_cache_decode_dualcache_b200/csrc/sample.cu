@@ -10,8 +10,8 @@
 // id).  Usually a small superset of them is known early: min-p bounds
 // z = (m - l) / T; the top_k-th largest of the threads' own maxima bounds the
 // top_k-th token; a histogram of the weights bounds the nucleus.  Then the
-// superset is gathered (at most CAP tokens), sorted by one CTA, and the
-// filters and the draw are prefix sums.  Larger kept sets are described by
+// superset is gathered (at most CAP tokens), ordered by one CTA (by counting,
+// or a sort if it is large), and the filters and the draw are prefix sums.  Larger kept sets are described by
 // a cut, the last kept token, found on counts (top-k) or weight sums (top-p)
 // by a histogram over 256 linear bins of z in [0, 32) (a token beyond weighs
 // under 2^-45 and cannot be drawn), one over 256 bins of the bin the cut
@@ -25,8 +25,11 @@
 // in float64: sums of up to 2^18 weights are exact in 64 bits, so no order
 // of additions can change a cut or a token.
 //
-// Bound: the logits' bytes for many rows; for few rows the chain of cluster
-// barriers.
+// Bound: for few rows the chain of cluster barriers (one row of 152064 float32
+// logits, all filters: 12 us); for many rows too, for a row's chain (maximum,
+// bound, gathered tokens, their order) takes 15 to 25 us of a CTA and an SM holds
+// two or three (512 rows of 126464 bf16 logits: 130 us, 1.0 TB/s, the last rows
+// being wide nuclei of 60 us each; 32 rows of float32 with wide nuclei: 35 us).
 #include <algorithm>
 #include <type_traits>
 
@@ -46,7 +49,10 @@ constexpr int SLICE_BYTES = 78 << 10;        // two CTAs and their lists fit on 
 constexpr int BINS = 256;
 constexpr float Z_BINS = 8.0f;               // bins per unit of z: 256 / 32
 constexpr int CAP = 1024;                    // tokens that are gathered and sorted
-constexpr int DIRECT = 192;                  // tokens whose order is taken by counting
+// Tokens whose order is taken by counting, which keeps all warps busy where the
+// steps of a sort wait for one another: 37 rows with about 250 tokens 31 us, 36 us
+// sorted; no gain above.
+constexpr int DIRECT = 384;
 constexpr double W_ONE = 17592186044416.0;   // 2^44
 
 typedef unsigned long long u64;
@@ -595,22 +601,30 @@ FD_DEV void draw_sorted(Shared& s, const Row& r, const Filters& f, int n, u64 ne
                         int32_t* tok, float* prob) {
   const int tid = threadIdx.x;
   if (n <= DIRECT) {
-    // token tid: its rank and the weight before it in the order, then in the ids
-    const bool have = tid < n;
-    const u64 o = have ? s.all[tid] : 0;
-    const float l = have ? order_logit(o) : r.m;
-    const double wd = weight(r, l);
+    // `per` threads a token count its rank and the weight before it
+    int per = 1;
+    while (2 * per * n <= ST && per < 8) per *= 2;
+    const int t = tid / per, part = tid % per;
+    const bool have = t < n;
+    const u64 o = have ? s.all[t] : 0;
+    const double wd = weight(r, have ? order_logit(o) : r.m);
     u64 w = have ? fixed(wd) : 0;
-    if (have) s.w[tid] = w;
+    if (have && part == 0) s.w[t] = w;
     __syncthreads();
     int rank = 0;
     u64 before = 0;
     if (have)
-      for (int i = 0; i < n; ++i)
+#pragma unroll 4
+      for (int i = part; i < n; i += per)
         if (s.all[i] > o) {
           ++rank;
           before += s.w[i];
         }
+    for (int d = per / 2; d > 0; d /= 2) {
+      rank += __shfl_xor_sync(0xffffffffu, rank, d);
+      before += __shfl_xor_sync(0xffffffffu, before, d);
+    }
+    if (part > 0) w = 0;   // the first of a token's threads stands for it in the sums
     if (f.top_k > 0 && rank >= f.top_k) w = 0;
     if (!(f.top_p >= 1.0)) {
       const u64 total = need ? 0 : block_sum(w, s);
@@ -619,19 +633,33 @@ FD_DEV void draw_sorted(Shared& s, const Row& r, const Filters& f, int n, u64 ne
     }
     if (f.min_p > 0.0 && wd < f.min_p) w = 0;
     const u64 all = block_sum(w, s);   // every thread has read s.w
-    if (have) s.w[tid] = w;
-    __syncthreads();
-    bool mine = f.greedy && have && rank == 0;
-    if (!f.greedy && w) {
-      const u64 target = min((u64)(fmax(u, 0.0) * (double)all), all - 1);
-      u64 lower = 0;
-      for (int i = 0; i < n; ++i)
-        if ((uint32_t)s.all[i] > (uint32_t)o) lower += s.w[i];   // low words: ~id
-      mine = lower <= target && target < lower + w;
+    if (f.greedy) {
+      if (have && part == 0 && rank == 0) {
+        *tok = order_id(o);
+        if (prob) *prob = (float)(wd / ((double)all / W_ONE));
+      }
+      return;
     }
-    if (mine) {
-      *tok = order_id(o);
-      if (prob) *prob = (float)(wd / ((double)all / W_ONE));
+    // the kept tokens, ranks 0 .. kept - 1, once more: the weight of lower ids
+    if (w) {
+      s.list[rank] = o;
+      s.w[rank] = w;
+    }
+    const int kept = __syncthreads_count(w > 0);
+    per = 1;
+    while (2 * per * kept <= ST && per < 32) per *= 2;
+    const int t2 = tid / per, part2 = tid % per;
+    const u64 target = min((u64)(fmax(u, 0.0) * (double)all), all - 1);
+    const uint32_t low = t2 < kept ? (uint32_t)s.list[t2] : 0;   // ~id
+    u64 lower = 0;
+    if (t2 < kept)
+#pragma unroll 4
+      for (int i = part2; i < kept; i += per)
+        if ((uint32_t)s.list[i] > low) lower += s.w[i];
+    for (int d = per / 2; d > 0; d /= 2) lower += __shfl_xor_sync(0xffffffffu, lower, d);
+    if (t2 < kept && part2 == 0 && lower <= target && target < lower + s.w[t2]) {
+      *tok = order_id(s.list[t2]);
+      if (prob) *prob = (float)(weight(r, order_logit(s.list[t2])) / ((double)all / W_ONE));
     }
     return;
   }
