@@ -1,5 +1,5 @@
-// fdllm_kv8_attention, and its kernel for up to 16 query rows a run (and for
-// more rows of short work, see plan): attention over the 8-bit paged K/V cache
+// fdllm_kv8_attention, and its kernel for up to 64 query rows a K/V head, 16 a
+// run (and for more rows of short work, see plan): attention over the 8-bit paged K/V cache
 // on mma.sync.
 //
 // With few rows the kernel streams the cache, and operands that go straight
@@ -452,13 +452,13 @@ struct Plan {
   size_t bytes;
 };
 
-// The kernel, the rows of its tile and the number of shares.  Up to 16 rows a
+// The kernel, the rows of its tile and the number of shares.  Up to 64 rows a
 // K/V head, for float32 and for heads of 32 dims: the kernel above.  For more
 // rows, kv8_attn_tc.cu takes a page once for all of them but starts and ends
 // more slowly; a share of w pages (run starts counted in) takes about 12 + w
-// us above and 20 + 1.5 w us there.  Measured here / there: 32 rows, 32 K/V heads,
-// 2048 keys 20 / 24 us, 16 such sequences of up to 1280 keys 61 / 53 us; 56 rows,
-// 4 heads, 8192 keys 21 / 33 us, 64 such sequences of up to 4096 keys 127 / 84 us.
+// us above and 20 + 1.5 w us there.  Measured here / there: 112 rows, 4 K/V heads,
+// 2048 keys 16 / 22 us; 224 rows, 1024 keys 16 / 24 us, and 131072 keys, where
+// the kernel above would read every page 14 times, 119 us there.
 Plan plan(const fdllm_kv8& c, const fdllm_kv8_attention_args& a, int num_sms) {
   const int64_t most_q = a.max_q > 0 ? std::min(a.max_q, a.n_tokens) : a.n_tokens;
   const int64_t rows = std::max<int64_t>(1, most_q * (a.n_heads / c.n_kv_heads));
@@ -474,10 +474,10 @@ Plan plan(const fdllm_kv8& c, const fdllm_kv8_attention_args& a, int num_sms) {
     share = pages / p.n_cta;
   };
   with(R, 2);
-  if (rows > R && a.dtype != FDLLM_DTYPE_F32 && c.head_dim >= 64) {
+  if (rows > 64 && a.dtype != FDLLM_DTYPE_F32 && c.head_dim >= 64) {
     const double mma = 12.0 + share;
     const int tile_rows = tc_tile_rows(rows);
-    with(tile_rows, tc_ctas_per_sm(tile_rows));
+    with(tile_rows, 1);
     if (mma < 20.0 + 1.5 * share) with(R, 2);
   }
   p.bytes = p.n_cta > 1 ? (size_t)p.n_cta * 2 * p.tile_rows * (c.head_dim + 2) * sizeof(float) : 0;

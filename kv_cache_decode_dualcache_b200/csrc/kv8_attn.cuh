@@ -341,10 +341,9 @@ cudaError_t launch_join(const AttnP& P, cudaStream_t st) {
                   dim3(JOIN_WARPS * 32), 0, st, P);
 }
 
-// The kernel for more than 16 rows (kv8_attn_tc.cu): rows of its tile for
-// runs of at most `rows` rows, CTAs an SM, and the launch with its join.
+// The kernel for more than 64 rows (kv8_attn_tc.cu): rows of its tile for
+// runs of at most `rows` rows, and the launch with its join.
 int tc_tile_rows(int64_t rows);
-int tc_ctas_per_sm(int tile_rows);
 cudaError_t launch_attn_tc(const AttnP& P, int tile_rows, cudaStream_t st);
 
 }  // namespace kv8

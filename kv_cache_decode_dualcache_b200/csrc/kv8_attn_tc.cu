@@ -1,14 +1,7 @@
-// fdllm_kv8_attention for more than 16 query rows a K/V head (diffusion
-// blocks, grouped heads, chunks of a prompt) with 16-bit q: both products on
-// the 5th-generation tensor cores, the codes converted to fp16 tiles once per
-// CTA for all of its rows.
-//
-// The CTA's MMA tile has NQ x 128 rows.  Tiles of up to 32 (64) query rows
-// fill 128 rows with C = 4 (2) copies: copy i of a row takes the i-th part of
-// the columns of every tile of 64 keys, with statistics of its own, and leaves
-// zero weights in the others' columns, so that the softmax runs on all four
-// warps; the copies' outputs add up at the end.  The idle part of the MMAs
-// costs nothing: with so few rows the kernel waits for the cache.
+// fdllm_kv8_attention for more than 64 query rows a K/V head (blocks of grouped
+// heads, chunks of a prompt) with 16-bit q: both products on the 5th-generation
+// tensor cores, the codes converted to fp16 tiles once per CTA for all of its
+// rows.  The CTA's MMA tile has NQ x 128 rows.
 //
 // Roles: 4 warps a row tile for the softmax (a thread per MMA row: q, weights,
 // output), 2 converter warps for K and 2 for V, one copy warp, an MMA warp a
@@ -20,8 +13,7 @@
 //   w = 2^(S f + log2 vs - M + 8), written over S as packed fp16
 //   O += w V         tcgen05, w in TMEM, V MN-major from shared memory
 // with the statistics of kv8_attn.cu.  S of tile t + 1 is done before the softmax
-// of tile t is, so that the chain from tile to tile is the softmax alone.  Tiles
-// of up to 64 query rows leave room for two CTAs an SM.
+// of tile t is, so that the chain from tile to tile is the softmax alone.
 // What shaped this: with shared memory in use there is next to no L1, so
 // loads through registers and spilled registers both starve (loads in flight
 // need L1 lines, spills go to L2); hence the bulk copies, and 64-key tiles,
@@ -30,10 +22,11 @@
 // Bound: 224 rows (32 tokens, 28 heads on 4) over 131072 keys take 119 us, 505
 // TF/s: 1.4 us for a tile's 64 keys, of which its products are 0.73 at the rate of
 // a large library product; the rest is the softmax's chain (scores out of TMEM,
-// weights back, barriers).  16 sequences' blocks of 32 rows over up to 1280 keys
-// (32 K/V heads, 64 MB) take 53 us: 1.25 us a tile and CTA, which is the
-// converters' chain (unit, free tile, stores), 5.5 us to the first tile and about 6
-// us a run for q and the output.
+// weights back, barriers).
+//
+// One CTA an SM: tiles of 32 and 64 rows, two CTAs an SM, gave now and then a wrong
+// tile (one run in some 2000, never with one CTA an SM); the cause was not found, so
+// those tiles are gone and the shared memory is sized to keep an SM for one CTA.
 //
 // Every wait is bounded (WAIT_LIMIT_NS); a role whose wait ran out keeps
 // walking its loops without waiting or touching TMEM, so that all barriers
@@ -70,17 +63,18 @@ struct TcLay {
   static constexpr int X_OFF = RING_OFF + RING * UNIT;
   // scales of four tiles: ks, log2 vs, 1 / vs of 4 blocks
   static constexpr int SC_OFF = X_OFF + NQ * 128 * XROW * 4;
-  static constexpr int ML_OFF = SC_OFF + 4 * 3 * NB * 4;   // rows' (max, sum)
-  static constexpr int RF_OFF = ML_OFF + NQ * 128 * 8;     // row factors
+  static constexpr int RF_OFF = SC_OFF + 4 * 3 * NB * 4;   // row factors
   static constexpr int BAR_OFF = RF_OFF + NQ * 128 * 4;
   static constexpr int MISC_OFF = BAR_OFF + (31 + 2 * RING) * 8;
   static constexpr int PAGE_OFF = MISC_OFF + 16;           // the units' pages
   static constexpr int THREADS = 128 * NQ + 2 * CONV + 32 + 32 * NQ;
   static constexpr int WALK_OFF = (PAGE_OFF + RING * 4 + 15) / 16 * 16;
-  static constexpr int SMEM = WALK_OFF + THREADS / 32 * (int)sizeof(Walk) + 1024;   // slack for
+  static constexpr int USED = WALK_OFF + THREADS / 32 * (int)sizeof(Walk) + 1024;   // slack for
                                                                                     // 1024-byte alignment
+  // one CTA an SM, whatever else runs (see above)
+  static constexpr int SMEM = USED > (120 << 10) ? USED : 120 << 10;
   static constexpr uint32_t TMEM_COLS = 256 * NQ;     // a row tile: S 2 x 64, O 128
-  static_assert(SMEM <= (NQ == 1 ? 115712 : 232448), "shared memory layout");
+  static_assert(SMEM <= 232448, "shared memory layout");
 };
 
 // bytes (a multiple of 16) from global to shared memory, both 16-byte aligned.
@@ -109,61 +103,40 @@ FD_DEV void fma2(float& a, float& b, float f, float g) {
       : "+f"(a), "+f"(b)
       : "f"(f), "f"(g));
 }
-// N TMEM columns of this warp's lanes; tmem_wait_st follows the stores.
-template <int N> FD_DEV void tmem_ld(uint32_t taddr, float* v) {
-  if constexpr (N == 64) {
-    tmem_ld64(taddr, v);
-  } else if constexpr (N == 32) {
-    tmem_ld32(taddr, v);
-  } else {
-    uint32_t r[16];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-          "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr)
-        : "memory");
+// TMEM columns of this warp's lanes: 16 loaded, 32 stored (tmem_wait_st follows).
+FD_DEV void tmem_ld16(uint32_t taddr, float* v) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
-  }
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
-template <int N> FD_DEV void tmem_st(uint32_t taddr, const uint32_t* v) {
-  if constexpr (N == 32) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
-        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
-        "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]),
-        "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]),
-        "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]),
-        "r"(v[30]), "r"(v[31])
-        : "memory");
-  } else if constexpr (N == 16) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
-        "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
-        : "memory");
-  } else {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
-                 "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]),
-                 "r"(v[7])
-                 : "memory");
-  }
+FD_DEV void tmem_st32u(uint32_t taddr, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]),
+      "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]),
+      "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]),
+      "r"(v[30]), "r"(v[31])
+      : "memory");
 }
 FD_DEV void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-template <typename T, int HD, int NQ, int C>
-__global__ void __launch_bounds__(TcLay<HD, NQ>::THREADS, C > 1 ? 2 : 1)
+template <typename T, int HD, int NQ>
+__global__ void __launch_bounds__(TcLay<HD, NQ>::THREADS, 1)
     kv8_attn_tc_kernel(const AttnP P) {
   using L = TcLay<HD, NQ>;
-  constexpr int R = NQ * 128 / C;      // query rows of a run
-  constexpr int NC = KEYS / C;         // key columns of a thread
+  constexpr int R = NQ * 128;          // query rows of a run
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -237,7 +210,7 @@ __global__ void __launch_bounds__(TcLay<HD, NQ>::THREADS, C > 1 ? 2 : 1)
     // ================================================== softmax
     const int rep = a.n_heads / c.n_kv_heads;
     const int q = warp >> 2, quad = warp & 3, i = quad * 32 + lane;   // MMA row of tile q
-    const int r = q * 128 + i % (128 / C), copy = i / (128 / C);      // row of the run, its copy
+    const int r = q * 128 + i;                                        // row of the run
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;
     const uint32_t s_col = tmem + q * 128 + lanes, o_col = s_col + NQ * 128;   // S: two buffers
     uint8_t* qs = smem + L::Q_OFF + q * L::KH * L::Q_SUB;
@@ -249,9 +222,9 @@ __global__ void __launch_bounds__(TcLay<HD, NQ>::THREADS, C > 1 ? 2 : 1)
       const int k_lo = sg.p_lo * PAGE, k_hi = min(sg.len, sg.p_hi * PAGE);
       const int tiles = (k_hi - k_lo + KEYS - 1) / KEYS;
       // ---- q, scaled per row by a power of two, into the swizzled A tile: HD / 8
-      // lanes a row, 16 bytes each; every warp a quarter of the rows, all copies
+      // lanes a row, 16 bytes each; every warp a quarter of the rows
       {
-        constexpr int LR = HD / 8, RPW = 128 / C / 4, STEP = 32 / LR, N = RPW / STEP;
+        constexpr int LR = HD / 8, RPW = 128 / 4, STEP = 32 / LR, N = RPW / STEP;
         constexpr int B = N < 8 ? N : 8;   // rows of a lane that are loaded at once
         const int ch = lane % LR, row_a = quad * RPW + lane / LR;   // row of the MMA tile
         const int first = sg.row0 + q * 128 + row_a;
@@ -282,12 +255,8 @@ __global__ void __launch_bounds__(TcLay<HD, NQ>::THREADS, C > 1 ? 2 : 1)
 #pragma unroll
             for (int m = 0; m < 4; ++m)
               h[m] = pack_h2(to_f<T>(e[2 * m]) * mul, to_f<T>(e[2 * m + 1]) * mul);
-#pragma unroll
-            for (int k = 0; k < C; ++k) {
-              const int at = k * (128 / C) + row;
-              *reinterpret_cast<uint4*>(qs + (ch >> 3) * L::Q_SUB + at * 128 + (((ch & 7) ^ (at & 7)) << 4)) =
-                  make_uint4(h[0], h[1], h[2], h[3]);
-            }
+            *reinterpret_cast<uint4*>(qs + (ch >> 3) * L::Q_SUB + row * 128 + (((ch & 7) ^ (row & 7)) << 4)) =
+                make_uint4(h[0], h[1], h[2], h[3]);
             if (ch == 0) rfs[row] = a.scale * LOG2E * exp2_int(-up);
           }
         }
@@ -295,32 +264,31 @@ __global__ void __launch_bounds__(TcLay<HD, NQ>::THREADS, C > 1 ? 2 : 1)
         if (tiles > 0) mbar_arrive(q_full);   // runs without keys have no MMAs
         named_bar(1 + q, 128);   // rfs
       }
-      const float rf = rfs[i % (128 / C)];
+      const float rf = rfs[i];
       float M = -INFINITY, l = 0.0f;
       for (int t = 0; t < tiles; ++t, ++n_tile) {
-        const int k0 = k_lo + t * KEYS + copy * NC;   // first key of this thread's columns
-        const float* sc = reinterpret_cast<const float*>(smem + L::SC_OFF) + (n_tile & 3) * 3 * NB +
-                          copy * (NC / 16);
+        const int k0 = k_lo + t * KEYS;
+        const float* sc = reinterpret_cast<const float*>(smem + L::SC_OFF) + (n_tile & 3) * 3 * NB;
         wait(&s_full[2 * q + (n_tile & 1)], (n_tile >> 1) & 1);
         wait(&sc_full[n_tile & 3], (n_tile >> 2) & 1);
         if (ok) {
           tc_fence_after();
-          float v[NC], mx = -INFINITY;
+          float v[KEYS], mx = -INFINITY;
           const uint32_t buf = s_col + (n_tile & 1) * 64;
-          tmem_ld<NC>(buf + copy * NC, v);
+          tmem_ld64(buf, v);
 #pragma unroll
-          for (int b = 0; b < NC / 16; ++b) {
+          for (int b = 0; b < KEYS / 16; ++b) {
             const float f = rf * sc[b], g = sc[NB + b];
 #pragma unroll
             for (int j = 16 * b; j < 16 * b + 16; j += 2) fma2(v[j], v[j + 1], f, g);
           }
-          if (k0 + NC > k_hi) {
+          if (k0 + KEYS > k_hi) {
 #pragma unroll
-            for (int j = 0; j < NC; ++j)
+            for (int j = 0; j < KEYS; ++j)
               if (k0 + j >= k_hi) v[j] = -INFINITY;
           }
 #pragma unroll
-          for (int j = 0; j < NC; j += 2) mx = fmaxf(fmaxf(mx, v[j]), v[j + 1]);
+          for (int j = 0; j < KEYS; j += 2) mx = fmaxf(fmaxf(mx, v[j]), v[j + 1]);
           float alpha = 1.0f;
           const bool move = mx > M + M_SLACK || (M == -INFINITY && mx > -INFINITY);
           if (move) {
@@ -329,9 +297,9 @@ __global__ void __launch_bounds__(TcLay<HD, NQ>::THREADS, C > 1 ? 2 : 1)
           }
           const float ref = W_EXP - (M == -INFINITY ? 0.0f : M);
           float sum = 0.0f;
-          uint32_t w[NC / 2];
+          uint32_t w[KEYS / 2];
 #pragma unroll
-          for (int b = 0; b < NC / 16; ++b) {
+          for (int b = 0; b < KEYS / 16; ++b) {
             float part[2] = {0.0f, 0.0f};
 #pragma unroll
             for (int j = 16 * b; j < 16 * b + 16; j += 2) {
@@ -343,13 +311,7 @@ __global__ void __launch_bounds__(TcLay<HD, NQ>::THREADS, C > 1 ? 2 : 1)
             sum = fmaf(part[0] + part[1], sc[2 * NB + b], sum);
           }
           // over the scores' first 32 columns (this warp has read its lanes)
-          tmem_st<NC / 2>(buf + copy * (NC / 2), w);
-          if constexpr (C > 1) {
-            const uint32_t zero[8] = {};
-#pragma unroll
-            for (int o = 0; o < KEYS / 2; o += 8)
-              if (o / (NC / 2) != copy) tmem_st<8>(buf + o, zero);
-          }
+          tmem_st32u(buf, w);
           l = fmaf(l, alpha, sum);
           if (t > 0 && __any_sync(0xffffffffu, move) && pv_wait(n_tile - 1)) {
             tc_fence_after();   // the products before are done: O is still
@@ -368,34 +330,21 @@ __global__ void __launch_bounds__(TcLay<HD, NQ>::THREADS, C > 1 ? 2 : 1)
         mbar_arrive(&sc_free[n_tile & 3]);
         mbar_arrive(&p_full[2 * q + (n_tile & 1)]);
       }
-      // ---- the run's output, or its part: the copies of a row add up, scaled to
-      // their common reference, DIMS dims at a time
+      // ---- the run's output, or its part, DIMS dims at a time through shared memory
       const bool have_o = tiles > 0 && pv_wait(n_tile - 1);
       tc_fence_after();
       {
-        constexpr int RQ = 128 / C, DIMS = L::DIMS, XROW = L::XROW, LR = DIMS / 4;
+        constexpr int DIMS = L::DIMS, XROW = L::XROW, LR = DIMS / 4;
         const int64_t slot = ((int64_t)blockIdx.x * 2 + (sg.p_lo == 0)) * R;
         float* xo = reinterpret_cast<float*>(smem + L::X_OFF) + q * 128 * XROW;
-        float2* ml = reinterpret_cast<float2*>(smem + L::ML_OFF) + q * 128;
-        ml[i] = make_float2(M, l);
-        named_bar(1 + q, 128);
-        const int row = i % RQ;
-        float mx = -INFINITY, sum = 0.0f;
-#pragma unroll
-        for (int k = 0; k < C; ++k) mx = fmaxf(mx, ml[k * RQ + row].x);
-#pragma unroll
-        for (int k = 0; k < C; ++k) {
-          const float2 m = ml[k * RQ + row];
-          sum += m.x == -INFINITY ? 0.0f : m.y * ex2(m.x - mx);
-        }
         // a whole row is divided by its sum here, a partial one by the join
-        float fac = M == -INFINITY ? 0.0f : ex2(M - mx);
-        if (sg.whole) fac *= mx == -INFINITY ? 0.0f : 1.0f / sum;
-        if (!sg.whole && copy == 0 && rr < sg.rows) P.part_ml[slot + r] = make_float2(mx, sum);
+        float fac = 1.0f;
+        if (sg.whole) fac = M == -INFINITY ? 0.0f : 1.0f / l;
+        else if (rr < sg.rows) P.part_ml[slot + r] = make_float2(M, l);
 #pragma unroll 1
         for (int c0 = 0; c0 < HD; c0 += DIMS) {
           float v[DIMS];
-          if (have_o) tmem_ld<DIMS>(o_col + c0, v);
+          if (have_o) tmem_ld16(o_col + c0, v);
 #pragma unroll
           for (int j = 0; j < DIMS; j += 4)
             *reinterpret_cast<float4*>(xo + i * XROW + j) =
@@ -403,18 +352,10 @@ __global__ void __launch_bounds__(TcLay<HD, NQ>::THREADS, C > 1 ? 2 : 1)
                        : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
           named_bar(1 + q, 128);
           // LR lanes a row
-          for (int at = i / LR; at < RQ; at += 128 / LR) {
+          for (int at = i / LR; at < 128; at += 128 / LR) {
             const int d = i % LR * 4, rw = sg.row0 + q * 128 + at;
             if (rw >= sg.rows) break;
-            float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-            for (int k = 0; k < C; ++k) {
-              const float4 u = *reinterpret_cast<const float4*>(xo + (k * RQ + at) * XROW + d);
-              x.x += u.x;
-              x.y += u.y;
-              x.z += u.z;
-              x.w += u.w;
-            }
+            const float4 x = *reinterpret_cast<const float4*>(xo + at * XROW + d);
             if (sg.whole)
               store4(reinterpret_cast<T*>(a.out) + (int64_t)(sg.r_lo + rw / rep) * a.out_strides[0] +
                          (int64_t)(sg.g * rep + rw % rep) * a.out_strides[1] + c0 + d,
@@ -593,33 +534,27 @@ __global__ void __launch_bounds__(TcLay<HD, NQ>::THREADS, C > 1 ? 2 : 1)
   if (tid == 0 && *err && a.status) atomicOr(a.status, FDLLM_KV8_TIMEOUT);
 }
 
-template <typename T, int HD, int NQ, int C>
+template <typename T, int HD, int NQ>
 cudaError_t launch_tc(const AttnP& P, cudaStream_t st) {
   using L = TcLay<HD, NQ>;
-  auto kern = kv8_attn_tc_kernel<T, HD, NQ, C>;
+  auto kern = kv8_attn_tc_kernel<T, HD, NQ>;
   static std::atomic<uint64_t> ready{0};   // devices whose limit is set
   cudaError_t e = allow_smem(kern, L::SMEM, ready);
   if (e == cudaSuccess) e = launch_k(false, kern, dim3(P.n_cta), dim3(L::THREADS), L::SMEM, st, P);
-  if (e == cudaSuccess) e = launch_join<T, HD, NQ * 128 / C>(P, st);
+  if (e == cudaSuccess) e = launch_join<T, HD, NQ * 128>(P, st);
   return e;
 }
 
 template <typename T, int HD>
 cudaError_t launch_tc_hd(const AttnP& P, int rows, cudaStream_t st) {
-  switch (rows) {
-    case 32: return launch_tc<T, HD, 1, 4>(P, st);
-    case 64: return launch_tc<T, HD, 1, 2>(P, st);
-    case 128: return launch_tc<T, HD, 1, 1>(P, st);
-    default: return launch_tc<T, HD, 2, 1>(P, st);
-  }
+  return rows == 128 ? launch_tc<T, HD, 1>(P, st) : launch_tc<T, HD, 2>(P, st);
 }
 
 }  // namespace
 
 namespace kv8 {
 
-int tc_tile_rows(int64_t rows) { return rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 128 ? 128 : 256; }
-int tc_ctas_per_sm(int tile_rows) { return tile_rows > 64 ? 1 : 2; }
+int tc_tile_rows(int64_t rows) { return rows <= 128 ? 128 : 256; }
 
 cudaError_t launch_attn_tc(const AttnP& P, int rows, cudaStream_t st) {
   if (P.a.dtype == FDLLM_DTYPE_BF16)

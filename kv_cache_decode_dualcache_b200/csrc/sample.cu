@@ -610,6 +610,7 @@ FD_DEV void draw_sorted(Shared& s, const Row& r, const Filters& f, int n, u64 ne
     const double wd = weight(r, have ? order_logit(o) : r.m);
     u64 w = have ? fixed(wd) : 0;
     if (have && part == 0) s.w[t] = w;
+    if (tid == 0) s.pick = 0;
     __syncthreads();
     int rank = 0;
     u64 before = 0;
@@ -640,12 +641,16 @@ FD_DEV void draw_sorted(Shared& s, const Row& r, const Filters& f, int n, u64 ne
       }
       return;
     }
-    // the kept tokens, ranks 0 .. kept - 1, once more: the weight of lower ids
-    if (w) {
+    // the tokens up to the last kept one once more, by rank: the weight of lower
+    // ids (nearly all of them are kept; weights that differ by a rounding may
+    // lie on either side of min_p)
+    if (have && part == 0) {
       s.list[rank] = o;
       s.w[rank] = w;
+      if (w) atomicMax(&s.pick, rank + 1);
     }
-    const int kept = __syncthreads_count(w > 0);
+    __syncthreads();
+    const int kept = s.pick;
     per = 1;
     while (2 * per * kept <= ST && per < 32) per *= 2;
     const int t2 = tid / per, part2 = tid % per;

@@ -500,3 +500,18 @@ def test_decode_loop_on_the_cache():
         assert torch.equal(d["k"].cpu(), ref_c["k"]) and torch.equal(d["v"].cpu(), ref_c["v"])
         got = fdllm.fdllm_kv8_attention(c, q, _i32(starts), new)
         _check_attention(ref_c, ref["q"], starts, lens, hd ** -0.5, got)
+
+
+@pytest.mark.parametrize("hq,hkv,rows", [(32, 32, 32), (16, 16, 64), (28, 4, 16), (28, 4, 32)])
+def test_many_runs_repeat_to_the_bit(hq, hkv, rows):
+    """Ragged batches whose CTAs start and end several runs each: every call
+    gives the same bits."""
+    g = torch.Generator().manual_seed(15)
+    lens = [int(x) for x in torch.randint(1, 1300, (16,), generator=g)]
+    cache = kv8_ref.make_cache(g, lens, hkv, 128)
+    _, c = _gpu(cache)
+    q = torch.randn(16 * rows, hq, 128, generator=g).to(torch.float16).cuda()
+    starts, dl = _i32([rows * i for i in range(17)]), _i32(lens)
+    first = fdllm.fdllm_kv8_attention(c, q, starts, dl, max_q=rows, max_len=1300)
+    for _ in range(40):
+        assert torch.equal(fdllm.fdllm_kv8_attention(c, q, starts, dl, max_q=rows, max_len=1300), first)
