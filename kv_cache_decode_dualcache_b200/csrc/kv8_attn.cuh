@@ -12,8 +12,7 @@
 // partial result in the workspace (at most two a CTA: the end of one run,
 // slot 0, and the start of another, slot 1), and a second kernel joins those.
 // RUN_START 3 / 4 / 6 / 8: 64 sequences' tokens over up to 8192 keys 77 / 72 / 70
-// / 70 us, 16 blocks of 32 over up to 1280 keys 56 / 55 / 53 / 53, one block over
-// 2048 keys 19.7 / 19.3 / 19.8 / 19.8.
+// / 70 us, one block of 32 over 2048 keys 19.7 / 19.3 / 19.8 / 19.8.
 #pragma once
 
 #include <atomic>
