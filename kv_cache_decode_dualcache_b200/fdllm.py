@@ -464,7 +464,8 @@ class Kv8Cache:
 
     k, v: int8 [n_pages, n_kv_heads, 64, head_dim]; k_scale, v_scale: float32
     [n_pages, n_kv_heads, 4] (pages may be strided, e.g. slices of one pool
-    for all layers; k and v alike); page_table: int32 [n_seqs, max_pages]."""
+    for all layers; k and v alike); page_table: int32 [n_seqs, max_pages], its
+    rows side by side or apart, not expanded from one."""
 
     def __init__(self, k, v, k_scale, v_scale, page_table):
         import torch
@@ -482,6 +483,11 @@ class Kv8Cache:
         if page_table.dim() != 2 or page_table.dtype != torch.int32 or (
                 page_table.stride(1) != 1 and page_table.shape[1] > 1):
             raise ValueError("page_table must be int32 [n_seqs, max_pages] with contiguous rows")
+        # a stride of 0 would reach C as "dense", i.e. rows behind the storage
+        for name, t, row in (("k and v", k, heads * KV8_PAGE * hd), ("k_scale and v_scale", k_scale, heads * 4),
+                             ("page_table", page_table, page_table.shape[1])):
+            if t.shape[0] > 1 and t.stride(0) < row:
+                raise ValueError(f"rows of {name} overlap (an expanded tensor must be made contiguous)")
         self.device = k.get_device()
         if self.device < 0:
             raise ValueError("the cache must be on a CUDA device")

@@ -145,6 +145,28 @@ def test_binding_refuses_cpu_tensors_and_wrong_shapes():
         fdllm.fdllm_sample(torch.zeros(2, 5), torch.zeros(2, dtype=torch.float64))
 
 
+def test_overlapping_cache_rows_are_refused():
+    """An expanded page table (one context for several sequences), pool or scales
+    have a row stride of 0, which the C struct takes for dense rows: reads past
+    the storage.  Rows that overlap otherwise are refused alike."""
+    k, s = torch.zeros(3, 2, 64, 32, dtype=torch.int8), torch.zeros(3, 2, 4)
+    table = torch.zeros(4, 8, dtype=torch.int32)
+    wide = torch.zeros(100, dtype=torch.int32)
+    for over in (dict(table=table[:1].expand(4, -1)), dict(table=wide.as_strided((4, 8), (7, 1))),
+                 dict(table=wide[:1].as_strided((4, 1), (0, 0))),
+                 dict(k=k[:1].expand(3, -1, -1, -1), v=k[:1].expand(3, -1, -1, -1)),
+                 dict(ks=s[:1].expand(3, -1, -1), vs=s[:1].expand(3, -1, -1))):
+        a = dict(k=k, v=k, ks=s, vs=s, table=table) | over
+        with pytest.raises(ValueError, match="overlap"):
+            fdllm.Kv8Cache(*a.values())
+    # one row or page: its stride says nothing; rows that only touch are dense
+    for table in (wide[:8].expand(1, -1), wide.as_strided((4, 8), (8, 1)), wide.as_strided((4, 1), (1, 1))):
+        with pytest.raises(ValueError, match="CUDA"):
+            fdllm.Kv8Cache(k, k, s, s, table)
+    with pytest.raises(ValueError, match="CUDA"):
+        fdllm.Kv8Cache(k[:1].expand(1, -1, -1, -1), k[:1], s[:1], s[:1], wide[:8].view(1, 8))
+
+
 # ------------------------------------------------ the plain implementations
 def test_plain_append_keeps_values_within_half_a_step():
     g = torch.Generator().manual_seed(1)
