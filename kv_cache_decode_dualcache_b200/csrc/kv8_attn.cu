@@ -116,6 +116,9 @@ template <typename T, int HD, bool TWO>
 __global__ void __launch_bounds__(AT_WARPS * 32, 2) kv8_attn_kernel(const AttnP P) {
   using L_ = Lay<HD, TWO>;
   constexpr int NH = L_::NH, NW = L_::NW, CB = L_::CB, NTERM = TWO ? 2 : 1;
+  // With the mantissa of vs a factor of the weight, which may then be twice as
+  // large: 2^(W_EXP + SLACK) 2 stays below fp16's 65504.
+  constexpr float SLACK = TWO ? M_SLACK - 1.0f : M_SLACK;
   extern __shared__ __align__(16) uint8_t smem[];
   const fdllm_kv8& c = P.c;
   const fdllm_kv8_attention_args& a = P.a;
@@ -306,7 +309,7 @@ __global__ void __launch_bounds__(AT_WARPS * 32, 2) kv8_attn_kernel(const AttnP 
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
           alpha[hf] = 1.0f;
-          if (mx > M[hf] + M_SLACK || (M[hf] == -INFINITY && mx > -INFINITY)) {
+          if (mx > M[hf] + SLACK || (M[hf] == -INFINITY && mx > -INFINITY)) {
             alpha[hf] = ex2(M[hf] - mx);
             M[hf] = mx;
             moved = true;

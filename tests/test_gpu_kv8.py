@@ -155,6 +155,27 @@ def test_attention_peaked_and_uneven_scales():
             _check_attention(cache, q, [0, 4], lens, scale, got)
 
 
+@pytest.mark.parametrize("space", [True, False])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_attention_value_scales_just_below_a_power_of_two(dtype, space):
+    """Equal scores, value scales 1 and then 2^8 (1 - 2^-15) or so: the later
+    keys' weights pass the first reference by almost as much as it may be passed
+    before it moves, times a mantissa of almost 2.  The results are finite."""
+    g = torch.Generator().manual_seed(16)
+    for late in (255.99, 127.995, 2.0 - 2.0 ** -20, 511.98):
+        lens, hd = [192], 64
+        cache = kv8_ref.make_cache(g, lens, 1, hd)
+        pages = cache["table"][0, :3].long()
+        cache["v_scale"][pages] = 1.0
+        cache["v_scale"][pages[2], 0, :2] = late       # keys 128 .. 159
+        for q in (torch.zeros(3, 2, hd), torch.randn(3, 2, hd, generator=g) * 1e-3):
+            q = q.to(TYPES[dtype])
+            _, c = _gpu(cache)
+            ws = None if space else torch.empty(0, dtype=torch.uint8, device="cuda")
+            got = fdllm.fdllm_kv8_attention(c, q.cuda(), _i32([0, 3]), _i32(lens), workspace=ws)
+            _check_attention(cache, q, [0, 3], lens, hd ** -0.5, got)
+
+
 def test_attention_uses_the_codes_full_range():
     """A code of -128 (not one the append writes) reads as -128."""
     cache = kv8_ref.make_cache(torch.Generator().manual_seed(0), [1], 1, 32)
