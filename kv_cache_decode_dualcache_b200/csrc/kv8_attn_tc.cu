@@ -13,7 +13,10 @@
 //   w = 2^(S f + log2 vs - M + 8), written over S as packed fp16
 //   O += w V         tcgen05, w in TMEM, V MN-major from shared memory
 // with the statistics of kv8_attn.cu.  S of tile t + 1 is done before the softmax
-// of tile t is, so that the chain from tile to tile is the softmax alone.
+// of tile t is, so that the chain from tile to tile is the softmax alone.  Products
+// of different shape or accumulator have no order of their own in the PTX model,
+// so S of tile n + 2, whose buffer holds the weights of tile n, waits for pv_done
+// of n; only products into the same accumulator follow one another without a wait.
 // What shaped this: with shared memory in use there is next to no L1, so
 // loads through registers and spilled registers both starve (loads in flight
 // need L1 lines, spills go to L2); hence the bulk copies, and 64-key tiles,
@@ -494,6 +497,8 @@ __global__ void __launch_bounds__(TcLay<HD, NQ>::THREADS, 1)
         if (t < tiles) {
           const int n = n_tile + t, st = n % L::STAGES;
           wait(&k_full[st], (n / L::STAGES) & 1);
+          // the weights of tile n - 2 lie where S goes
+          if (n >= 2) wait(&pv_done[2 * q + (n & 1)], ((n >> 1) - 1) & 1);
           if (ok && lane == 0) {
             tc_fence_after();
             // a step along K moves the descriptors' start address (in 16 bytes)
