@@ -13,10 +13,7 @@
 //   w = 2^(S f + log2 vs - M + 8), written over S as packed fp16
 //   O += w V         tcgen05, w in TMEM, V MN-major from shared memory
 // with the statistics of kv8_attn.cu.  S of tile t + 1 is done before the softmax
-// of tile t is, so that the chain from tile to tile is the softmax alone.  Products
-// of different shape or accumulator have no order of their own in the PTX model,
-// so S of tile n + 2, whose buffer holds the weights of tile n, waits for pv_done
-// of n; only products into the same accumulator follow one another without a wait.
+// of tile t is, so that the chain from tile to tile is the softmax alone.
 // What shaped this: with shared memory in use there is next to no L1, so
 // loads through registers and spilled registers both starve (loads in flight
 // need L1 lines, spills go to L2); hence the bulk copies, and 64-key tiles,
@@ -27,9 +24,26 @@
 // a large library product; the rest is the softmax's chain (scores out of TMEM,
 // weights back, barriers).
 //
-// One CTA an SM: tiles of 32 and 64 rows, two CTAs an SM, gave now and then a wrong
-// tile (one run in some 2000, never with one CTA an SM); the cause was not found, so
-// those tiles are gone and the shared memory is sized to keep an SM for one CTA.
+// Orderings.  Who waits for whom (n: the CTA's running tile, a barrier's phase
+// is the n-th use of its slot, and none can be two phases ahead of a waiter):
+//   unit_full   codes of n have landed            -> converter reads them
+//   unit_free   converted and stored, proxy fence -> copy of tile n + DEPTH
+//   k/v_full    fp16 tile written, proxy fence    -> S (n), w V (n)
+//   k/v_free    commit after S (n), w V (n)       -> converter writes n + STAGES
+//   q_full      Q written, proxy fence            -> first S of the run
+//   s_full      commit after S (n)                -> softmax reads S
+//   p_full      w stored, O rescaled, TMEM fence  -> w V (n)
+//   pv_done     commit after w V (n)              -> S (n + 2), whose buffer holds the
+//               weights of n; O's rescale for n + 1; O's and Q's last use of a run
+//   sc_full/free  the scales of n                 -> softmax; scales of n + 4
+// A commit follows all earlier products of its warp, so s_full (n) also says
+// that w V (n - 2) is done, and a pv_done that nobody waited for is no phase
+// behind.  Products of different shape or accumulator have no order of their own
+// in the PTX model, so S (n + 2) waits for pv_done (n); only products into the
+// same accumulator follow one another without a wait.  A converter's reads of
+// a unit (generic proxy) and the copy that refills it (async proxy) need the
+// proxy fence between them: with the unit released as soon as its loads were
+// issued, a tile's last keys were now and then those of the tile after next.
 //
 // Every wait is bounded (WAIT_LIMIT_NS); a role whose wait ran out keeps
 // walking its loops without waiting or touching TMEM, so that all barriers
@@ -53,7 +67,7 @@ struct TcLay {
   static constexpr int SUB = KEYS * 128;              // [64 keys][64 dims] fp16
   static constexpr int MAT = KH * SUB;                // fp16 K or V of a tile
   static constexpr int UNIT = KEYS * HD;              // int8 K or V of a tile
-  static constexpr int DEPTH = NQ == 1 ? 2 : 4;       // tiles in the ring, K and V a unit each
+  static constexpr int DEPTH = 4;                     // tiles in the ring, K and V a unit each
   static constexpr int RING = 2 * DEPTH;
   static constexpr int STAGES = NQ;                   // fp16 tiles of K, and of V
   static constexpr int Q_SUB = 128 * 128;             // [128 rows][64 dims] fp16
@@ -72,10 +86,8 @@ struct TcLay {
   static constexpr int PAGE_OFF = MISC_OFF + 16;           // the units' pages
   static constexpr int THREADS = 128 * NQ + 2 * CONV + 32 + 32 * NQ;
   static constexpr int WALK_OFF = (PAGE_OFF + RING * 4 + 15) / 16 * 16;
-  static constexpr int USED = WALK_OFF + THREADS / 32 * (int)sizeof(Walk) + 1024;   // slack for
+  static constexpr int SMEM = WALK_OFF + THREADS / 32 * (int)sizeof(Walk) + 1024;   // slack for
                                                                                     // 1024-byte alignment
-  // one CTA an SM, whatever else runs (see above)
-  static constexpr int SMEM = USED > (120 << 10) ? USED : 120 << 10;
   static constexpr uint32_t TMEM_COLS = 256 * NQ;     // a row tile: S 2 x 64, O 128
   static_assert(SMEM <= 232448, "shared memory layout");
 };
@@ -414,9 +426,10 @@ __global__ void __launch_bounds__(TcLay<HD, NQ>::THREADS, 1)
           x[j] = none ? make_uint4(0, 0, 0, 0)
                       : *reinterpret_cast<const uint4*>(ring + slot * L::UNIT + (j / HALVES * ROWS + row0) * HD +
                                                         j % HALVES * 64 + ch * 16);
-        mbar_arrive(&unit_free[slot]);
         if (use > 0) wait(&free[st], (use - 1) & 1);
         put(smem + (is_v ? L::V_OFF : L::K_OFF) + st * L::MAT, x);
+        // behind the stores, which need all that was loaded, and their proxy fence
+        mbar_arrive(&unit_free[slot]);
         mbar_arrive(&full[st]);
       }
     }

@@ -536,3 +536,37 @@ def test_many_runs_repeat_to_the_bit(hq, hkv, rows):
     first = fdllm.fdllm_kv8_attention(c, q, starts, dl, max_q=rows, max_len=1300)
     for _ in range(40):
         assert torch.equal(fdllm.fdllm_kv8_attention(c, q, starts, dl, max_q=rows, max_len=1300), first)
+
+
+@pytest.mark.parametrize("hq,hkv,hd,rows", [(28, 4, 128, 16), (28, 4, 128, 32), (8, 2, 64, 40), (16, 4, 64, 21)])
+def test_grouped_blocks_stay_the_same_over_many_calls(hq, hkv, hd, rows):
+    """Runs of 112, 224, 160 and 84 rows a K/V head: 1500 calls give the bits of the
+    first, alone, with a matrix product on another stream beside them, and with
+    the same call on another stream."""
+    g = torch.Generator().manual_seed(17)
+    lens = [int(x) for x in torch.randint(1, 1300, (16,), generator=g)]
+    cache = kv8_ref.make_cache(g, lens, hkv, hd)
+    _, c = _gpu(cache)
+    q = torch.randn(16 * rows, hq, hd, generator=g).to(torch.float16)
+    Q, starts, dl = q.cuda(), _i32([rows * i for i in range(17)]), _i32(lens)
+
+    def call():
+        return fdllm.fdllm_kv8_attention(c, Q, starts, dl, max_q=rows, max_len=1300)
+
+    first = call()
+    _check_attention(cache, q, starts.tolist(), lens, hd ** -0.5, first)
+    bad = torch.zeros(2, dtype=torch.int64, device="cuda")
+    a = torch.randn(2048, 2048, device="cuda").to(torch.bfloat16)
+    s = torch.cuda.Stream()
+    for beside in (None, "product", "call"):
+        s.wait_stream(torch.cuda.current_stream())
+        for i in range(500):
+            if beside is not None:
+                with torch.cuda.stream(s):
+                    if beside == "product":
+                        a @ a
+                    else:
+                        bad[1] += (call() != first).any()
+            bad[0] += (call() != first).any()
+        torch.cuda.synchronize()
+    assert bad.tolist() == [0, 0]
