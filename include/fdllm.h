@@ -408,7 +408,7 @@ FDLLM_API int fdllm_gemm_noalloc(const void* w_dev, const void* x_dev, float* y_
 #define FDLLM_KV8_BLOCK 16  /* positions that share a scale (per K/V head) */
 #define FDLLM_KV8_BAD_PAGE 1   /* a page id outside [0, n_pages) where one was needed */
 #define FDLLM_KV8_BAD_RANGE 2  /* starts, lens, pos or the rotation table out of range */
-#define FDLLM_KV8_TIMEOUT 4    /* a bounded device-side wait ran out: results invalid */
+#define FDLLM_KV8_TIMEOUT 4    /* a bounded device-side wait ran out: the rows concerned are NaN */
 
 /* One layer's 8-bit K/V cache: key and value = code * scale, code an int8 in
  * [-127, 127], one float scale >= 0 for each block of 16 positions and K/V

@@ -47,7 +47,9 @@
 //
 // Every wait is bounded (WAIT_LIMIT_NS); a role whose wait ran out keeps
 // walking its loops without waiting or touching TMEM, so that all barriers
-// are still met, and FDLLM_KV8_TIMEOUT is reported.
+// are still met.  The rows of that run and of the CTA's later ones are then NaN,
+// and FDLLM_KV8_TIMEOUT is reported.  Before the CTA frees TMEM and ends, its
+// copies and products in flight are waited for, on every path.
 #include <algorithm>
 
 #include "kv8_attn.cuh"
@@ -161,6 +163,7 @@ __global__ void __launch_bounds__(TcLay<HD, NQ>::THREADS, 1)
   uint64_t* v_full = bars + 4;
   uint64_t* v_free = bars + 6;
   uint64_t* s_full = bars + 8;         // [NQ][2], by tile parity
+  uint64_t* drained = bars + 12;       // [NQ]: all products of the CTA
   uint64_t* pv_done = bars + 27;       // [NQ][2], by tile parity
   uint64_t* sc_full = bars + 14;       // [4]: scales
   uint64_t* sc_free = bars + 18;
@@ -191,6 +194,7 @@ __global__ void __launch_bounds__(TcLay<HD, NQ>::THREADS, 1)
       mbar_init(&pv_done[2 + i], 1);
       mbar_init(&p_full[i], 128);
       mbar_init(&p_full[2 + i], 128);
+      mbar_init(&drained[i], 1);
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(&sc_full[i], NB);
@@ -346,7 +350,9 @@ __global__ void __launch_bounds__(TcLay<HD, NQ>::THREADS, 1)
         mbar_arrive(&p_full[2 * q + (n_tile & 1)]);
       }
       // ---- the run's output, or its part, DIMS dims at a time through shared memory
-      const bool have_o = tiles > 0 && pv_wait(n_tile - 1);
+      // (a role whose wait ran out has said so before it went on)
+      const bool have_o = tiles > 0 && pv_wait(n_tile - 1) && !__any_sync(0xffffffffu, *abort_flag);
+      const float none = tiles > 0 ? __int_as_float(0x7fffffff) : 0.0f;
       tc_fence_after();
       {
         constexpr int DIMS = L::DIMS, XROW = L::XROW, LR = DIMS / 4;
@@ -364,7 +370,7 @@ __global__ void __launch_bounds__(TcLay<HD, NQ>::THREADS, 1)
           for (int j = 0; j < DIMS; j += 4)
             *reinterpret_cast<float4*>(xo + i * XROW + j) =
                 have_o ? make_float4(v[j] * fac, v[j + 1] * fac, v[j + 2] * fac, v[j + 3] * fac)
-                       : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                       : make_float4(none, none, none, none);
           named_bar(1 + q, 128);
           // LR lanes a row
           for (int at = i / LR; at < 128; at += 128 / LR) {
@@ -440,6 +446,7 @@ __global__ void __launch_bounds__(TcLay<HD, NQ>::THREADS, 1)
     // scales of block `lane` of the last tile asked for, on their way
     float ks = 0.0f, vs = 0.0f;
     bool live = false;
+    int issued[2] = {0, 0};   // tiles whose units of K, of V were asked for
     auto store_scales = [&](int n) {
       const int at = n & 3;
       if (n >= 4) wait(&sc_free[at], (n / 4 - 1) & 1);
@@ -471,6 +478,7 @@ __global__ void __launch_bounds__(TcLay<HD, NQ>::THREADS, 1)
         for (int is_v = 0; is_v < 2; ++is_v) {
           const int slot = n % L::DEPTH * 2 + is_v;
           if (n >= L::DEPTH) wait(&unit_free[slot], (n / L::DEPTH - 1) & 1);
+          if (ok) issued[is_v] = n + 1;
           if (ok && lane == 0) {
             unit_page[slot] = page;
             if (page < 0) {
@@ -496,6 +504,11 @@ __global__ void __launch_bounds__(TcLay<HD, NQ>::THREADS, 1)
       if (tiles > 0) store_scales(n_tile + tiles - 1);
       n_tile += tiles;
     }
+    // no copy may land in shared memory that the CTA has given back
+#pragma unroll
+    for (int is_v = 0; is_v < 2; ++is_v)
+      for (int n = max(0, issued[is_v] - L::DEPTH); n < issued[is_v]; ++n)
+        mbar_wait(&unit_full[n % L::DEPTH * 2 + is_v], (n / L::DEPTH) & 1, err, nullptr);
   } else {
     // ================================================== MMA, a warp a row tile
     const int q = warp - (4 * NQ + 2 * CONV / 32 + 1);
@@ -544,6 +557,9 @@ __global__ void __launch_bounds__(TcLay<HD, NQ>::THREADS, 1)
       }
       n_tile += tiles;
     }
+    // no product may touch TMEM or shared memory that the CTA has given back
+    if (lane == 0) tc_commit(&drained[q]);
+    mbar_wait(&drained[q], 0, err, nullptr);
   }
   tc_fence_before();
   __syncthreads();

@@ -434,7 +434,7 @@ def fdllm_attention(ctx, q_dev, o_dev, layer: int, L: int) -> None:
 # These calls take a CUDA stream handle (None: torch's current stream) and
 # allocate what they return as torch does under that stream.
 KV8_PAGE, KV8_BLOCK = 64, 16              # positions per page, positions that share a scale
-KV8_BAD_PAGE, KV8_BAD_RANGE = 1, 2        # bits of a call's status word
+KV8_BAD_PAGE, KV8_BAD_RANGE, KV8_TIMEOUT = 1, 2, 4   # bits of a call's status word
 
 
 _ops = None

@@ -4,6 +4,7 @@ message before the device is touched, and the tests' own plain
 implementations obey the operators' formulas."""
 import ctypes
 import os
+import re
 import subprocess
 
 import numpy as np
@@ -134,6 +135,15 @@ def test_struct_sizes_match_the_header(tmp_path):
                      (fdllm.FdllmKv8AttentionArgs, "status"), (fdllm.FdllmSampleArgs, "prob")):
         want += [ctypes.sizeof(st), getattr(st, last).offset]
     assert got == want
+
+
+def test_constants_match_the_header():
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    text = open(os.path.join(root, "include", "fdllm.h")).read()
+    found = dict(re.findall(r"#define FDLLM_(KV8_\w+) (\d+)", text))
+    assert set(found) == {"KV8_PAGE", "KV8_BLOCK", "KV8_BAD_PAGE", "KV8_BAD_RANGE", "KV8_TIMEOUT"}
+    assert {n: getattr(fdllm, n) for n in found} == {n: int(v) for n, v in found.items()}
+
 
 def test_binding_refuses_cpu_tensors_and_wrong_shapes():
     c = kv8_ref.make_cache(torch.Generator().manual_seed(0), [5], 2, 64)
