@@ -309,12 +309,12 @@ __global__ void __launch_bounds__(AT_WARPS * 32, 2) kv8_attn_kernel(const AttnP 
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
           alpha[hf] = 1.0f;
-          if (mx > M[hf] + SLACK || (M[hf] == -INFINITY && mx > -INFINITY)) {
+          if (passes(mx, M[hf], SLACK)) {
             alpha[hf] = ex2(M[hf] - mx);
             M[hf] = mx;
             moved = true;
           }
-          const float ref = W_EXP - (M[hf] == -INFINITY ? 0.0f : M[hf]);
+          const float ref = weight_ref(M[hf]);
           float sum = 0.0f;
 #pragma unroll
           for (int b = 0; b < 2; ++b) {

@@ -204,6 +204,14 @@ FD_DEV float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// Whether a row's reference M moves to its new maximum mx (M = -inf: to any that
+// is above).  The difference of two near numbers is exact; M + slack would round
+// up from 2^24 on.
+FD_DEV bool passes(float mx, float M, float slack) { return mx - M > slack; }
+// What is added to t to give a weight's exponent, at most W_EXP + M_SLACK.
+// Rounded down, for where 16 lies between the numbers around M (2^27), half of
+// the sums W_EXP - M would round up by 8.
+FD_DEV float weight_ref(float M) { return __fadd_rd(W_EXP, M == -INFINITY ? 0.0f : -M); }
 // Two of the four offset-binary bytes of x (selector) as exact fp16 codes:
 // the byte under the exponent of 1024, minus 1024 + 128.
 template <uint32_t SEL> FD_DEV uint32_t codes_h2(uint32_t x) {

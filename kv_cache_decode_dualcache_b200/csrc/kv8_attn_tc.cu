@@ -309,12 +309,12 @@ __global__ void __launch_bounds__(TcLay<HD, NQ>::THREADS, 1)
 #pragma unroll
           for (int j = 0; j < KEYS; j += 2) mx = fmaxf(fmaxf(mx, v[j]), v[j + 1]);
           float alpha = 1.0f;
-          const bool move = mx > M + M_SLACK || (M == -INFINITY && mx > -INFINITY);
+          const bool move = passes(mx, M, M_SLACK);
           if (move) {
             alpha = ex2(M - mx);
             M = mx;
           }
-          const float ref = W_EXP - (M == -INFINITY ? 0.0f : M);
+          const float ref = weight_ref(M);
           float sum = 0.0f;
           uint32_t w[KEYS / 2];
 #pragma unroll

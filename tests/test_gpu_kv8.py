@@ -176,6 +176,61 @@ def test_attention_value_scales_just_below_a_power_of_two(dtype, space):
             _check_attention(cache, q, [0, 3], lens, hd ** -0.5, got)
 
 
+@pytest.mark.parametrize("rows", [1, 70])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_attention_scores_beyond_2_24(dtype, rows):
+    """Scores up to 2^30 and down to -2^30, whose neighbours in float32 are up to 128
+    apart: finite weights all the same.  With one key, or two that are equal, the
+    result is the value: the weight and its sum are off by at most 2^-11 (one fp16
+    term) and 2^-20 (exp2, the sums, the division)."""
+    hd = 64
+    cache = kv8_ref.make_cache(torch.Generator().manual_seed(18), [2], 1, hd)
+    page = int(cache["table"][0, 0])
+    cache["k"][page, 0] = 64
+    cache["k_scale"][page, 0, 0] = 2.0 ** -6
+    cache["v"][page, 0, 1] = cache["v"][page, 0, 0]
+    for vs in (1.0, 1.75):
+        cache["v_scale"][page, 0, 0] = vs
+        _, c = _gpu(cache)
+        v = cache["v"][page, 0, 0].double() * vs
+        tol = v.abs() * (2.0 ** -11 + 2.0 ** -20 + torch.finfo(TYPES[dtype]).eps / 2)
+        for n in (1, 2):
+            for sign in (1, -1):
+                for e in range(20, 31):
+                    for m in (1.0, 1.13, 1.31, 1.5, 1.77, 1.93):
+                        # q . k = hd, so the score in base 2 is sign m 2^e or so
+                        scale = sign * m * 2.0 ** e / hd / 1.4426950408889634
+                        q = torch.ones(rows, 1, hd, dtype=TYPES[dtype], device="cuda")
+                        got = fdllm.fdllm_kv8_attention(c, q, _i32([0, rows]), _i32([n]), scale=scale)
+                        assert ((got.cpu().double() - v).abs() <= tol).all(), (vs, n, sign, e, m)
+
+
+@pytest.mark.parametrize("rows", [1, 70])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_attention_large_scores_step_by_a_power_of_two(dtype, rows):
+    """Equal scores of 2^22 to 2^29, value scales 1 and then 2^6 to 2^9: where
+    float32 has no number between, a later key passes the reference by just what
+    it may, or by the next number."""
+    hd, lens = 64, [192]
+    cache = kv8_ref.make_cache(torch.Generator().manual_seed(19), lens, 1, hd)
+    pages = cache["table"][0, :3].long()
+    cache["k"][pages] = 64
+    cache["k_scale"][pages] = 2.0 ** -6
+    q = torch.ones(rows, 1, hd, dtype=TYPES[dtype])
+    for up in (6, 7, 8, 9):
+        cache["v_scale"][pages] = 1.0
+        cache["v_scale"][pages[2]] = 2.0 ** up * 0.99999
+        _, c = _gpu(cache)
+        for sign in (1, -1):
+            for e in range(22, 30):
+                for m in (1.0, 1.2500001, 1.5000002, 1.9):
+                    scale = sign * m * 2.0 ** e / hd / 1.4426950408889634
+                    for space in (None, torch.empty(0, dtype=torch.uint8, device="cuda")):
+                        got = fdllm.fdllm_kv8_attention(c, q.cuda(), _i32([0, rows]), _i32(lens), scale=scale,
+                                                        workspace=space)
+                        assert torch.isfinite(got).all(), (up, sign, e, m)
+
+
 def test_attention_uses_the_codes_full_range():
     """A code of -128 (not one the append writes) reads as -128."""
     cache = kv8_ref.make_cache(torch.Generator().manual_seed(0), [1], 1, 32)
