@@ -407,7 +407,8 @@ FDLLM_API int fdllm_gemm_noalloc(const void* w_dev, const void* x_dev, float* y_
 #define FDLLM_KV8_PAGE 64   /* positions per page */
 #define FDLLM_KV8_BLOCK 16  /* positions that share a scale (per K/V head) */
 #define FDLLM_KV8_BAD_PAGE 1   /* a page id outside [0, n_pages) where one was needed */
-#define FDLLM_KV8_BAD_RANGE 2  /* starts, lens, pos or the rotation table out of range */
+#define FDLLM_KV8_BAD_RANGE 2  /* starts (falling, negative or beyond n_tokens: clamped), lens, pos or
+                                  the rotation table out of range */
 #define FDLLM_KV8_TIMEOUT 4    /* a bounded device-side wait ran out: the rows concerned are NaN */
 
 /* One layer's 8-bit K/V cache: key and value = code * scale, code an int8 in

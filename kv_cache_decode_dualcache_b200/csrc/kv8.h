@@ -38,6 +38,13 @@ inline bool rows_ok(const void* p, const int64_t* strides, int esz) {
   return aligned16(p) && (strides[0] * esz) % 16 == 0 && (strides[1] * esz) % 16 == 0;
 }
 
+#ifdef __CUDACC__
+// Whether sequence i's rows [starts[i], starts[i + 1]) lie in [0, n_tokens).
+__device__ __forceinline__ bool starts_ok(const int32_t* starts, int i, int n_tokens) {
+  return 0 <= starts[i] && starts[i] <= starts[i + 1] && starts[i + 1] <= n_tokens;
+}
+#endif
+
 // Device facts that do not change, asked once per device.
 inline cudaError_t sm_count(int* n) {
   static std::atomic<int> known[64];

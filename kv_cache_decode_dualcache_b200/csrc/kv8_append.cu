@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(APP_WARPS * 32, 2) kv8_append_kernel(const App
   const int len_in = a.lens[seq];
   const int w0 = a.pos ? a.pos[seq] : len_in;
   int n = r_hi - r_lo;
-  int bad = 0;
+  int bad = kv8::starts_ok(a.starts, seq, a.n_tokens) ? 0 : FDLLM_KV8_BAD_RANGE;
   int limit = c.max_pages * FDLLM_KV8_PAGE;
   const int len = min(max(len_in, 0), limit);
   if (len != len_in) bad |= FDLLM_KV8_BAD_RANGE;

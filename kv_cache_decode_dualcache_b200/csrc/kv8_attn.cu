@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(AT_WARPS * 32, 2) kv8_attn_kernel(const AttnP 
   float* xo = reinterpret_cast<float*>(smem);                // [warp][R][XROW]
 
   pdl_trigger();   // the join may be set up; it waits for this grid's end
-  report_lengths(P);
+  report_range(P);
   Walk* walk = reinterpret_cast<Walk*>(smem + L_::WALK_OFF) + warp;
   walk_start(walk, P, R);
   Segment sg;

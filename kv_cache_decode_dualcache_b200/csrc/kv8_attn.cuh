@@ -251,11 +251,11 @@ template <typename T> FD_DEV void store4(T* p, float a, float b, float c, float 
   }
 }
 
-// Block 0 reports lengths out of range.
-FD_DEV void report_lengths(const AttnP& P) {
+// Block 0 reports lengths and starts out of range.
+FD_DEV void report_range(const AttnP& P) {
   if (blockIdx.x == 0 && P.a.status)
     for (int i = threadIdx.x; i < P.c.n_seqs; i += blockDim.x)
-      if (P.a.lens[i] < 0 || P.a.lens[i] > P.c.max_pages * PAGE)
+      if (P.a.lens[i] < 0 || P.a.lens[i] > P.c.max_pages * PAGE || !starts_ok(P.a.starts, i, P.a.n_tokens))
         atomicOr(P.a.status, FDLLM_KV8_BAD_RANGE);
 }
 

@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(TcLay<HD, NQ>::THREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = misc[0];
-  report_lengths(P);
+  report_range(P);
   Walk* walk = reinterpret_cast<Walk*>(smem + L::WALK_OFF) + warp;
   walk_start(walk, P, R);
   Segment sg;

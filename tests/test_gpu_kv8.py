@@ -272,6 +272,29 @@ def test_attention_bad_pages_and_lengths_are_reported():
     assert torch.isfinite(out).all()
 
 
+@pytest.mark.parametrize("starts,bad", [([0, 1, 2], False), ([0, 0, 0], False), ([2, 2, 2], False), ([1, 0, 2], True),
+                                        ([0, 1, 3], True), ([-1, 1, 2], True), ([3, 3, 3], True), ([0, 5, 2], True)])
+@pytest.mark.parametrize("rows", [2, 140])
+def test_starts_out_of_range_are_reported(starts, bad, rows):
+    """By both calls (and both attention kernels); the starts are clamped, rows of
+    no sequence are left as they are."""
+    g = torch.Generator().manual_seed(20)
+    cache = kv8_ref.make_cache(g, [200, 70], 2, 64)
+    d, c = _gpu(cache)
+    q = torch.randn(rows, 4, 64, generator=g).to(torch.float16).cuda()
+    # 1 stands for the middle, 2 for the end, 3 and 5 for what is behind it
+    at = _i32([x if x < 1 else rows // 2 if x == 1 else rows + x - 2 for x in starts])
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = torch.full((rows, 4, 64), 7.0, dtype=q.dtype, device="cuda")
+    fdllm.fdllm_kv8_attention(c, q, at, _i32([130, 70]), out=out, status=st)
+    assert st.item() == (fdllm.KV8_BAD_RANGE if bad else 0) and torch.isfinite(out).all()
+    if starts in ([0, 0, 0], [2, 2, 2], [3, 3, 3]):
+        assert (out == 7.0).all()
+    st.zero_()
+    fdllm.fdllm_kv8_append(c, q[:, :2], q[:, 2:], at, _i32([0, 0]), status=st)
+    assert st.item() & fdllm.KV8_BAD_RANGE == (fdllm.KV8_BAD_RANGE if bad else 0)
+
+
 def test_attention_refuses_a_small_workspace():
     cache = kv8_ref.make_cache(torch.Generator().manual_seed(0), [9000], 1, 64)
     _, c = _gpu(cache)
