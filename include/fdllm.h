@@ -468,7 +468,8 @@ typedef struct {
   void* v_out;             /* optional, likewise */
   void* q_out;             /* the rotated q, dense [n_tokens, n_heads, head_dim]; NULL iff q is;
                               may be q itself when q is dense */
-  int32_t* lens_out;       /* optional [n_seqs], neither lens nor pos: max(lens, position after the last row) */
+  int32_t* lens_out;       /* optional [n_seqs], not overlapping starts, lens or pos: max(lens, position
+                              after the last row) */
   int32_t* status;         /* optional */
 } fdllm_kv8_append_args;
 

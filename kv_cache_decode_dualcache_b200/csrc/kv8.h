@@ -31,6 +31,11 @@ inline bool aligned4(std::initializer_list<const void*> ps) {
     if (reinterpret_cast<uintptr_t>(p) & 3) return false;
   return true;
 }
+// Whether arrays a of n and b of m int32 share a byte.
+inline bool overlap(const int32_t* a, int64_t n, const int32_t* b, int64_t m) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return b && x < y + 4 * m && y < x + 4 * n;
+}
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 // Rows of `heads` vectors of hd elements that start on 16-byte boundaries.

@@ -340,8 +340,10 @@ extern "C" int fdllm_kv8_append(const fdllm_kv8* cache, const fdllm_kv8_append_a
   if (!a.starts || !a.lens) return kv8::fail(call, FDLLM_ERR_ARG, "starts or lens is NULL");
   if (!kv8::aligned4({a.starts, a.lens, a.pos, a.lens_out, a.status}))
     return kv8::fail(call, FDLLM_ERR_ARG, "int32 arrays must be 4-byte aligned");
-  if (a.lens_out && (a.lens_out == a.lens || a.lens_out == a.pos))
-    return kv8::fail(call, FDLLM_ERR_ARG, "lens_out must be neither lens nor pos");
+  const int64_t seqs = P.c.n_seqs;
+  if (a.lens_out && (kv8::overlap(a.lens_out, seqs, a.starts, seqs + 1) ||
+                     kv8::overlap(a.lens_out, seqs, a.lens, seqs) || kv8::overlap(a.lens_out, seqs, a.pos, seqs)))
+    return kv8::fail(call, FDLLM_ERR_ARG, "lens_out must not overlap starts, lens or pos");
   if (a.rope && (a.rope_len < 1 || !kv8::aligned16(a.rope)))
     return kv8::fail(call, FDLLM_ERR_ARG, "rope needs rope_len >= 1 and 16-byte alignment");
   if (a.n_tokens > 0) {

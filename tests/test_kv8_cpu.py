@@ -91,6 +91,16 @@ def test_bad_attention_arguments_are_refused(lib, over):
     assert lib.fdllm_last_error(None).startswith(b"fdllm_kv8_attention: ")
 
 
+@pytest.mark.parametrize("over", [dict(lens_out=P16 + 4), dict(lens_out=P16 + 8), dict(lens_out=P16 - 4),
+                                  dict(lens=P16 + 64, lens_out=P16 + 68), dict(pos=P16 + 64, lens_out=P16 + 60)], ids=str)
+def test_append_lens_out_over_its_inputs_is_refused(lib, over):
+    """Two sequences: starts are 3 words, lens and pos 2 each; other CTAs may read
+    them after lens_out has been written."""
+    a = _append_args(**over)
+    assert lib.fdllm_kv8_append(ctypes.byref(_cache()), ctypes.byref(a), None) == fdllm.FDLLM_ERR_ARG
+    assert b"lens_out" in lib.fdllm_last_error(None)
+
+
 @pytest.mark.parametrize("over", [
     dict(dtype=7), dict(rows=-1), dict(vocab=0), dict(vocab=(1 << 18) + 1, row_stride=1 << 20),
     dict(row_stride=99), dict(mask_id=100), dict(mask_id=-2), dict(logits=None), dict(u=None),
