@@ -509,7 +509,8 @@ typedef struct {
   int64_t q_strides[2];
   const int32_t* starts;   /* [n_seqs + 1] */
   const int32_t* lens;     /* [n_seqs]: keys [0, lens[i]) of sequence i */
-  void* out;               /* like q, with its own strides; not overlapping q */
+  void* out;               /* like q, with its own strides; not overlapping q, nor
+                              its rows and heads one another */
   int64_t out_strides[2];
   void* workspace;         /* 16-byte aligned, workspace_bytes long, free to be overwritten while
                               the call's work runs; may be NULL (keys are then not split) */

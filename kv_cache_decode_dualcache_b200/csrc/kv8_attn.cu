@@ -35,6 +35,7 @@
 // mantissa (a factor of w).
 #include <algorithm>
 #include <cmath>
+#include <cstdlib>
 
 #include "kv8_attn.cuh"
 
@@ -559,6 +560,9 @@ extern "C" int fdllm_kv8_attention(const fdllm_kv8* cache, const fdllm_kv8_atten
   const int esz = kv8::elem_bytes(a.dtype);
   if (!kv8::rows_ok(a.q, a.q_strides, esz) || !kv8::rows_ok(a.out, a.out_strides, esz))
     return kv8::fail(call, FDLLM_ERR_ARG, "rows and heads of q and out must be 16-byte aligned");
+  if (a.out == a.q || (a.n_tokens > 1 && std::abs(a.out_strides[0]) < P.c.head_dim) ||
+      (a.n_heads > 1 && std::abs(a.out_strides[1]) < P.c.head_dim))
+    return kv8::fail(call, FDLLM_ERR_ARG, "out must not overlap q, nor its rows and heads one another");
   int sms = 0;
   cudaError_t e = kv8::sm_count(&sms);
   if (e != cudaSuccess) return kv8::fail(call, FDLLM_ERR_CUDA, cudaGetErrorString(e));

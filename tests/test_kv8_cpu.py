@@ -91,6 +91,15 @@ def test_bad_attention_arguments_are_refused(lib, over):
     assert lib.fdllm_last_error(None).startswith(b"fdllm_kv8_attention: ")
 
 
+@pytest.mark.parametrize("over", [dict(out=P16 * 2, out_token=0), dict(out=P16 * 2, out_head=0), dict(),
+                                  dict(out=P16 * 2, out_token=64), dict(out=P16 * 2, out_head=-64)], ids=str)
+def test_attention_outputs_that_share_memory_are_refused(lib, over):
+    """Rows or heads of out on top of one another (an expanded tensor), and out on
+    q, whose rows other CTAs may still read."""
+    rc = lib.fdllm_kv8_attention(ctypes.byref(_cache()), ctypes.byref(_attn_args(**over)), None)
+    assert rc == fdllm.FDLLM_ERR_ARG and b"overlap" in lib.fdllm_last_error(None)
+
+
 @pytest.mark.parametrize("over", [dict(lens_out=P16 + 4), dict(lens_out=P16 + 8), dict(lens_out=P16 - 4),
                                   dict(lens=P16 + 64, lens_out=P16 + 68), dict(pos=P16 + 64, lens_out=P16 + 60)], ids=str)
 def test_append_lens_out_over_its_inputs_is_refused(lib, over):
