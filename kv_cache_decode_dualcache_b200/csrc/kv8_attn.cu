@@ -516,7 +516,8 @@ const char* check_args(const fdllm_kv8_attention_args* args, const fdllm_kv8& c)
   if (a.n_tokens < 0 || a.max_q < 0 || a.max_len < 0) return "n_tokens, max_q and max_len must be >= 0";
   if (a.n_heads < 1 || a.n_heads > 65535 || a.n_heads % c.n_kv_heads)
     return "n_heads must be a multiple of n_kv_heads in [1, 65535]";
-  if ((int64_t)a.n_tokens * (a.n_heads / c.n_kv_heads) > 0x7fffffff) return "too many query rows";
+  // rows are counted in 32 bits, up to a tile's end
+  if ((int64_t)a.n_tokens * (a.n_heads / c.n_kv_heads) > 0x7fffff00) return "too many query rows";
   if (!std::isfinite(a.scale)) return "scale must be finite";
   return nullptr;
 }

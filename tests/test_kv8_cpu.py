@@ -100,6 +100,14 @@ def test_attention_outputs_that_share_memory_are_refused(lib, over):
     assert rc == fdllm.FDLLM_ERR_ARG and b"overlap" in lib.fdllm_last_error(None)
 
 
+@pytest.mark.parametrize("tokens,heads", [(0x7fffffff, 4), (0x7fffff01, 4), (0x3fffffc0, 8)])
+def test_query_rows_beyond_the_kernels_indices_are_refused(lib, tokens, heads):
+    """Tiles of up to 256 rows are counted in 32 bits."""
+    a = _attn_args(out=2 * P16, n_tokens=tokens, n_heads=heads)
+    assert lib.fdllm_kv8_attention(ctypes.byref(_cache()), ctypes.byref(a), None) == fdllm.FDLLM_ERR_ARG
+    assert b"query rows" in lib.fdllm_last_error(None)
+
+
 @pytest.mark.parametrize("over", [dict(lens_out=P16 + 4), dict(lens_out=P16 + 8), dict(lens_out=P16 - 4),
                                   dict(lens=P16 + 64, lens_out=P16 + 68), dict(pos=P16 + 64, lens_out=P16 + 60)], ids=str)
 def test_append_lens_out_over_its_inputs_is_refused(lib, over):
