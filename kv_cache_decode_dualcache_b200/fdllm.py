@@ -465,7 +465,13 @@ class Kv8Cache:
     k, v: int8 [n_pages, n_kv_heads, 64, head_dim]; k_scale, v_scale: float32
     [n_pages, n_kv_heads, 4] (pages may be strided, e.g. slices of one pool
     for all layers; k and v alike); page_table: int32 [n_seqs, max_pages], its
-    rows side by side or apart, not expanded from one."""
+    rows side by side or apart, not expanded from one.  The calls see the
+    tensors given here (their contents may change): attributes are read-only."""
+
+    def __setattr__(self, name, value):
+        if "address" in self.__dict__:   # set last
+            raise AttributeError(f"{name} of a Kv8Cache is read-only: make a new one")
+        super().__setattr__(name, value)
 
     def __init__(self, k, v, k_scale, v_scale, page_table):
         import torch

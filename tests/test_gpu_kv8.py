@@ -295,6 +295,16 @@ def test_starts_out_of_range_are_reported(starts, bad, rows):
     assert st.item() & fdllm.KV8_BAD_RANGE == (fdllm.KV8_BAD_RANGE if bad else 0)
 
 
+def test_a_cache_keeps_its_tensors():
+    """The C struct holds their addresses: a table assigned later (a longer one,
+    say) would not be seen, and the old one's memory be read when it is gone."""
+    d, c = _gpu(kv8_ref.make_cache(torch.Generator().manual_seed(0), [70], 1, 64))
+    for name in ("k", "v", "k_scale", "v_scale", "page_table", "n_seqs", "struct", "address"):
+        with pytest.raises(AttributeError, match="read-only"):
+            setattr(c, name, getattr(c, name))
+    assert c.page_table.data_ptr() == c.struct.page_table == d["table"].data_ptr()
+
+
 def test_attention_refuses_a_small_workspace():
     cache = kv8_ref.make_cache(torch.Generator().manual_seed(0), [9000], 1, 64)
     _, c = _gpu(cache)
