@@ -501,7 +501,8 @@ typedef struct {
   int32_t n_tokens;        /* rows of q and out */
   int32_t n_heads;         /* query heads, a multiple of n_kv_heads; query head h reads K/V head
                               h / (n_heads / n_kv_heads) */
-  int32_t max_q;           /* launch hint: largest number of rows of one sequence (0 = n_tokens) */
+  int32_t max_q;           /* launch hint: largest number of rows of one sequence (0 = n_tokens /
+                              n_seqs, an even batch) */
   int32_t max_len;         /* launch hint: largest lens (0 = 64 max_pages); wrong hints only cost
                               time */
   float scale;             /* softmax scale, e.g. 1 / sqrt(head_dim); finite */

@@ -464,7 +464,9 @@ struct Plan {
 // 2048 keys 16 / 22 us; 224 rows, 1024 keys 16 / 24 us, and 131072 keys, where
 // the kernel above would read every page 14 times, 119 us there.
 Plan plan(const fdllm_kv8& c, const fdllm_kv8_attention_args& a, int num_sms) {
-  const int64_t most_q = a.max_q > 0 ? std::min(a.max_q, a.n_tokens) : a.n_tokens;
+  // rows of a sequence; without a hint those of an even batch, not all of them
+  const int64_t most_q = a.max_q > 0 ? std::min(a.max_q, a.n_tokens)
+                                     : ((int64_t)a.n_tokens + c.n_seqs - 1) / c.n_seqs;
   const int64_t rows = std::max<int64_t>(1, most_q * (a.n_heads / c.n_kv_heads));
   const int64_t table = (int64_t)c.max_pages * PAGE;
   const int64_t len = std::max<int64_t>(1, a.max_len > 0 ? std::min<int64_t>(a.max_len, table) : table);

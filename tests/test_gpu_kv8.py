@@ -611,6 +611,22 @@ def test_decode_loop_on_the_cache():
         _check_attention(ref_c, ref["q"], starts, lens, hd ** -0.5, got)
 
 
+@pytest.mark.parametrize("n,rows,hq,hkv", [(64, 1, 28, 4), (16, 32, 32, 32), (16, 32, 28, 4), (1, 70, 8, 2), (7, 3, 8, 8)])
+def test_a_batch_is_laid_out_alike_with_and_without_hints(n, rows, hq, hkv):
+    """n sequences of as many rows: without max_q the rows of one are taken to be
+    n_tokens / n_seqs, so the same kernel, grid and workspace, and the same bits."""
+    g = torch.Generator().manual_seed(21)
+    lens = [int(x) for x in torch.randint(1, 400, (n,), generator=g)]
+    cache = kv8_ref.make_cache(g, lens, hkv, 128)
+    _, c = _gpu(cache)
+    q = torch.randn(n * rows, hq, 128, generator=g).to(torch.bfloat16)
+    a, b = (fdllm.fdllm_kv8_attention_workspace(c, n * rows, hq, q.dtype, m, 64 * c.max_pages) for m in (0, rows))
+    assert a == b
+    starts, dl = _i32([rows * i for i in range(n + 1)]), _i32(lens)
+    got, want = (fdllm.fdllm_kv8_attention(c, q.cuda(), starts, dl, max_q=m) for m in (0, rows))
+    assert torch.equal(got, want)
+
+
 @pytest.mark.parametrize("hq,hkv,rows", [(32, 32, 32), (16, 16, 64), (28, 4, 16), (28, 4, 32)])
 def test_many_runs_repeat_to_the_bit(hq, hkv, rows):
     """Ragged batches whose CTAs start and end several runs each: every call
