@@ -2,7 +2,8 @@
 
 ``python -m kv_cache_decode_dualcache_b200.build`` (or ``build()``) compiles
 ``csrc/*.cu`` into ``libfdllm.so`` next to this file, and the Python binding of
-the stream-ordered operators into ``_binding.so``.  Nothing is
+the stream-ordered operators into ``_binding.so`` (a warning where torch's
+headers or g++ do not allow it; the library does not need it).  Nothing is
 JIT-compiled at import time; the binding loads the prebuilt library and fails
 loudly when it is missing.
 """
@@ -13,6 +14,7 @@ import os
 import shutil
 import subprocess
 import sys
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -23,6 +25,7 @@ LIB_CHECKS = os.path.join(HERE, "libfdllm_checks.so")
 # Python binding of the stream-ordered operators (an extension module over
 # torch's C++ interface; host code only).
 BINDING = os.path.join(HERE, "_binding.so")
+BINDING_STAMP = os.path.join(ROOT, "_build", "binding.stamp")   # what it was built for
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -53,12 +56,15 @@ def build_binding(force: bool = False, verbose: bool = False) -> str:
     import sysconfig
 
     src = os.path.join(HERE, "csrc", "binding.cpp")
-    inputs = (src, os.path.join(ROOT, "include", "fdllm.h"))
-    if not force and os.path.exists(BINDING) and all(
-            os.path.getmtime(p) <= os.path.getmtime(BINDING) for p in inputs):
-        return BINDING
     import torch
 
+    inputs = (src, os.path.join(ROOT, "include", "fdllm.h"))
+    stamp = f"python {sys.version} torch {torch.__version__} {os.path.dirname(torch.__file__)}"
+    if not force and os.path.exists(BINDING) and os.path.exists(BINDING_STAMP) and all(
+            os.path.getmtime(p) <= os.path.getmtime(BINDING) for p in inputs):
+        with open(BINDING_STAMP) as f:
+            if f.read() == stamp:
+                return BINDING
     root = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(_nvcc()))
     tmp = BINDING + ".tmp"
@@ -71,16 +77,31 @@ def build_binding(force: bool = False, verbose: bool = False) -> str:
            "-Wl,-rpath," + os.path.join(root, "lib")]
     if verbose:
         print(" ".join(cmd), file=sys.stderr)
-    r = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
-    if r.returncode != 0:
-        raise RuntimeError("g++ failed on binding.cpp:\n" + r.stdout.decode(errors="replace"))
+    try:
+        r = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+        if r.returncode != 0:
+            raise RuntimeError("g++ failed on binding.cpp:\n" + r.stdout.decode(errors="replace"))
+    except (OSError, RuntimeError):
+        if os.path.exists(BINDING):   # of another torch, or of older sources
+            os.remove(BINDING)
+        raise
     os.replace(tmp, BINDING)
+    os.makedirs(os.path.dirname(BINDING_STAMP), exist_ok=True)
+    with open(BINDING_STAMP, "w") as f:
+        f.write(stamp)
     return BINDING
 
 
 def build(force: bool = False, verbose: bool = False, extra=None, checks: bool = False) -> str:
-    lib = LIB_CHECKS if checks else LIB
-    build_binding(force, verbose)
+    lib = build_library(LIB_CHECKS if checks else LIB, force, verbose, extra, checks)
+    try:
+        build_binding(force, verbose)
+    except (ImportError, OSError, RuntimeError) as e:
+        warnings.warn(f"the Python binding of the stream-ordered operators was not built: {e}", RuntimeWarning)
+    return lib
+
+
+def build_library(lib: str, force: bool, verbose: bool, extra, checks: bool) -> str:
     if not force and up_to_date(lib):
         return lib
     nvcc = _nvcc()

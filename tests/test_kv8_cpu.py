@@ -204,6 +204,46 @@ def test_overlapping_cache_rows_are_refused():
         fdllm.Kv8Cache(k[:1].expand(1, -1, -1, -1), k[:1], s[:1], s[:1], wide[:8].view(1, 8))
 
 
+def test_the_library_is_built_without_its_python_binding(tmp_path, monkeypatch):
+    """A box whose torch headers or g++ do not fit still gets libfdllm.so; the
+    operators then say why they are missing.  A binding of another torch is
+    built anew, and not left in place when that fails."""
+    made = []
+    monkeypatch.setattr(build, "LIB", str(tmp_path / "libfdllm.so"))
+    monkeypatch.setattr(build, "BINDING", str(tmp_path / "_binding.so"))
+    monkeypatch.setattr(build, "BINDING_STAMP", str(tmp_path / "stamp"))
+    monkeypatch.setattr(build, "build_library", lambda lib, *a: made.append(lib) or lib)
+    run = subprocess.run
+
+    def no_gxx(cmd, *a, **kw):
+        if cmd[0] == "g++":
+            return subprocess.CompletedProcess(cmd, 1, b"no headers", b"")
+        return run(cmd, *a, **kw)
+
+    monkeypatch.setattr(build.subprocess, "run", no_gxx)
+    (tmp_path / "_binding.so").write_bytes(b"of another torch")
+    with pytest.warns(RuntimeWarning, match="no headers"):
+        assert build.build() == build.LIB
+    assert made == [build.LIB] and not os.path.exists(build.BINDING)
+    with pytest.raises(RuntimeError, match="no headers"):
+        build.build_binding()
+    # built, then found up to date; another torch's stamp: built again
+    calls = []
+
+    def gxx(cmd, *a, **kw):
+        calls.append(cmd)
+        open(cmd[cmd.index("-o") + 1], "wb").close()
+        return subprocess.CompletedProcess(cmd, 0, b"", b"")
+
+    monkeypatch.setattr(build.subprocess, "run", gxx)
+    build.build_binding()
+    build.build_binding()
+    assert len(calls) == 1 and os.path.exists(build.BINDING)
+    monkeypatch.setattr(torch, "__version__", "0.0")
+    build.build_binding()
+    assert len(calls) == 2
+
+
 # ------------------------------------------------ the plain implementations
 def test_plain_append_keeps_values_within_half_a_step():
     g = torch.Generator().manual_seed(1)
