@@ -120,6 +120,29 @@ def test_attention_where_contexts_may_be_long(dtype, hq, hkv, hd, rows, lens):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("hq,hkv,hd,most", [(8, 2, 64, 1), (28, 4, 128, 1), (28, 4, 128, 17), (8, 2, 64, 33)])
+@pytest.mark.parametrize("n", [33, 64, 100])
+def test_attention_many_sequences(dtype, n, hq, hkv, hd, most):
+    """More sequences than a warp scans at once, idle slots among them, split runs
+    in the first, the 33rd and later ones."""
+    g = torch.Generator().manual_seed(n + most)
+    lens = [int(x) for x in torch.randint(0, 300, (n,), generator=g)]
+    rows = [int(x) for x in torch.randint(0, most + 1, (n,), generator=g)]
+    for i, x in ((0, 1900), (32, 2500), (n - 1, 3000), (n // 2, 0)):
+        lens[i], rows[i] = x, most
+    starts = _starts(rows)
+    cache = kv8_ref.make_cache(g, lens, hkv, hd)
+    q = torch.randn(sum(rows) + 2, hq, hd, generator=g).to(TYPES[dtype])
+    _, c = _gpu(cache)
+    for kw in ({}, dict(max_q=most, max_len=3000)):
+        out = torch.full(q.shape, 7.0, dtype=q.dtype, device="cuda")
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        fdllm.fdllm_kv8_attention(c, q.cuda(), _i32(starts), _i32(lens), out=out, status=status, **kw)
+        assert status.item() == 0
+        _check_attention(cache, q, starts, lens, hd ** -0.5, out, sentinel=7.0)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 def test_attention_strided_rows_and_starts_offset(dtype):
     """q is a slice of a fused projection, out a slice of a wider buffer, the
     first sequence does not start at row 0."""
@@ -402,6 +425,36 @@ def test_append(dtype, hq, hkv, hd, rows, lens, pos):
         pos=_i32(pos) if pos else None, rope=rope.cuda(), q=G[:, :hq], max_new=max(rows),
         stored=True, lens_out=lens_out, status=status)
     _check_append(cache_ref, d, got, ref, status, lens_out)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("hq,hkv,hd,rows,lens", [
+    (36, 12, 128, [2400], [77]),      # a CTA's heads are of K, of V and of q
+    (32, 32, 128, [1700], [5]),
+    (40, 20, 64, [2600], [0]),
+    (28, 4, 128, [500, 3, 0, 250, 100, 16, 499, 1], [3, 61, 40, 0, 1000, 64, 7, 15]),
+])
+def test_append_with_several_heads_a_warp(dtype, hq, hkv, hd, rows, lens):
+    """Calls large enough for four heads a warp, each but the first loaded while
+    the one before is worked on (float32 rows of 128 dims are not)."""
+    blocks = (max(rows) + 30) // 16
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    assert -(-(2 * hkv + hq) // 8) * blocks * len(rows) > 8 * sms
+    g = torch.Generator().manual_seed(sum(rows) + hkv)
+    T, starts, ends = sum(rows), _starts(rows), [a + b for a, b in zip(lens, rows)]
+    cache = kv8_ref.make_cache(g, ends, hkv, hd)
+    qkv = (torch.randn(T, hq + 2 * hkv, hd, generator=g) * torch.exp(torch.randn(T, 1, 1, generator=g))).to(TYPES[dtype])
+    q, k, v = qkv[:, :hq], qkv[:, hq:hq + hkv], qkv[:, hq + hkv:]
+    rope = _rope(max(ends), hd)
+    ref_c = {n: t.clone() for n, t in cache.items()}
+    ref = kv8_ref.append(ref_c, k, v, starts, lens, None, rope, q)
+    d, c = _gpu(cache)
+    G = qkv.cuda()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    lens_out = torch.zeros(len(lens), dtype=torch.int32, device="cuda")
+    got = fdllm.fdllm_kv8_append(c, G[:, hq:hq + hkv], G[:, hq + hkv:], _i32(starts), _i32(lens), rope=rope.cuda(),
+                                 q=G[:, :hq], max_new=max(rows), stored=True, lens_out=lens_out, status=status)
+    _check_append(ref_c, d, got, ref, status, lens_out)
 
 
 def test_append_without_rotation_hint_outputs_or_q():
