@@ -530,11 +530,12 @@ FDLLM_API int fdllm_kv8_attention_workspace(const fdllm_kv8* cache,
  * new token, of a diffusion block over its prefix, itself and the suffix, or
  * of a ragged batch of either.  The products run on fp16 tensor-core
  * operands (codes are exact there) with float32 accumulation and float32
- * softmax statistics; float32 q and softmax weights are carried as two fp16
- * terms.  Rows of a sequence without keys give 0; rows behind
- * starts[n_seqs] are left as they are.  Keys on a bad page are left out
- * (BAD_PAGE).  A workspace smaller than asked is an error.  Errors: ARG,
- * CUDA. */
+ * softmax statistics.  With 16-bit q a softmax weight (times its key's value
+ * scale) is one fp16 term, off by up to 2^-11 of itself; float32 q and
+ * weights are carried as two fp16 terms.  Rows of a sequence without keys
+ * give 0; rows behind starts[n_seqs] are left as they are.  Keys on a bad
+ * page are left out (BAD_PAGE).  A workspace smaller than asked is an error.
+ * Errors: ARG, CUDA. */
 FDLLM_API int fdllm_kv8_attention(const fdllm_kv8* cache, const fdllm_kv8_attention_args* args,
                                   void* cuda_stream);
 

@@ -1,23 +1,23 @@
 // fdllm_kv8_attention, and its kernel for up to 64 query rows a K/V head, 16 a
-// run (and for more rows of short work, see plan): attention over the 8-bit paged K/V cache
-// on mma.sync.
+// run (and for more rows of short work, see plan): attention over the 8-bit paged
+// K/V cache on mma.sync.
 //
 // With few rows the kernel streams the cache, and operands that go straight
 // to registers spare the round trip through shared memory and TMEM that a
-// converted tile would take (kv8_attn_tc.cu takes it for more rows).
-//
-// Bound: 64 sequences' tokens over up to 8192 keys (4 K/V heads of 128 dims, 281
-// MB) take 70 us, 4.0 TB/s: 8 warps an SM with 2 stages in flight each wait for
-// instructions of their own chain (933 a tile of 32 keys) as much as for memory;
-// more warps do not fit the accumulators' registers (234 a thread).  A lone token
-// over 512 keys takes 9.1 us, a chain of latencies: the lengths (1.2), page ids
-// (0.8), q (0.8), the tile (1.3), the warps' exchange (0.8), the join's launch.
-//  A CTA's
+// converted tile would take (kv8_attn_tc.cu takes it for more rows).  A CTA's
 // 4 warps take its part of a run in tiles of 32 keys, every warp with a ring
 // of cp.async stages, softmax statistics and an output accumulator of its
 // own, so the loop has no barrier beyond the warp's; the warps' results meet
 // in shared memory.  Two CTAs an SM: one's start and end hide behind the
 // other's loop.
+//
+// Bound: 64 sequences' tokens over up to 8192 keys (4 K/V heads of 128 dims, 281
+// MB) take 68 us, 4.2 TB/s: 8 warps an SM with 2 stages in flight each wait for
+// instructions of their own chain (933 a tile of 32 keys) as much as for memory;
+// more warps do not fit the accumulators' registers (234 a thread), half of
+// which are idle rows when a K/V head has 8 query rows or fewer.  A lone token
+// over 512 keys takes 8.9 us, a chain of latencies: the lengths (1.2), page ids
+// (0.8), q (0.8), the tile (1.3), the warps' exchange (0.8), the join's launch.
 //
 // Codes are exact in fp16 and become matrix operands on the way from shared
 // memory to registers.  Both contractions are free in the order of their
@@ -462,7 +462,8 @@ struct Plan {
 // more slowly; a share of w pages (run starts counted in) takes about 12 + w
 // us above and 20 + 1.5 w us there.  Measured here / there: 112 rows, 4 K/V heads,
 // 2048 keys 16 / 22 us; 224 rows, 1024 keys 16 / 24 us, and 131072 keys, where
-// the kernel above would read every page 14 times, 119 us there.
+// the kernel above would read every page 14 times, 122 us there.  Tiles of 32
+// and 64 rows there took 53 us for 16 blocks of 32, which is 54 above.
 Plan plan(const fdllm_kv8& c, const fdllm_kv8_attention_args& a, int num_sms) {
   // rows of a sequence; without a hint those of an even batch, not all of them
   const int64_t most_q = a.max_q > 0 ? std::min(a.max_q, a.n_tokens)

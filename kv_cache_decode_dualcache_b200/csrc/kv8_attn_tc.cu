@@ -19,10 +19,10 @@
 // need L1 lines, spills go to L2); hence the bulk copies, and 64-key tiles,
 // whose scores fit a thread's registers.
 //
-// Bound: 224 rows (32 tokens, 28 heads on 4) over 131072 keys take 119 us, 505
+// Bound: 224 rows (32 tokens, 28 heads on 4) over 131072 keys take 122 us, 493
 // TF/s: 1.4 us for a tile's 64 keys, of which its products are 0.73 at the rate of
-// a large library product; the rest is the softmax's chain (scores out of TMEM,
-// weights back, barriers).
+// a large library product (the tensor pipe is active for 33% of the cycles); the
+// rest is the softmax's chain (scores out of TMEM, weights back, barriers).
 //
 // Orderings.  Who waits for whom (n: the CTA's running tile, a barrier's phase
 // is the n-th use of its slot, and none can be two phases ahead of a waiter):

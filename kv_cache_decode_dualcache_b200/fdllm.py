@@ -518,7 +518,8 @@ def fdllm_kv8_append(cache: Kv8Cache, k, v, starts, lens, pos=None, rope=None, q
     by rope [positions, head_dim / 2, 2] (cos, sin), and rotate q [tokens,
     heads, head_dim] (see the header).  Returns (q_out, k_out, v_out): the
     rotated q (None without q) and, with stored, the rows as the cache now
-    stands for them (else None, None)."""
+    stands for them (else None, None).  Their rows that belong to no sequence, or
+    that could not be stored, are not written."""
     r = (_ops or _load_ops()).append(cache.address, cache.device, k, v, starts, lens, pos, rope, q,
                                      max_new, stored, lens_out, status, stream)
     if type(r) is int:
@@ -531,6 +532,7 @@ def fdllm_kv8_attention(cache: Kv8Cache, q, starts, lens, scale: Optional[float]
                         stream=None):
     """softmax(scale q K^T) V of every row of q [tokens, heads, head_dim] over
     its sequence's cached keys [0, lens[i]); scale None = 1 / sqrt(head_dim).
+    Rows that belong to no sequence are not written; out may not be q.
     workspace: a uint8 tensor to use instead of a fresh one (its size:
     fdllm_kv8_attention_workspace)."""
     r = (_ops or _load_ops()).attention(cache.address, cache.device, q, starts, lens, scale, out, max_q,
