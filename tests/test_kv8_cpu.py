@@ -205,7 +205,7 @@ def test_overlapping_cache_rows_are_refused():
 
 
 def test_the_library_is_built_without_its_python_binding(tmp_path, monkeypatch):
-    """A box whose torch headers or g++ do not fit still gets libfdllm.so; the
+    """A machine whose torch headers or g++ do not fit still gets libfdllm.so; the
     operators then say why they are missing.  A binding of another torch is
     built anew, and not left in place when that fails."""
     made = []
